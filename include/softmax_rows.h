@@ -228,6 +228,159 @@ int attention_forward(const void* q, const void* k, const void* v, void* o, floa
                       int64_t Sk, int64_t d, float scale, int causal, int dtype, void* stream);
 
 /*
+ * The decoding step: a paged key/value cache held in 4 bits, the attention that reads it, and what is
+ * done to the logits before their softmax.  (The pages stop at the attention of a prompt, "Softmax
+ * 数值稳定性与 IO-Aware Attention" §八; a step with one token a sequence keeps its keys and values from
+ * call to call, and the same online (m, l, o) recurrence runs over them.)
+ *
+ * The cache is one array of bytes, [num_pages][heads][page_size / 16][20 * head_dim]: a block holds
+ * 16 tokens of one key/value head.  Each group of 32 elements of a key or value has a scale s and a
+ * zero z (fp16), an element is s * c + z with a code c of 0 .. 15; 5 bits an element in all.  With
+ * d = head_dim and G = d / 32, a block is
+ *   [0, 8 d)      key codes: 32-bit word r (d / 8) + G t + j (token r < 16, t < 4, j < G) holds
+ *                 elements 32 j + 8 t + n of token r in nibble n (bits 4 n .. 4 n + 3), n < 8;
+ *   [8 d, 16 d)   value codes: 16-bit word 2 (((8 f + g) 4 + t) G + j) + e (f < 2, g < 8, t < 4, e < 2)
+ *                 holds elements 32 j + 4 g + n of token 8 f + 2 t + e in nibble n, n < 4;
+ *   16 d          fp16 key scales [16][G], then key zeros [16][G];
+ *   16 d + 64 G   fp16 value scales [8][G][2] (token pair, group, token of the pair), then value zeros.
+ * Pages belong to the caller, who gives each sequence its pages through the page table; pages may be
+ * shared by sequences that only read them.
+ *
+ * A call handles `tokens` rows: sequence b owns rows cu_tokens[b] .. cu_tokens[b + 1] - 1, its last
+ * n_b tokens in the cache, so row i is the token at position seq_lens[b] - (cu_tokens[b + 1] - i).
+ * cu_tokens = NULL means one token for each sequence (tokens == batch).  Rows from cu_tokens[batch] on
+ * belong to no sequence and are left as they were.
+ *
+ * Values on the device cannot be checked before the launch.  A page, length, position or offset out
+ * of its range is never followed: it is recorded (softmax_get_status returns
+ * SOFTMAX_ERR_INVALID_ARG), a row of kv4_append or kv4_gather concerned is skipped, and the sequence's
+ * rows of attention_kv4 are undefined.
+ */
+typedef struct kv4_cache {
+  void* data;                /* 16-byte aligned */
+  const int32_t* page_table; /* [batch][table_width]: page of tokens p * page_size .. of each sequence */
+  const int32_t* seq_lens;   /* [batch]: tokens of each sequence, those of this call included */
+  const int32_t* cu_tokens;  /* [batch + 1], ascending, or NULL */
+  int64_t num_pages;
+  int64_t page_size;         /* a multiple of 16 */
+  int64_t heads;             /* key/value heads */
+  int64_t head_dim;          /* 64 or 128 */
+  int64_t batch;
+  int64_t table_width;
+  int64_t tokens;
+} kv4_cache;
+
+/* Rows [tokens][heads][head_dim] of bf16 or fp16 elements: strides in elements, multiples of 8; data
+   16-byte aligned; the elements of a head lie side by side. */
+typedef struct kv4_rows {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} kv4_rows;
+
+enum kv4_flags { KV4_FLAG_NEIGHBOURS = 1 /* rotate pairs (2 i, 2 i + 1) instead of (i, i + rotated / 2) */ };
+
+/*
+ * kv4_append -- writes this call's keys and values into the cache, keys (and queries) rotated by
+ * their positions on the way.
+ *   k, v      -- [tokens][heads][head_dim].
+ *   q, q_out  -- [tokens][q_heads][head_dim], both or neither: q_out = q rotated (q_out may be q).
+ *   cos_sin   -- fp32 [positions][rotated], 16-byte aligned: rotated / 2 cosines, then as many sines of
+ *                each position; (a, b) becomes (a cos - b sin, b cos + a sin).  NULL: no rotation.
+ *   rotated   -- leading elements of a head that are rotated, a multiple of 8 up to head_dim.
+ * Quantisation of a group x of 32 (fp32 arithmetic, every operation rounded by itself, so a host can
+ * reproduce the bytes): x limited to +-65504, z = fp16(min x), s = fp16((max x - min x) / 15),
+ * c = (x - z) / s rounded to the nearest integer (ties to even) and limited to 0 .. 15, 0 where s = 0.
+ * Non-finite inputs give unspecified values in their own group only.
+ * Every token needs a place of its own: two tokens of one call that fall on one place of one page
+ * leave it with bytes of either.  head_dim other than 64 and 128, fp32 and sizes beyond 2^31 rows
+ * or positions return SOFTMAX_ERR_UNSUPPORTED.
+ */
+int kv4_append(const kv4_cache* cache, const kv4_rows* k, const kv4_rows* v, const kv4_rows* q, const kv4_rows* q_out, int64_t q_heads,
+               const float* cos_sin, int64_t positions, int64_t rotated, int flags, int dtype, void* stream);
+
+/*
+ * kv4_gather -- the values s * c + z of this call's tokens (whole sequences where n_b = seq_lens[b]),
+ * rounded once to the element type: what attention_forward takes for a prompt whose prefix is in the cache.
+ * k and v: [tokens][heads][head_dim], written.
+ */
+int kv4_gather(const kv4_cache* cache, const kv4_rows* k, const kv4_rows* v, int dtype, void* stream);
+
+/*
+ * attention_kv4 -- O = softmax(scale Q K^T) V of this call's tokens over the cache, query head h with
+ * key/value head h / (q_heads / heads).  Row i at position p sees the keys at positions 0 .. p, so the
+ * call's own tokens must be in the cache (kv4_append) first.
+ *   q         -- [tokens][q_heads][head_dim], bf16 or fp16; finite.
+ *   o         -- [tokens][q_heads][head_dim], contiguous, written.
+ *   lse_out   -- fp32 [tokens][q_heads]: m + ln l of each row (natural log, of scale Q K^T), or NULL.
+ *   q_heads   -- a multiple of heads.
+ *   scale     -- finite, > 0; 0 means 1/sqrt(head_dim).
+ *   workspace -- device memory of at least attention_kv4_workspace(...) bytes, 256-byte aligned, that
+ *                no other call uses until this one is done (calls that may run at the same time, captured
+ *                graphs among them, need one each).  Nothing in it is kept from call to call.
+ * Built for a few tokens a sequence (decoding, drafts): any number is right, but a long prompt runs
+ * faster through attention_forward on 16-bit keys and values.  Scores and row states are fp32; weights are
+ * rounded to fp16 for the product with V.  A row that sees no key gets o = 0, LSE = -inf.
+ */
+int attention_kv4(const kv4_cache* cache, const kv4_rows* q, void* o, float* lse_out, int64_t q_heads, float scale, int dtype,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for attention_kv4 on the current device; -1 for sizes that it refuses. */
+int64_t attention_kv4_workspace(int64_t batch, int64_t tokens, int64_t q_heads, int64_t heads, int64_t head_dim);
+
+/*
+ * logits_process_rows -- penalties for repeated tokens, biases and a mask on M rows of N logits, with
+ * the softmax or log softmax that follows in the same pass.  For token j of a row, c its count among
+ * the row's generated tokens, "seen" if it is among its prompt or generated tokens:
+ *     l = x_j
+ *     l = l > 0 ? l / repetition : l * repetition      where j is seen
+ *     l = l - (frequency * c + presence)               where c > 0
+ *     l = l + (biases of j, added up in list order)
+ *     l = l * scale
+ *     l = -inf                                         where j's mask bit is 0
+ * y = l, softmax(l) or log softmax(l).  A row whose entries are all -inf gives softmax 0, log softmax
+ * -inf, LSE -inf.
+ *   x, y        -- rows at pitches ldx, ldy in elements (0: N); y may be x (with ldx == ldy).
+ *   lse_out     -- fp32 [M]: LSE of l, or NULL.
+ *   tokens      -- int32 [M][token_width]: a row's prompt, then its generated tokens; negative entries
+ *                  count as absent.  NULL: no penalties.  token_width < 2^20.
+ *   prompt_lens -- int32 [M]: how many of them are the prompt (NULL: 0).
+ *   token_lens  -- int32 [M]: how many there are, prompt included.
+ *   repetition, frequency, presence, scale -- fp32 [M] each, or NULL for 1, 0, 0, 1; repetition and
+ *                  scale > 0.
+ *   bias_ids, bias_values -- int32 and fp32 [M][bias_count], negative ids count as absent; at most 1024.
+ *   mask        -- 32-bit words [M][ld_mask] (0: ceil(N / 32)), bit j % 32 of word j / 32 is set where j is
+ *                  allowed; NULL: all.
+ * A token or bias id >= N is ignored, and softmax_get_status returns SOFTMAX_ERR_INVALID_ARG, as it does
+ * for lengths outside 0 <= prompt <= all <= token_width (which are limited to that range).
+ * Arithmetic is fp32; the results do not depend on the order in which the GPU counts.
+ */
+typedef struct logits_rows {
+  const void* x;
+  int64_t ldx;
+  void* y;
+  int64_t ldy;
+  float* lse_out;
+  const int32_t* tokens;
+  int64_t token_width;
+  const int32_t* prompt_lens;
+  const int32_t* token_lens;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_ids;
+  const float* bias_values;
+  int64_t bias_count;
+  const uint32_t* mask;
+  int64_t ld_mask;
+  const float* scale;
+} logits_rows;
+
+enum logits_out { LOGITS_OUT_LOGITS = 0, LOGITS_OUT_SOFTMAX = 1, LOGITS_OUT_LOG_SOFTMAX = 2 };
+
+int logits_process_rows(const logits_rows* a, int64_t M, int64_t N, int dtype, int out, void* stream);
+
+/*
  * softmax_row_state -- only the per-row state (m, d) and LSE: the first pass
  * of the online method ("5.2 CUDA Online Softmax 实现优化", §2.2, pass 1;
  * "Softmax 数值稳定性与 IO-Aware Attention" §四, the mergeable state).  Reads x
@@ -297,7 +450,8 @@ int softmax_rows_splitrow_noalloc(const void* x, void* y, float* m_out, float* d
  * status word of the current device: SOFTMAX_OK, or the error a kernel
  * recorded since the last call (SOFTMAX_ERR_TIMEOUT for a bounded wait that
  * ran out, which takes precedence; SOFTMAX_ERR_INVALID_ARG for a cross-entropy
- * label >= N).  SOFTMAX_ERR_CUDA if the synchronisation itself failed.
+ * label >= N, or a page, token, length or position that a call of the decoding
+ * step found out of range).  SOFTMAX_ERR_CUDA if the synchronisation itself failed.
  */
 int softmax_get_status(void* stream);
 

@@ -20,7 +20,8 @@ __all__ = [
     "VARIANT_SPLITROW", "VARIANT_SPLITROW_STREAM", "VARIANT_NAMES", "SoftmaxError", "softmax_rows", "softmax_rows_ex",
     "softmax_row_state", "merge_states", "softmax_rows_host", "get_status", "status_string",
     "last_variant", "debug_set_fault", "debug_set_wait_limit_ns", "capi", "library_path",
-    "softmax_rows_splitrow_noalloc", "softmax_rows_causal",
+    "softmax_rows_splitrow_noalloc", "softmax_rows_causal", "kv4_cache_empty", "kv4_append", "kv4_gather",
+    "attention_kv4", "attention_kv4_workspace", "logits_process_rows",
 ]
 
 F32, BF16, F16 = 0, 1, 2
@@ -41,6 +42,7 @@ EXPORTED = (
     "softmax_get_status", "softmax_status_string", "softmax_last_cuda_error", "softmax_last_variant",
     "softmax_debug_set_fault", "softmax_debug_set_wait_limit_ns", "softmax_rows_splitrow_noalloc",
     "softmax_rows_causal", "log_softmax_rows", "cross_entropy_rows", "softmax_rows_strided", "attention_forward",
+    "kv4_append", "kv4_gather", "attention_kv4", "attention_kv4_workspace", "logits_process_rows",
 )
 
 
@@ -92,6 +94,7 @@ def capi() -> ctypes.CDLL:
                      "softmax_debug_set_fault", "softmax_rows_splitrow_noalloc", "softmax_rows_causal",
                      "log_softmax_rows", "cross_entropy_rows", "softmax_rows_strided", "attention_forward"):
             getattr(lib, name).restype = ci
+        decode._declare(lib)
         _lib = lib
     return _lib
 
@@ -375,3 +378,8 @@ def debug_set_fault(fault: int) -> int:
 
 def debug_set_wait_limit_ns(ns: int) -> int:
     return int(capi().softmax_debug_set_wait_limit_ns(int(ns)))
+
+
+from . import decode  # noqa: E402  (uses the helpers above)
+from .decode import (attention_kv4, attention_kv4_workspace, kv4_append, kv4_cache_empty, kv4_gather,  # noqa: E402
+                     logits_process_rows)

@@ -630,7 +630,7 @@ int softmax_get_status(void* stream) {
   if (err == cudaSuccess) err = cudaStreamSynchronize(s);
   if (err != cudaSuccess) return cuda_fail(err);
   if (word & kStatusTimeout) return SOFTMAX_ERR_TIMEOUT;
-  if (word & kStatusBadLabel) return SOFTMAX_ERR_INVALID_ARG;
+  if (word & (kStatusBadLabel | kStatusBadIndex)) return SOFTMAX_ERR_INVALID_ARG;
   return SOFTMAX_OK;
 }
 

@@ -40,6 +40,7 @@ struct RowProblem {
 // Status bits a kernel may set in the per-device status word.
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusBadLabel = 2u;  // a cross-entropy label >= N
+constexpr unsigned kStatusBadIndex = 4u;  // a page, token, position or length outside its range
 
 inline int elem_bytes(int dtype) { return dtype == 0 ? 4 : 2; }
 

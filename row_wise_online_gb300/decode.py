@@ -1,0 +1,274 @@
+"""The decoding step: a paged key/value cache held in 4 bits (``kv4_append``, ``kv4_gather``,
+``attention_kv4``) and the processing of logits before their softmax (``logits_process_rows``).
+
+As the rest of the package, this module only marshals arguments; the calls and the layout of the cache are
+described in ``include/softmax_rows.h``.  Every tensor of a call is on one CUDA device, which need not be the
+current one; the work is enqueued on ``stream`` or on that device's current stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import row_wise_online_gb300 as _rwo
+
+KV4_FLAG_NEIGHBOURS = 1
+LOGITS_OUT = {"logits": 0, "softmax": 1, "log_softmax": 2}
+
+_vp, _i64 = ctypes.c_void_p, ctypes.c_int64
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("data", _vp), ("page_table", _vp), ("seq_lens", _vp), ("cu_tokens", _vp)] + [
+        (n, _i64) for n in ("num_pages", "page_size", "heads", "head_dim", "batch", "table_width", "tokens")]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64)]
+
+
+class _Logits(ctypes.Structure):
+    _fields_ = [("x", _vp), ("ldx", _i64), ("y", _vp), ("ldy", _i64), ("lse_out", _vp), ("tokens", _vp),
+                ("token_width", _i64), ("prompt_lens", _vp), ("token_lens", _vp), ("repetition", _vp),
+                ("frequency", _vp), ("presence", _vp), ("bias_ids", _vp), ("bias_values", _vp), ("bias_count", _i64),
+                ("mask", _vp), ("ld_mask", _i64), ("scale", _vp)]
+
+
+def _declare(lib) -> None:
+    """Argument types of the calls of this module."""
+    rows, ci = ctypes.POINTER(_Rows), ctypes.c_int
+    cache = ctypes.POINTER(_Cache)
+    lib.kv4_append.argtypes = [cache, rows, rows, rows, rows, _i64, _vp, _i64, _i64, ci, ci, _vp]
+    lib.kv4_gather.argtypes = [cache, rows, rows, ci, _vp]
+    lib.attention_kv4.argtypes = [cache, rows, _vp, _vp, _i64, ctypes.c_float, ci, _vp, _i64, _vp]
+    lib.attention_kv4_workspace.argtypes = [_i64] * 5
+    lib.attention_kv4_workspace.restype = _i64
+    lib.logits_process_rows.argtypes = [ctypes.POINTER(_Logits), _i64, _i64, ci, ci, _vp]
+    for name in ("kv4_append", "kv4_gather", "attention_kv4", "logits_process_rows"):
+        getattr(lib, name).restype = ci
+
+
+def _tensor(t, name, dtype, shape, device):
+    """Data pointer of a contiguous tensor of a dtype and shape on the call's device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The device made current, and the stream as a pointer; torch allocations inside belong to that stream."""
+    import torch
+
+    with torch.cuda.device(device):
+        if stream is None:
+            s = torch.cuda.current_stream(device)
+        elif hasattr(stream, "cuda_stream"):
+            s = stream
+        else:
+            s = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(s):
+            yield ctypes.c_void_p(int(s.cuda_stream))
+
+
+def _rows(t, name, heads, tokens, dim, dtype, device):
+    """[tokens, heads, dim] with the elements of a head side by side."""
+    if t.dim() != 3 or tuple(t.shape) != (tokens, heads, dim) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(tokens, heads, dim)} on {device}")
+    if t.stride(2) != 1 and t.numel():
+        raise ValueError(f"{name}: the elements of a head must be contiguous (stride(2) == 1)")
+    return _Rows(t.data_ptr(), t.stride(0) if tokens > 1 else heads * dim, t.stride(1) if heads > 1 else dim)
+
+
+def _paged(cache, page_table, seq_lens, cu_tokens, tokens):
+    """The cache argument: shapes and types checked, pointers taken."""
+    import torch
+
+    if not cache.is_cuda or cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] % 20:
+        raise ValueError("cache must be a contiguous CUDA uint8 tensor [pages, heads, page_size / 16, 20 * head_dim] (kv4_cache_empty)")
+    pages, heads, blocks, held = (int(s) for s in cache.shape)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be a 2-D int32 tensor [batch, pages a sequence has room for]")
+    batch, width = (int(s) for s in page_table.shape)
+    if cu_tokens is None and tokens != batch:
+        raise ValueError(f"{tokens} rows for {batch} sequences: cu_tokens is needed where they are not one each")
+    dev = cache.device
+    return _Cache(cache.data_ptr(), _tensor(page_table, "page_table", torch.int32, (batch, width), dev),
+                  _tensor(seq_lens, "seq_lens", torch.int32, (batch,), dev),
+                  _tensor(cu_tokens, "cu_tokens", torch.int32, (batch + 1,), dev),
+                  pages, blocks * 16, heads, held // 20, batch, width, tokens)
+
+
+def kv4_cache_empty(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, device=None):
+    """A zeroed cache [num_pages, num_kv_heads, page_size / 16, 20 * head_dim] of bytes: page_size a multiple of
+    16, head_dim 64 or 128.  Room for num_pages * page_size tokens, 1.25 * head_dim bytes a token and head."""
+    import torch
+
+    if page_size < 16 or page_size % 16:
+        raise ValueError("page_size must be a multiple of 16")
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim must be 64 or 128")
+    return torch.zeros((num_pages, num_kv_heads, page_size // 16, 20 * head_dim), dtype=torch.uint8, device=device or "cuda")
+
+
+def kv4_append(k, v, cache, page_table, seq_lens, cu_tokens=None, q=None, q_out=None, cos_sin=None, interleaved: bool = False,
+               stream=None):
+    """Write new keys and values [T, kv_heads, d] (bf16 or fp16) into the 4-bit cache, keys rotated by their positions.
+
+    page_table int32 [B, W] and seq_lens int32 [B] say where a sequence lies and how long it is with the new
+    tokens; cu_tokens int32 [B + 1] where its rows are (None: one each).  cos_sin fp32 [positions, rotated]
+    holds cosines, then sines; pairs are (i, i + rotated / 2), or neighbours if ``interleaved``.  With q
+    [T, heads, d], also rotates q into q_out (default: a new tensor; q_out may be q) and returns it.
+    """
+    import torch
+
+    if k.dim() != 3:
+        raise ValueError("k must be a 3-D tensor [tokens, kv_heads, head_dim]")
+    T = int(k.shape[0])
+    c = _paged(cache, page_table, seq_lens, cu_tokens, T)
+    dt, dev = _rwo._dtype_code(k), cache.device
+    kr, vr = (_rows(t, n, c.heads, T, c.head_dim, k.dtype, dev) for t, n in ((k, "k"), (v, "v")))
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    positions = rotated = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be a 2-D float32 tensor [positions, rotated]")
+        positions, rotated = (int(s) for s in cos_sin.shape)
+    table = _tensor(cos_sin, "cos_sin", torch.float32, (positions, rotated), dev)
+    qr = qo = None
+    heads = 0
+    with _on(dev, stream) as s:
+        if q is not None:
+            heads = int(q.shape[1]) if q.dim() == 3 else 0
+            qr = _rows(q, "q", heads, T, c.head_dim, k.dtype, dev)
+            if q_out is None:
+                q_out = torch.empty((T, heads, c.head_dim), dtype=q.dtype, device=dev)
+            qo = _rows(q_out, "q_out", heads, T, c.head_dim, k.dtype, dev)
+        st = _rwo.capi().kv4_append(c, kr, vr, qr, qo, heads, table, positions, rotated, KV4_FLAG_NEIGHBOURS if interleaved else 0, dt, s)
+    _rwo._check(st, "kv4_append")
+    return q_out
+
+
+def kv4_gather(cache, page_table, seq_lens, cu_tokens=None, num_tokens: int | None = None, k=None, v=None, dtype=None, stream=None):
+    """The last cu_tokens[b + 1] - cu_tokens[b] tokens of each sequence (None: one) read back as bf16 or fp16.
+
+    Returns (k, v), [num_tokens, kv_heads, d] in ``dtype`` (default bf16) unless given; num_tokens defaults to
+    the given k's rows, or to one a sequence.  Rows that belong to no sequence are left as they were.
+    """
+    import torch
+
+    if num_tokens is None:
+        if k is None and cu_tokens is not None:
+            raise ValueError("num_tokens (cu_tokens' last entry) is needed to allocate k and v")
+        num_tokens = int(k.shape[0]) if k is not None else int(page_table.shape[0])
+    c = _paged(cache, page_table, seq_lens, cu_tokens, int(num_tokens))
+    dev = cache.device
+    dtype = dtype or (k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16)
+    shape = (int(num_tokens), c.heads, c.head_dim)
+    with _on(dev, stream) as s:
+        k = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
+        v = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
+        kr, vr = (_rows(t, n, c.heads, shape[0], c.head_dim, dtype, dev) for t, n in ((k, "k"), (v, "v")))
+        st = _rwo.capi().kv4_gather(c, kr, vr, _rwo._dtype_code(k), s)
+    _rwo._check(st, "kv4_gather")
+    return k, v
+
+
+def attention_kv4_workspace(batch: int, tokens: int, num_heads: int, num_kv_heads: int, head_dim: int, device=None):
+    """A workspace tensor for attention_kv4 calls of these sizes.  Calls that may run at the same time need one each."""
+    import torch
+
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(device):
+        n = int(_rwo.capi().attention_kv4_workspace(batch, tokens, num_heads, num_kv_heads, head_dim))
+        if n < 0:
+            raise _rwo.SoftmaxError(_rwo.ERR_UNSUPPORTED, "attention_kv4_workspace")
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def attention_kv4(q, cache, page_table, seq_lens, cu_tokens=None, o=None, lse_out=None, scale: float | None = None, workspace=None,
+                  stream=None):
+    """O = softmax(scale Q K^T) V of q [T, heads, d] (bf16 or fp16) over the 4-bit cache; row i of a sequence sees the
+    tokens up to its own position.  scale defaults to 1/sqrt(d).  Returns o (and fills lse_out [T, heads] fp32).
+
+    The workspace (attention_kv4_workspace) is allocated for the call unless given.
+    """
+    import torch
+
+    if q.dim() != 3:
+        raise ValueError("q must be a 3-D tensor [tokens, heads, head_dim]")
+    T, heads = int(q.shape[0]), int(q.shape[1])
+    c = _paged(cache, page_table, seq_lens, cu_tokens, T)
+    dt, dev = _rwo._dtype_code(q), cache.device
+    qr = _rows(q, "q", heads, T, c.head_dim, q.dtype, dev)
+    lse = _tensor(lse_out, "lse_out", torch.float32, (T, heads), dev)
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev):
+        raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
+    with _on(dev, stream) as s:
+        if o is None:
+            o = torch.empty((T, heads, c.head_dim), dtype=q.dtype, device=dev)
+        op = _tensor(o, "o", q.dtype, (T, heads, c.head_dim), dev)
+        if workspace is None:
+            n = int(_rwo.capi().attention_kv4_workspace(c.batch, T, heads, c.heads, c.head_dim))
+            workspace = torch.empty(max(n, 0), dtype=torch.uint8, device=dev)
+        st = _rwo.capi().attention_kv4(c, qr, op, lse, heads, 0.0 if scale is None else float(scale), dt, workspace.data_ptr(),
+                                       workspace.numel(), s)
+    _rwo._check(st, "attention_kv4")
+    return o
+
+
+def logits_process_rows(x, y=None, out: str = "softmax", lse_out=None, tokens=None, prompt_lens=None, token_lens=None,
+                        repetition=None, frequency=None, presence=None, bias_ids=None, bias_values=None, mask=None, scale=None,
+                        stream=None):
+    """Penalties for repeated tokens, biases, scale and mask on logits x [M, N] (rows may be pitched), then ``out``:
+    "logits", "softmax" or "log_softmax".
+
+    tokens int32 [M, L] (prompt, then generated; negative: absent) with prompt_lens and token_lens int32 [M];
+    repetition, frequency, presence, scale fp32 [M]; bias_ids int32 and bias_values fp32 [M, K]; mask int32
+    [M, words >= ceil(N / 32)], a set bit allows its token.  y defaults to a new contiguous tensor and may be x.
+    """
+    import torch
+
+    if out not in LOGITS_OUT:
+        raise ValueError(f"out must be one of {sorted(LOGITS_OUT)}")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    M, N, ldx = _rwo._rows_strided(x)
+    dt, dev = _rwo._dtype_code(x), x.device
+    a = _Logits(x=x.data_ptr(), ldx=ldx)
+    if tokens is not None:
+        if tokens.dim() != 2 or token_lens is None:
+            raise ValueError("tokens must be a 2-D int32 tensor [M, L], with token_lens")
+        a.token_width = int(tokens.shape[1])
+        a.tokens = _tensor(tokens, "tokens", torch.int32, (M, a.token_width), dev)
+        a.token_lens = _tensor(token_lens, "token_lens", torch.int32, (M,), dev)
+        a.prompt_lens = _tensor(prompt_lens, "prompt_lens", torch.int32, (M,), dev)
+    elif any(t is not None for t in (prompt_lens, token_lens, repetition, frequency, presence)):
+        raise ValueError("penalties need tokens")
+    for n, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence), ("scale", scale), ("lse_out", lse_out)):
+        setattr(a, n, _tensor(t, n, torch.float32, (M,), dev))
+    if (bias_ids is None) != (bias_values is None):
+        raise ValueError("bias_ids and bias_values go together")
+    if bias_ids is not None:
+        if bias_ids.dim() != 2:
+            raise ValueError("bias_ids must be a 2-D int32 tensor [M, K]")
+        a.bias_count = int(bias_ids.shape[1])
+        a.bias_ids = _tensor(bias_ids, "bias_ids", torch.int32, (M, a.bias_count), dev)
+        a.bias_values = _tensor(bias_values, "bias_values", torch.float32, (M, a.bias_count), dev)
+    if mask is not None:
+        a.ld_mask = int(mask.shape[1]) if mask.dim() == 2 else 0
+        if a.ld_mask < (N + 31) // 32:
+            raise ValueError("mask must be an int32 tensor [M, words] with a bit for each token")
+        a.mask = _tensor(mask, "mask", torch.int32, (M, a.ld_mask), dev)
+    with _on(dev, stream) as s:
+        if y is None:
+            y = torch.empty((M, N), dtype=x.dtype, device=dev)
+        if tuple(y.shape) != (M, N) or y.dtype != x.dtype or y.device != dev:
+            raise ValueError("y must have x's shape, dtype and device")
+        a.y, a.ldy = y.data_ptr(), _rwo._rows_strided(y)[2]
+        st = _rwo.capi().logits_process_rows(a, M, N, dt, LOGITS_OUT[out], s)
+    _rwo._check(st, "logits_process_rows")
+    return y
