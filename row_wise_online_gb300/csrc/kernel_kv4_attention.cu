@@ -24,6 +24,8 @@
 //   resident CTA: long and short sequences mix without imbalance.  A run that ends inside a (sequence, head) leaves its
 //   state (m, l, O) in the workspace; a second kernel merges such states in the order of the runs.
 // Every wait is bounded; a wait that runs out sets the status word.
+#include <atomic>
+
 #include "kv4.cuh"
 
 namespace rwo {
@@ -700,6 +702,24 @@ Plan plan_for(int64_t batch, int64_t tokens, int q_heads, int heads, int d, int 
 
 constexpr int kMaxCtasPerSm = 4;
 
+// CTAs of the main kernel that an SM holds: asked once per device and kernel (the answer is the kernel's own).
+cudaError_t resident_ctas(const Plan& p, bool d64, bool f16, const DeviceInfo& dev, int* out) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][8];
+  std::atomic<int>& slot = known[dev.device % kDevices][(d64 ? 4 : 0) + (f16 ? 2 : 0) + (p.rows == 16 ? 1 : 0)];
+  int n = slot.load(std::memory_order_acquire);
+  if (n == 0) {
+    cudaError_t err = cudaFuncSetAttribute((const void*)p.main, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+    if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, (const void*)p.main, kThreads, size_t(p.smem));
+    if (err != cudaSuccess) return err;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    if (n > kMaxCtasPerSm) n = kMaxCtasPerSm;
+    slot.store(n, std::memory_order_release);
+  }
+  *out = n;
+  return cudaSuccess;
+}
+
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
@@ -713,12 +733,9 @@ size_t attention_kv4_scratch(int64_t batch, int64_t tokens, int q_heads, int hea
 cudaError_t launch_attention_kv4(const Kv4View& c, const Kv4Rows& q, void* o, float* lse, int q_heads, float scale, int dtype,
                                  void* scratch, cudaStream_t stream, const DeviceInfo& dev) {
   const Plan p = plan_for(c.batch, c.tokens, q_heads, c.heads, c.d, dtype);
-  cudaError_t err = cudaFuncSetAttribute((const void*)p.main, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
   int per_sm = 0;
-  if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, (const void*)p.main, kThreads, size_t(p.smem));
+  cudaError_t err = resident_ctas(p, c.d == 64, dtype == 2, dev, &per_sm);
   if (err != cudaSuccess) return err;
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  if (per_sm > kMaxCtasPerSm) per_sm = kMaxCtasPerSm;
   AttnArgs a;
   a.c = c;
   a.q = q;

@@ -193,9 +193,323 @@ __global__ void __launch_bounds__(kCacheThreads) k_kv4_gather(GatherArgs a) {
   }
 }
 
+// ---- runs of tokens -------------------------------------------------------------------------------------------
+//
+// Where sequences bring many tokens (prompts, prefixes read back), a warp takes a block of 16 tokens of one head: the
+// lookups are made once for the block and whole words move.  The blocks that the call's tokens touch form one list over
+// the sequences, cut into equal parts, one a CTA; each CTA finds its part by a scan over the sequences.
+
+// The blocks of sequence b's new tokens: positions [len - n, len).  Tokens before the sequence's start have none.
+struct RunSeq {
+  Kv4Seq s;
+  int first, blocks;  // first block, how many
+};
+__device__ __forceinline__ RunSeq run_seq(const Kv4View& c, int b, bool& bad) {
+  RunSeq r;
+  r.s = kv4_seq(c, b, bad);
+  const int p0 = r.s.len - r.s.n;
+  if (p0 < 0) bad = true;
+  r.first = max(p0, 0) / kKv4Block;
+  r.blocks = r.s.n > 0 && r.s.len > 0 ? (r.s.len - 1) / kKv4Block - r.first + 1 : 0;
+  return r;
+}
+
+// Calls f(sequence, block of it, head or other sub-task) for the units of this warp: `subs` a block.
+template <class F>
+__device__ __forceinline__ void for_units(const Kv4View& c, int subs, F f) {
+  __shared__ int64_t scan[kCacheThreads / 32];
+  __shared__ int64_t where[2];  // sequence, first unit of it
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (c.batch + kCacheThreads - 1) / kCacheThreads, b0 = min(tid * per, c.batch), b1 = min(b0 + per, c.batch);
+  bool bad = false;
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += int64_t(run_seq(c, b, bad).blocks) * subs;
+  if (bad && blockIdx.x == 0) kv4_bad(c);
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(kFull, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  int64_t total = 0, before = upto - mine;
+  for (int w = 0; w < kCacheThreads / 32; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  const int64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (u0 >= u1) return;
+  if (u0 >= before && u0 < before + mine) {
+    int64_t at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t n = int64_t(run_seq(c, b, bad).blocks) * subs;
+      if (u0 < at + n) {
+        where[0] = b;
+        where[1] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  int b = int(where[0]);
+  int64_t at = where[1];
+  RunSeq r = run_seq(c, b, bad);
+  for (int64_t u = u0 + warp; u < u1; u += kCacheThreads / 32) {
+    while (u >= at + int64_t(r.blocks) * subs) {
+      at += int64_t(r.blocks) * subs;
+      r = run_seq(c, ++b, bad);
+    }
+    const int x = int((u - at) / subs);
+    f(b, r, r.first + x, int((u - at) - int64_t(x) * subs));
+  }
+}
+
+template <class D>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&f)[8]) {
+  D::unpack(*reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p) + at * 2), f);
+}
+template <class D>
+__device__ __forceinline__ void store8(void* p, int64_t at, const float (&f)[8]) {
+  *reinterpret_cast<uint4*>(static_cast<unsigned char*>(p) + at * 2) = D::pack(f);
+}
+
+// Angles of elements e .. e + 7 at a position: y = x c + o s with o the partner (its sign in s).
+struct Turn {
+  float c[8], s[8];
+};
+__device__ __forceinline__ Turn turn_at(const float* cs, int rot, int e, bool neighbours) {
+  Turn t;
+  const int half = rot >> 1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t.c[i] = 1.f;
+    t.s[i] = 0.f;
+  }
+  if (e >= rot) return t;
+  if (neighbours) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + (e >> 1))), s = __ldg(reinterpret_cast<const float4*>(cs + half + (e >> 1)));
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      t.c[i] = cc[i >> 1];
+      t.s[i] = (i & 1) ? ss[i >> 1] : -ss[i >> 1];
+    }
+    return t;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {  // four elements lie on one side of rot / 2, a multiple of 4
+    const bool first = e + i < half;
+    const int k = first ? e + i : e + i - half;
+    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + k)), s = __ldg(reinterpret_cast<const float4*>(cs + half + k));
+    t.c[i] = c.x;
+    t.c[i + 1] = c.y;
+    t.c[i + 2] = c.z;
+    t.c[i + 3] = c.w;
+    t.s[i] = first ? -s.x : s.x;
+    t.s[i + 1] = first ? -s.y : s.y;
+    t.s[i + 2] = first ? -s.z : s.z;
+    t.s[i + 3] = first ? -s.w : s.w;
+  }
+  return t;
+}
+// The partners of elements e .. e + 7 of the row at `at`, x being the elements themselves.
+template <class D>
+__device__ __forceinline__ void partners(const void* p, int64_t at, int e, int rot, bool neighbours, const float (&x)[8], float (&o)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = neighbours ? x[i ^ 1] : 0.f;
+  if (neighbours || e >= rot) return;
+  const int half = rot >> 1;
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const float4 y = load4<D>(p, at + (e + i < half ? e + i + half : e + i - half));
+    o[i] = y.x;
+    o[i + 1] = y.y;
+    o[i + 2] = y.z;
+    o[i + 3] = y.w;
+  }
+}
+__device__ __forceinline__ void turned(float (&x)[8], const float (&o)[8], const Turn& t, bool rotated) {
+  if (!rotated) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(o[i], t.s[i]));
+}
+
+constexpr int kQHeads = 4;  // query heads of a unit
+
+template <class D, int DH>
+__global__ void __launch_bounds__(kCacheThreads) k_kv4_append_runs(AppendArgs a) {
+  using B = Kv4Block<DH>;
+  constexpr int kLanes = DH / 8, kRows = 32 / kLanes;  // lanes a row; rows a warp moves at once
+  const Kv4View& c = a.c;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, e = (lane % kLanes) * 8;
+  const int j = e >> 5, t8 = (e & 31) >> 3;
+  const int rot = a.cos_sin ? a.rot : 0;
+  const int q_units = (a.q_heads + kQHeads - 1) / kQHeads;
+  for_units(c, 2 * c.heads + q_units, [&](int b, const RunSeq& rs, int blk, int what) {
+    const int64_t at = kv4_block_at(c, b, blk * kKv4Block, B::kBytes);
+    const int p0 = max(rs.s.len - rs.s.n, blk * kKv4Block), p1 = min(rs.s.len, (blk + 1) * kKv4Block);
+    if (at < 0 || (a.cos_sin && p1 > a.positions)) {
+      if (lane == 0) kv4_bad(c);
+      if (at < 0) return;
+    }
+    const int last = a.cos_sin && p1 > a.positions ? int(a.positions) : p1;  // positions [p0, last) are handled
+    const int64_t row0 = int64_t(rs.s.start) + rs.s.n - rs.s.len;             // row of position 0
+    if (what >= 2 * c.heads) {  // queries: kRows heads at once, the angles loaded once a token
+      const int h0 = (what - 2 * c.heads) * kQHeads;
+      for (int p = p0; p < last; ++p) {
+        Turn t;
+        if (rot) t = turn_at(a.cos_sin + int64_t(p) * rot, rot, e, a.neighbours);
+        float x[kQHeads / kRows > 0 ? kQHeads / kRows : 1][8];
+#pragma unroll
+        for (int k = 0; k < kQHeads / kRows; ++k) {
+          const int h = h0 + k * kRows + sub;
+          if (h >= a.q_heads) continue;
+          const int64_t from = (row0 + p) * a.q.token + h * a.q.head;
+          float o[8];
+          load8<D>(a.q.p, from + e, x[k]);
+          if (rot) {
+            partners<D>(a.q.p, from, e, rot, a.neighbours, x[k], o);
+            turned(x[k], o, t, e < rot);
+          }
+        }
+        __syncwarp();  // q may be rotated in place: every lane has its partners
+#pragma unroll
+        for (int k = 0; k < kQHeads / kRows; ++k) {
+          const int h = h0 + k * kRows + sub;
+          if (h < a.q_heads) store8<D>(const_cast<void*>(a.q_out.p), (row0 + p) * a.q_out.token + h * a.q_out.head + e, x[k]);
+        }
+      }
+      return;
+    }
+    const bool is_v = what >= c.heads;
+    const int h = is_v ? what - c.heads : what;
+    const Kv4Rows& src = is_v ? a.v : a.k;
+    unsigned char* out = c.data + at + int64_t(h) * c.page_blocks * B::kBytes;
+#pragma unroll 2
+    for (int r0 = 0; r0 < kKv4Block; r0 += kRows) {  // token r of the block
+      const int r = r0 + sub, p = blk * kKv4Block + r;
+      const bool on = p >= p0 && p < last;
+      if (!__any_sync(kFull, on)) continue;
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (on) {
+        const int64_t from = (row0 + p) * src.token + h * src.head;
+        load8<D>(src.p, from + e, x);
+        if (!is_v && e < rot) {
+          float o[8];
+          partners<D>(src.p, from, e, rot, a.neighbours, x, o);
+          turned(x, o, turn_at(a.cos_sin + int64_t(p) * rot, rot, e, a.neighbours), true);
+        }
+      }
+      float lo = 65504.f, hi = -65504.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = limited(x[i]);
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+      }
+#pragma unroll
+      for (int o = 2; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
+      }
+      const __half zh = __float2half_rn(lo), sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+      const float z = __half2float(zh), s = __half2float(sh);
+      uint32_t eight = 0;
+      if (s > 0.f) {
+        const float inv = __frcp_rn(s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) eight |= code_of(x[i], z, s, inv) << (4 * i);
+      }
+      if (!is_v) {
+        if (on) {
+          reinterpret_cast<uint32_t*>(out)[r * (DH / 8) + B::G * t8 + j] = eight;
+          if (t8 == 0) {
+            reinterpret_cast<__half*>(out + B::kKScale)[r * B::G + j] = sh;
+            reinterpret_cast<__half*>(out + B::kKZero)[r * B::G + j] = zh;
+          }
+        }
+      } else {  // a word holds four elements of two tokens: the lanes of an even and an odd token make one each
+        const uint32_t other = __shfl_xor_sync(kFull, eight, kLanes);
+        const bool odd = r & 1, both = __shfl_xor_sync(kFull, on ? 1 : 0, kLanes) && on;
+        const int f = r >> 3, t = (r & 7) >> 1;
+        uint32_t* w = reinterpret_cast<uint32_t*>(out + B::kV) + ((f * 8 + 2 * t8) * 4 + t) * B::G + j;  // g = 2 t8; g + 1 is 4 G further
+        if (both) {
+          w[odd ? 4 * B::G : 0] = odd ? (other >> 16) | (eight & 0xffff0000u) : (eight & 0xffffu) | (other << 16);
+        } else if (on) {
+          reinterpret_cast<uint16_t*>(w)[odd] = uint16_t(eight);
+          reinterpret_cast<uint16_t*>(w + 4 * B::G)[odd] = uint16_t(eight >> 16);
+        }
+        if (on && t8 == 0) {
+          reinterpret_cast<__half*>(out + B::kVScale)[((r >> 1) * B::G + j) * 2 + odd] = sh;
+          reinterpret_cast<__half*>(out + B::kVZero)[((r >> 1) * B::G + j) * 2 + odd] = zh;
+        }
+      }
+    }
+  });
+}
+
+template <class D, int DH>
+__global__ void __launch_bounds__(kCacheThreads) k_kv4_gather_runs(GatherArgs a) {
+  using B = Kv4Block<DH>;
+  constexpr int G = B::G;
+  const Kv4View& c = a.c;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  for_units(c, c.heads, [&](int b, const RunSeq& rs, int blk, int h) {
+    int64_t at = kv4_block_at(c, b, blk * kKv4Block, B::kBytes);
+    if (at < 0) {
+      if (lane == 0) kv4_bad(c);
+      return;
+    }
+    const unsigned char* from = c.data + at + int64_t(h) * c.page_blocks * B::kBytes;
+    const int p0 = max(rs.s.len - rs.s.n, 0);
+    const int64_t row0 = int64_t(rs.s.start) + rs.s.n - rs.s.len;
+    // keys: lane (g, t) has words G t .. of token g, then of token g + 8
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i, p = blk * kKv4Block + r;
+      if (p < p0 || p >= rs.s.len) continue;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(from) + r * (DH / 8) + G * t;
+      const __half* s = reinterpret_cast<const __half*>(from + B::kKScale) + r * G;
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const uint32_t x = __ldg(w + j);
+        const float4 lo = decoded4(x & 0xffffu, __half2float(s[j]), __half2float(s[16 * G + j]));
+        const float4 hi = decoded4(x >> 16, __half2float(s[j]), __half2float(s[16 * G + j]));
+        const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        store8<D>(const_cast<void*>(a.k.p), (row0 + p) * a.k.token + h * a.k.head + 32 * j + 8 * t, f);
+      }
+    }
+    // values: lane (g, t) has words of tokens 8 f + 2 t and the next
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(from + B::kV) + ((f * 8 + g) * 4 + t) * G;
+      const uint32_t* s = reinterpret_cast<const uint32_t*>(from + B::kVScale) + (4 * f + t) * G;
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const uint32_t x = __ldg(w + j), sc = __ldg(s + j), z = __ldg(s + 8 * G + j);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int p = blk * kKv4Block + 8 * f + 2 * t + k;
+          if (p < p0 || p >= rs.s.len) continue;
+          const float4 v = decoded4(k ? x >> 16 : x & 0xffffu, k ? f16_hi(sc) : f16_lo(sc), k ? f16_hi(z) : f16_lo(z));
+          store4<D>(const_cast<void*>(a.v.p), (row0 + p) * a.v.token + h * a.v.head + 32 * j + 4 * g, v);
+        }
+      }
+    }
+  });
+}
+
 int grid_for(int64_t warps, const DeviceInfo& dev) {
   const int64_t blocks = (warps + kCacheThreads / 32 - 1) / (kCacheThreads / 32), most = int64_t(dev.sm_count) * 32;
   return int(blocks < most ? blocks : most);
+}
+
+// Runs of at least 4 tokens a sequence on average go by blocks of 16, fewer by single rows.
+bool in_runs(const Kv4View& c) { return c.cu && c.tokens >= 4 * int64_t(c.batch); }
+int grid_for_runs(const Kv4View& c, int subs, const DeviceInfo& dev) {
+  return grid_for((c.tokens / kKv4Block + 2 * int64_t(c.batch)) * subs, dev);
 }
 
 }  // namespace
@@ -204,9 +518,15 @@ cudaError_t launch_kv4_append(const Kv4View& c, const Kv4Rows& k, const Kv4Rows&
                               int q_heads, const float* cos_sin, int64_t positions, int rot, bool neighbours, int dtype,
                               cudaStream_t stream, const DeviceInfo& dev) {
   const AppendArgs a{c, k, v, q, q_out, cos_sin, positions, q_heads, rot, neighbours ? 1 : 0};
+  using Kern = void (*)(AppendArgs);
+  if (in_runs(c)) {
+    const Kern kern = dtype == 2 ? (c.d == 64 ? (Kern)k_kv4_append_runs<F16, 64> : (Kern)k_kv4_append_runs<F16, 128>)
+                                 : (c.d == 64 ? (Kern)k_kv4_append_runs<BF16, 64> : (Kern)k_kv4_append_runs<BF16, 128>);
+    kern<<<grid_for_runs(c, 2 * c.heads + (q_heads + kQHeads - 1) / kQHeads, dev), kCacheThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
   const int per = c.d == 64 ? 2 : 1, rows = 2 * c.heads + q_heads;
   const int grid = grid_for(c.tokens * ((rows + per - 1) / per), dev);
-  using Kern = void (*)(AppendArgs);
   const Kern kern = dtype == 2 ? (c.d == 64 ? (Kern)k_kv4_append<F16, 64> : (Kern)k_kv4_append<F16, 128>)
                                : (c.d == 64 ? (Kern)k_kv4_append<BF16, 64> : (Kern)k_kv4_append<BF16, 128>);
   kern<<<grid, kCacheThreads, 0, stream>>>(a);
@@ -216,9 +536,15 @@ cudaError_t launch_kv4_append(const Kv4View& c, const Kv4Rows& k, const Kv4Rows&
 cudaError_t launch_kv4_gather(const Kv4View& c, const Kv4Rows& k, const Kv4Rows& v, int dtype, cudaStream_t stream,
                               const DeviceInfo& dev) {
   const GatherArgs a{c, k, v};
+  using Kern = void (*)(GatherArgs);
+  if (in_runs(c)) {
+    const Kern kern = dtype == 2 ? (c.d == 64 ? (Kern)k_kv4_gather_runs<F16, 64> : (Kern)k_kv4_gather_runs<F16, 128>)
+                                 : (c.d == 64 ? (Kern)k_kv4_gather_runs<BF16, 64> : (Kern)k_kv4_gather_runs<BF16, 128>);
+    kern<<<grid_for_runs(c, c.heads, dev), kCacheThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
   const int per = c.d == 64 ? 2 : 1;
   const int grid = grid_for(c.tokens * ((c.heads + per - 1) / per), dev);
-  using Kern = void (*)(GatherArgs);
   const Kern kern = dtype == 2 ? (c.d == 64 ? (Kern)k_kv4_gather<F16, 64> : (Kern)k_kv4_gather<F16, 128>)
                                : (c.d == 64 ? (Kern)k_kv4_gather<BF16, 64> : (Kern)k_kv4_gather<BF16, 128>);
   kern<<<grid, kCacheThreads, 0, stream>>>(a);

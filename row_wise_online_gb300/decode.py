@@ -48,57 +48,76 @@ def _declare(lib) -> None:
         getattr(lib, name).restype = ci
 
 
-def _tensor(t, name, dtype, shape, device):
-    """Data pointer of a contiguous tensor of a dtype and shape on the call's device (None stays None)."""
+def _tensor(t, name, dtype, shape, index):
+    """Data pointer of a contiguous tensor of a dtype and shape on CUDA device ``index`` (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
     return t.data_ptr()
 
 
 @contextlib.contextmanager
-def _on(device, stream):
-    """The device made current, and the stream as a pointer; torch allocations inside belong to that stream."""
+def _switched(index, stream):
     import torch
 
-    with torch.cuda.device(device):
-        if stream is None:
-            s = torch.cuda.current_stream(device)
-        elif hasattr(stream, "cuda_stream"):
-            s = stream
-        else:
-            s = torch.cuda.ExternalStream(int(stream), device=device)
-        with torch.cuda.stream(s):
-            yield ctypes.c_void_p(int(s.cuda_stream))
+    s = stream
+    if s is not None and not hasattr(s, "cuda_stream"):
+        s = torch.cuda.ExternalStream(int(s), device=index)
+    with torch.cuda.device(index), torch.cuda.stream(s):
+        yield torch.cuda.current_stream(index).cuda_stream
 
 
-def _rows(t, name, heads, tokens, dim, dtype, device):
+class _Here:
+    """The current device's current stream, where nothing has to be switched."""
+
+    __slots__ = ("stream",)
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        return self.stream
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _on(index, stream):
+    """Context: device ``index`` current, the stream's pointer; what torch allocates inside belongs to that stream."""
+    import torch
+
+    if stream is None and torch.cuda.current_device() == index:
+        return _Here(torch.cuda.current_stream(index).cuda_stream)
+    return _switched(index, stream)
+
+
+def _rows(t, name, heads, tokens, dim, dtype, index):
     """[tokens, heads, dim] with the elements of a head side by side."""
-    if t.dim() != 3 or tuple(t.shape) != (tokens, heads, dim) or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {(tokens, heads, dim)} on {device}")
-    if t.stride(2) != 1 and t.numel():
+    if t.shape != (tokens, heads, dim) or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(tokens, heads, dim)} on cuda:{index}")
+    s = t.stride()
+    if s[2] != 1 and t.numel():
         raise ValueError(f"{name}: the elements of a head must be contiguous (stride(2) == 1)")
-    return _Rows(t.data_ptr(), t.stride(0) if tokens > 1 else heads * dim, t.stride(1) if heads > 1 else dim)
+    return _Rows(t.data_ptr(), s[0] if tokens > 1 else heads * dim, s[1] if heads > 1 else dim)
 
 
 def _paged(cache, page_table, seq_lens, cu_tokens, tokens):
-    """The cache argument: shapes and types checked, pointers taken."""
+    """The cache argument and its device: shapes and types checked, pointers taken."""
     import torch
 
-    if not cache.is_cuda or cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] % 20:
+    if cache.dtype is not torch.uint8 or cache.dim() != 4 or not cache.is_cuda or not cache.is_contiguous() or cache.shape[3] % 20:
         raise ValueError("cache must be a contiguous CUDA uint8 tensor [pages, heads, page_size / 16, 20 * head_dim] (kv4_cache_empty)")
-    pages, heads, blocks, held = (int(s) for s in cache.shape)
+    pages, heads, blocks, held = cache.shape
     if page_table.dim() != 2:
         raise ValueError("page_table must be a 2-D int32 tensor [batch, pages a sequence has room for]")
-    batch, width = (int(s) for s in page_table.shape)
+    batch, width = page_table.shape
     if cu_tokens is None and tokens != batch:
         raise ValueError(f"{tokens} rows for {batch} sequences: cu_tokens is needed where they are not one each")
-    dev = cache.device
-    return _Cache(cache.data_ptr(), _tensor(page_table, "page_table", torch.int32, (batch, width), dev),
-                  _tensor(seq_lens, "seq_lens", torch.int32, (batch,), dev),
-                  _tensor(cu_tokens, "cu_tokens", torch.int32, (batch + 1,), dev),
-                  pages, blocks * 16, heads, held // 20, batch, width, tokens)
+    index, i32 = cache.get_device(), torch.int32
+    return _Cache(cache.data_ptr(), _tensor(page_table, "page_table", i32, (batch, width), index),
+                  _tensor(seq_lens, "seq_lens", i32, (batch,), index), _tensor(cu_tokens, "cu_tokens", i32, (batch + 1,), index),
+                  pages, blocks * 16, heads, held // 20, batch, width, tokens), index
 
 
 def kv4_cache_empty(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, device=None):
@@ -127,26 +146,26 @@ def kv4_append(k, v, cache, page_table, seq_lens, cu_tokens=None, q=None, q_out=
     if k.dim() != 3:
         raise ValueError("k must be a 3-D tensor [tokens, kv_heads, head_dim]")
     T = int(k.shape[0])
-    c = _paged(cache, page_table, seq_lens, cu_tokens, T)
-    dt, dev = _rwo._dtype_code(k), cache.device
-    kr, vr = (_rows(t, n, c.heads, T, c.head_dim, k.dtype, dev) for t, n in ((k, "k"), (v, "v")))
+    c, index = _paged(cache, page_table, seq_lens, cu_tokens, T)
+    dt, d = _rwo._dtype_code(k), cache.shape[3] // 20
+    kr, vr = (_rows(t, n, c.heads, T, d, k.dtype, index) for t, n in ((k, "k"), (v, "v")))
     if q is None and q_out is not None:
         raise ValueError("q_out without q")
     positions = rotated = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be a 2-D float32 tensor [positions, rotated]")
-        positions, rotated = (int(s) for s in cos_sin.shape)
-    table = _tensor(cos_sin, "cos_sin", torch.float32, (positions, rotated), dev)
+        positions, rotated = cos_sin.shape
+    table = _tensor(cos_sin, "cos_sin", torch.float32, (positions, rotated), index)
     qr = qo = None
     heads = 0
-    with _on(dev, stream) as s:
+    with _on(index, stream) as s:
         if q is not None:
             heads = int(q.shape[1]) if q.dim() == 3 else 0
-            qr = _rows(q, "q", heads, T, c.head_dim, k.dtype, dev)
+            qr = _rows(q, "q", heads, T, d, k.dtype, index)
             if q_out is None:
-                q_out = torch.empty((T, heads, c.head_dim), dtype=q.dtype, device=dev)
-            qo = _rows(q_out, "q_out", heads, T, c.head_dim, k.dtype, dev)
+                q_out = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
+            qo = _rows(q_out, "q_out", heads, T, d, k.dtype, index)
         st = _rwo.capi().kv4_append(c, kr, vr, qr, qo, heads, table, positions, rotated, KV4_FLAG_NEIGHBOURS if interleaved else 0, dt, s)
     _rwo._check(st, "kv4_append")
     return q_out
@@ -164,14 +183,13 @@ def kv4_gather(cache, page_table, seq_lens, cu_tokens=None, num_tokens: int | No
         if k is None and cu_tokens is not None:
             raise ValueError("num_tokens (cu_tokens' last entry) is needed to allocate k and v")
         num_tokens = int(k.shape[0]) if k is not None else int(page_table.shape[0])
-    c = _paged(cache, page_table, seq_lens, cu_tokens, int(num_tokens))
-    dev = cache.device
+    c, index = _paged(cache, page_table, seq_lens, cu_tokens, int(num_tokens))
     dtype = dtype or (k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16)
     shape = (int(num_tokens), c.heads, c.head_dim)
-    with _on(dev, stream) as s:
-        k = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
-        v = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
-        kr, vr = (_rows(t, n, c.heads, shape[0], c.head_dim, dtype, dev) for t, n in ((k, "k"), (v, "v")))
+    with _on(index, stream) as s:
+        k = torch.empty(shape, dtype=dtype, device=cache.device) if k is None else k
+        v = torch.empty(shape, dtype=dtype, device=cache.device) if v is None else v
+        kr, vr = (_rows(t, n, shape[1], shape[0], shape[2], dtype, index) for t, n in ((k, "k"), (v, "v")))
         st = _rwo.capi().kv4_gather(c, kr, vr, _rwo._dtype_code(k), s)
     _rwo._check(st, "kv4_gather")
     return k, v
@@ -201,20 +219,21 @@ def attention_kv4(q, cache, page_table, seq_lens, cu_tokens=None, o=None, lse_ou
     if q.dim() != 3:
         raise ValueError("q must be a 3-D tensor [tokens, heads, head_dim]")
     T, heads = int(q.shape[0]), int(q.shape[1])
-    c = _paged(cache, page_table, seq_lens, cu_tokens, T)
-    dt, dev = _rwo._dtype_code(q), cache.device
-    qr = _rows(q, "q", heads, T, c.head_dim, q.dtype, dev)
-    lse = _tensor(lse_out, "lse_out", torch.float32, (T, heads), dev)
-    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev):
+    c, index = _paged(cache, page_table, seq_lens, cu_tokens, T)
+    dt, d = _rwo._dtype_code(q), cache.shape[3] // 20
+    qr = _rows(q, "q", heads, T, d, q.dtype, index)
+    lse = _tensor(lse_out, "lse_out", torch.float32, (T, heads), index)
+    if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != index):
         raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
-    with _on(dev, stream) as s:
+    lib = _rwo.capi()
+    with _on(index, stream) as s:
         if o is None:
-            o = torch.empty((T, heads, c.head_dim), dtype=q.dtype, device=dev)
-        op = _tensor(o, "o", q.dtype, (T, heads, c.head_dim), dev)
+            o = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
+        op = _tensor(o, "o", q.dtype, (T, heads, d), index)
         if workspace is None:
-            n = int(_rwo.capi().attention_kv4_workspace(c.batch, T, heads, c.heads, c.head_dim))
-            workspace = torch.empty(max(n, 0), dtype=torch.uint8, device=dev)
-        st = _rwo.capi().attention_kv4(c, qr, op, lse, heads, 0.0 if scale is None else float(scale), dt, workspace.data_ptr(),
+            n = lib.attention_kv4_workspace(page_table.shape[0], T, heads, cache.shape[1], d)
+            workspace = torch.empty(max(n, 0), dtype=torch.uint8, device=q.device)
+        st = lib.attention_kv4(c, qr, op, lse, heads, 0.0 if scale is None else float(scale), dt, workspace.data_ptr(),
                                        workspace.numel(), s)
     _rwo._check(st, "attention_kv4")
     return o
@@ -237,36 +256,37 @@ def logits_process_rows(x, y=None, out: str = "softmax", lse_out=None, tokens=No
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
     M, N, ldx = _rwo._rows_strided(x)
-    dt, dev = _rwo._dtype_code(x), x.device
+    dt, index = _rwo._dtype_code(x), x.get_device()
     a = _Logits(x=x.data_ptr(), ldx=ldx)
     if tokens is not None:
         if tokens.dim() != 2 or token_lens is None:
             raise ValueError("tokens must be a 2-D int32 tensor [M, L], with token_lens")
         a.token_width = int(tokens.shape[1])
-        a.tokens = _tensor(tokens, "tokens", torch.int32, (M, a.token_width), dev)
-        a.token_lens = _tensor(token_lens, "token_lens", torch.int32, (M,), dev)
-        a.prompt_lens = _tensor(prompt_lens, "prompt_lens", torch.int32, (M,), dev)
+        a.tokens = _tensor(tokens, "tokens", torch.int32, (M, a.token_width), index)
+        a.token_lens = _tensor(token_lens, "token_lens", torch.int32, (M,), index)
+        a.prompt_lens = _tensor(prompt_lens, "prompt_lens", torch.int32, (M,), index)
     elif any(t is not None for t in (prompt_lens, token_lens, repetition, frequency, presence)):
         raise ValueError("penalties need tokens")
     for n, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence), ("scale", scale), ("lse_out", lse_out)):
-        setattr(a, n, _tensor(t, n, torch.float32, (M,), dev))
+        if t is not None:
+            setattr(a, n, _tensor(t, n, torch.float32, (M,), index))
     if (bias_ids is None) != (bias_values is None):
         raise ValueError("bias_ids and bias_values go together")
     if bias_ids is not None:
         if bias_ids.dim() != 2:
             raise ValueError("bias_ids must be a 2-D int32 tensor [M, K]")
         a.bias_count = int(bias_ids.shape[1])
-        a.bias_ids = _tensor(bias_ids, "bias_ids", torch.int32, (M, a.bias_count), dev)
-        a.bias_values = _tensor(bias_values, "bias_values", torch.float32, (M, a.bias_count), dev)
+        a.bias_ids = _tensor(bias_ids, "bias_ids", torch.int32, (M, a.bias_count), index)
+        a.bias_values = _tensor(bias_values, "bias_values", torch.float32, (M, a.bias_count), index)
     if mask is not None:
         a.ld_mask = int(mask.shape[1]) if mask.dim() == 2 else 0
         if a.ld_mask < (N + 31) // 32:
             raise ValueError("mask must be an int32 tensor [M, words] with a bit for each token")
-        a.mask = _tensor(mask, "mask", torch.int32, (M, a.ld_mask), dev)
-    with _on(dev, stream) as s:
+        a.mask = _tensor(mask, "mask", torch.int32, (M, a.ld_mask), index)
+    with _on(index, stream) as s:
         if y is None:
-            y = torch.empty((M, N), dtype=x.dtype, device=dev)
-        if tuple(y.shape) != (M, N) or y.dtype != x.dtype or y.device != dev:
+            y = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        if y.shape != (M, N) or y.dtype is not x.dtype or y.get_device() != index:
             raise ValueError("y must have x's shape, dtype and device")
         a.y, a.ldy = y.data_ptr(), _rwo._rows_strided(y)[2]
         st = _rwo.capi().logits_process_rows(a, M, N, dt, LOGITS_OUT[out], s)
