@@ -14,12 +14,14 @@
 // * S^T = K Q^T (m16n8k16: 16 keys by 8 query rows) and O^T = V^T P^T: with the keys as M a tile of 8 query rows wastes
 //   nothing, as it would with queries as M = 16.  P changes from accumulator to operand layout with movmatrix.
 // * Per group, P is multiplied by the values' scales (8 packed multiplications per 16 keys) instead of 512 values per
-//   16 keys being multiplied by them; the zeros are one more product, with P alone.
-// * P is fp16 with 2^9 as the weight of the running maximum, which moves only when a score exceeds it by 2^6 (so
-//   weights stay below 2^15): a vote per 16 keys instead of a maximum over lanes.  fp16's rounding is 2^-11 of a weight
-//   (bf16 would be 2^-8); weights down to 2^-33 of the largest still count.  l sums unrounded weights in fp32.  The
-//   scales of V are brought below 1 by a power of two that only grows, moved by the same vote, so P s fits fp16.
-// * A CTA is 4 consumer warps and a producer warp, which keeps a ring of 64-key stages (cp.async.bulk of one block per
+//   16 keys being multiplied by them; the zeros are one more product, with P alone.  A row of ones beside the zeros gives
+//   the sum of the rounded weights, by which the result is divided, so that what rounding does to all weights alike
+//   cancels; l, for the LSE, sums the weights before rounding, in fp32.
+// * A weight is p = 2^(score + mb), fp16 for the product: mb puts the running maximum at 2^(9 - e) and moves only when a
+//   score exceeds it by 2^6, or a scale of V exceeds 2^e (e = 0 at first, so V up to 15 in magnitude), so that p s stays
+//   below 2^15.  One vote per 32 keys replaces a maximum over lanes.  fp16's rounding is 2^-11 of a weight (bf16 would
+//   be 2^-8); weights down to 2^-33 of the largest still count.
+// * A CTA is 4 consumer warps and a producer warp, which keeps a ring of stages (cp.async.bulk of one or two blocks per
 //   consumer warp) ahead of them.  The tiles of all sequences and heads form one list, cut into equal runs, one per
 //   resident CTA: long and short sequences mix without imbalance.  A run that ends inside a (sequence, head) leaves its
 //   state (m, l, O) in the workspace; a second kernel merges such states in the order of the runs.
@@ -31,13 +33,10 @@
 namespace rwo {
 namespace {
 
-constexpr int kWarps = 4;                     // consumer warps, one block of 16 keys each per stage
-constexpr int kKeys = kWarps * kKv4Block;     // keys of a stage
+constexpr int kWarps = 4;                     // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kStages = 4;
-constexpr int kMinTiles = 2;                  // stages a CTA takes at least
 constexpr float kBase = 9.f, kSlack = 6.f;    // log2 of the maximum's weight, and by how much a score may exceed it
-constexpr float kUnseen = -1e30f;             // maximum of a row that has seen no key
+constexpr float kUnseen = 1e30f;              // mb of a row that has seen no key
 
 struct AttnArgs {
   Kv4View c;
@@ -47,21 +46,27 @@ struct AttnArgs {
   int q_heads, group;
   float scale;       // scale * log2 e
   int64_t* prefix;   // [batch + 1]: first tile of each sequence in the list (workspace)
-  float* part_ml;    // [2 grid][rows][2]
+  float4* part_l;    // [2 grid][rows]: mb, l, sum of the rounded weights
   float* part_o;     // [2 grid][rows][d]
   int runs;          // CTAs of the main kernel
   uint64_t wait_ns;
 };
 
+// D = A B + C, 16 x 8 x 16 and 16 x 8 x 8, fp16 in, fp32 out.
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(b0));
+__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma8_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 // An 8 x 8 matrix of 16-bit elements: lane (g, t) gives row g, columns 2 t and 2 t + 1 and gets column g, rows 2 t, 2 t + 1.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -74,39 +79,37 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 
-// n consecutive 32-bit words of shared memory.
+// n consecutive 32-bit words.
 template <int n>
-__device__ __forceinline__ void lds_words(uint32_t (&w)[n], uint32_t addr) {
+__device__ __forceinline__ void words_at(uint32_t (&w)[n], const unsigned char* p) {
   if constexpr (n == 4) {
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
   } else if constexpr (n == 2) {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
   } else {
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
-__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
-  uint32_t w;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
-  return w;
-}
+__device__ __forceinline__ uint32_t word_at(const unsigned char* p) { return *reinterpret_cast<const uint32_t*>(p); }
 
 // Tiles of a sequence in the list: every head and block of query rows takes all of its keys.
 struct SeqWork {
   Kv4Seq s;
   int row_blocks, tiles;
 };
-__device__ __forceinline__ SeqWork seq_work(const Kv4View& c, int b, int group, int rows, bool& bad) {
+template <int R, int KEYS>
+__device__ __forceinline__ SeqWork seq_work(const Kv4View& c, int b, int group, bool& bad) {
   SeqWork w;
   w.s = kv4_seq(c, b, bad);
-  w.row_blocks = (w.s.n * group + rows - 1) / rows;
-  w.tiles = (w.s.len + kKeys - 1) / kKeys;
+  w.row_blocks = (w.s.n * group + R - 1) / R;
+  w.tiles = (w.s.len + KEYS - 1) / KEYS;
   if (w.tiles < 1) w.tiles = 1;
   return w;
 }
@@ -119,10 +122,7 @@ struct Runs {
   __device__ __forceinline__ int64_t first(int i) const { return W * i / n; }
   __device__ __forceinline__ int of(int64_t tile) const { return int(((tile + 1) * n - 1) / W); }
 };
-__device__ __forceinline__ Runs runs_of(int64_t W, int runs) {
-  const int64_t n = (W + kMinTiles - 1) / kMinTiles;
-  return Runs{W, int(n < 1 ? 1 : n < runs ? n : runs)};
-}
+__device__ __forceinline__ Runs runs_of(int64_t W, int runs) { return Runs{W, int(W < 1 ? 1 : W < runs ? W : runs)}; }
 
 // A place in the list: one (sequence, head, block of rows) and a range of its tiles.
 struct Cursor {
@@ -130,7 +130,8 @@ struct Cursor {
   SeqWork w;
 };
 // To the next (sequence, head, block of rows).
-__device__ __forceinline__ void next_item(Cursor& k, const Kv4View& c, int group, int rows) {
+template <int R, int KEYS>
+__device__ __forceinline__ void next_item(Cursor& k, const Kv4View& c, int group) {
   k.tile = 0;
   if (++k.rb < k.w.row_blocks) return;
   k.rb = 0;
@@ -139,21 +140,25 @@ __device__ __forceinline__ void next_item(Cursor& k, const Kv4View& c, int group
   bool bad = false;
   do {
     if (++k.b >= c.batch) return;
-    k.w = seq_work(c, k.b, group, rows, bad);
+    k.w = seq_work<R, KEYS>(c, k.b, group, bad);
   } while (k.w.row_blocks == 0);
 }
 
-template <int DH, int NT>
+template <int DH, int NT, int KB>
 struct Smem {
   using B = Kv4Block<DH>;
+  static constexpr int kStages = KB * DH >= 256 ? 2 : DH == 128 ? 4 : 6 / KB;
+  static constexpr int kCtas = NT == 2 ? (DH == 64 ? 3 : 2) : DH == 64 ? 4 : 3;  // resident on an SM: bounds the registers
+  static constexpr int kBlocks = kWarps * KB;            // of a stage
+  static constexpr int kKeys = kBlocks * kKv4Block;
   static constexpr int R = 8 * NT;                       // query rows of a tile
-  static constexpr int kStage = kWarps * B::kBytes;
+  static constexpr int kStage = kBlocks * B::kBytes;
   static constexpr int kPad = DH + 8;
   static constexpr int kOffQ = kStages * kStage;         // fragments: [NT][2 G][32 lanes][2 words]
   static constexpr int kOffQz = kOffQ + NT * 2 * B::G * 256;   // [NT][32 lanes] words
   static constexpr int kOffRow = kOffQz + NT * 128;      // [R] score factors
-  static constexpr int kOffMl = kOffRow + R * 4;         // [4 warps][R][2]
-  static constexpr int kOffO = kOffMl + kWarps * R * 8;  // [4 warps][8 rows][kPad]
+  static constexpr int kOffMl = kOffRow + R * 4;         // [4 warps][R] x 3
+  static constexpr int kOffO = kOffMl + kWarps * R * 16;  // [4 warps][8 rows][kPad]
   static constexpr int kOffBar = kOffO + kWarps * 8 * kPad * 4;
   static constexpr int kOffScan = kOffBar + 2 * kStages * 8;  // [4 warps] + start
   static constexpr int kBytes = kOffScan + 64;
@@ -168,11 +173,12 @@ __device__ __forceinline__ float elem_to_f32(uint32_t w, int half) {
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 
-// One finished row: O / l in the element type, LSE = (m - base) ln 2 + ln l.  A row that saw no key gives 0 and -inf.
+// One finished row: O over the sum of its weights in the element type, LSE = ln l - mb ln 2.  A row that saw no key gives
+// 0 and -inf.  s: mb, l, sum of the rounded weights.
 template <bool H, int DH>
-__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t out, int lane, const float (&x)[DH / 32], float M, float L) {
+__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t out, int lane, const float (&x)[DH / 32], float4 s) {
   constexpr int E = DH / 32;
-  const float inv = safe_inv(L);
+  const float inv = safe_inv(s.z);
   uint32_t w[E / 2];
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
@@ -182,15 +188,15 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t out, int la
   unsigned char* o = a.o + out * DH * 2 + lane * E * 2;
   if constexpr (E == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
   else *reinterpret_cast<uint32_t*>(o) = w[0];
-  if (lane == 0 && a.lse) a.lse[out] = L > 0.f ? __fmaf_rn(__fsub_rn(M, kBase), 0.6931471805599453f, logf(L)) : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[out] = s.y > 0.f ? __fmaf_rn(s.x, -0.6931471805599453f, logf(s.y)) : -INFINITY;
 }
 
-// H: fp16 elements (else bf16); DH: head dimension; NT: tiles of 8 query rows.
-template <bool H, int DH, int NT>
-__global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
+// H: fp16 elements (else bf16); DH: head dimension; NT: tiles of 8 query rows; KB: blocks of 16 keys a warp takes at once.
+template <bool H, int DH, int NT, int KB>
+__global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention_kv4(AttnArgs a) {
   using B = Kv4Block<DH>;
-  using SM = Smem<DH, NT>;
-  constexpr int G = B::G, R = SM::R;
+  using SM = Smem<DH, NT, KB>;
+  constexpr int G = B::G, R = SM::R, kKeys = SM::kKeys, kStages = SM::kStages;
   extern __shared__ __align__(128) unsigned char smem[];
   const Kv4View& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
   const int per = (c.batch + 127) / 128, b0 = tid < 128 ? min(tid * per, c.batch) : c.batch, b1 = tid < 128 ? min(b0 + per, c.batch) : c.batch;
   bool bad = false;
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_tiles(seq_work(c, b, a.group, R, bad), c.heads);
+  for (int b = b0; b < b1; ++b) mine += seq_tiles(seq_work<R, kKeys>(c, b, a.group, bad), c.heads);
   if (bad && blockIdx.x == 0) kv4_bad(c);
   int64_t before = mine;
 #pragma unroll
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
     int64_t p = before;
     for (int b = b0; b < b1; ++b) {
       a.prefix[b] = p;
-      p += seq_tiles(seq_work(c, b, a.group, R, bad), c.heads);
+      p += seq_tiles(seq_work<R, kKeys>(c, b, a.group, bad), c.heads);
     }
     if (tid == 0) a.prefix[c.batch] = W;
   }
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
   if (tid < 128 && run0 >= before && run0 < before + mine) {
     int64_t p = before;
     for (int b = b0; b < b1; ++b) {
-      const SeqWork w = seq_work(c, b, a.group, R, bad);
+      const SeqWork w = seq_work<R, kKeys>(c, b, a.group, bad);
       const int64_t n = seq_tiles(w, c.heads);
       if (run0 < p + n) {
         const int64_t x = run0 - p, item = x / w.tiles;
@@ -258,47 +264,45 @@ __global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
   at.h = start[1];
   at.rb = start[2];
   at.tile = start[3];
-  at.w = seq_work(c, at.b, a.group, R, bad);
+  at.w = seq_work<R, kKeys>(c, at.b, a.group, bad);
   int64_t left = run1 - run0;  // tiles of the run that remain
   bool timed_out = false;
 
   if (warp == kWarps) {
-    // ---- producer: lanes 0-3 copy the block of consumer warp `lane` for each stage ----
+    // ---- producer: one lane a block of the stage; the next stage's pages are looked up while a slot is waited for ----
+    const uint64_t policy = policy_evict_first();
+    auto block_of = [&]() -> int64_t {  // byte offset of this lane's block in the cursor's tile; -1: no key in it
+      const int key = at.tile * kKeys + lane * kKv4Block;
+      if (lane >= SM::kBlocks || key >= at.w.s.len) return -1;
+      int64_t off = kv4_block_at(c, at.b, key, B::kBytes);
+      if (off < 0) {  // no page: the status says so, and page 0 stands in
+        kv4_bad(c);
+        off = 0;
+      }
+      return off + int64_t(at.h) * c.page_blocks * B::kBytes;
+    };
     int slot = 0;
     uint32_t lap = 0;
-    int64_t issued = 0;
+    int64_t issued = 0, off = block_of();
     while (left > 0) {
-      const int here = int(left < at.w.tiles - at.tile ? left : at.w.tiles - at.tile);
-      for (int k = 0; k < here; ++k) {
-        const int key = (at.tile + k) * kKeys + lane * kKv4Block;
-        int64_t off = -1;
-        bool lost = false;
-        if (lane < kWarps && key < at.w.s.len) {
-          off = kv4_block_at(c, at.b, key, B::kBytes);
-          if (off < 0) {  // no page: the status says so, and page 0 stands in
-            lost = true;
-            off = 0;
-          }
-          off += int64_t(at.h) * c.page_blocks * B::kBytes;
-        }
-        if (lost) kv4_bad(c);
-        const int n = __popc(__ballot_sync(kFull, off >= 0));
-        if (issued >= kStages && !mbar_wait(empty(slot), lap ^ 1u, a.wait_ns)) timed_out = true;
-        if (lane == 0) {
-          if (n) mbar_arrive_expect_tx(full(slot), uint32_t(n * B::kBytes));
-          else mbar_arrive(full(slot));
-        }
-        __syncwarp();
-        if (off >= 0)
-          bulk_g2s(sbase + uint32_t(slot * SM::kStage + lane * B::kBytes), c.data + off, uint32_t(B::kBytes), full(slot), policy_evict_first());
-        ++issued;
-        if (++slot == kStages) {
-          slot = 0;
-          lap ^= 1u;
-        }
+      const int64_t now = off;
+      if (--left > 0) {
+        if (++at.tile == at.w.tiles) next_item<R, kKeys>(at, c, a.group);
+        off = block_of();
       }
-      left -= here;
-      if (left > 0) next_item(at, c, a.group, R);
+      const int n = __popc(__ballot_sync(kFull, now >= 0));
+      if (issued >= kStages && !mbar_wait(empty(slot), lap ^ 1u, a.wait_ns)) timed_out = true;
+      if (lane == 0) {
+        if (n) mbar_arrive_expect_tx(full(slot), uint32_t(n * B::kBytes));
+        else mbar_arrive(full(slot));
+      }
+      __syncwarp();
+      if (now >= 0) bulk_g2s(sbase + uint32_t(slot * SM::kStage + lane * B::kBytes), c.data + now, uint32_t(B::kBytes), full(slot), policy);
+      ++issued;
+      if (++slot == kStages) {
+        slot = 0;
+        lap ^= 1u;
+      }
     }
     // no copy may be in flight into this CTA when it exits: the last phase of every stage
     for (int s = 0; s < kStages && s < issued; ++s) {
@@ -348,8 +352,7 @@ __global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
       int ex = int(top >> 23) - 127;
       ex = ex < -90 ? -90 : ex > 90 ? 90 : ex;
       const float to = pow2(5 - ex);
-      if (lane == 0)
-        reinterpret_cast<float*>(smem + SM::kOffRow)[r] = a.scale * pow2(ex - 5 + 24);
+      if (lane == 0) reinterpret_cast<float*>(smem + SM::kOffRow)[r] = a.scale * pow2(ex - 5 + 24);
       float sum = 0.f;
       __half* qf = reinterpret_cast<__half*>(smem + SM::kOffQ);
 #pragma unroll
@@ -372,171 +375,188 @@ __global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
     }
     named_barrier_sync(1, kWarps * 32);
     uint32_t qf[NT][2 * G][2], qz[NT];
-    float ch[NT][2], m[NT][2], l[NT][2], O[NT][2 * G][4], Z[NT][4];
+    float ch[NT][2], mb[NT][2], l[NT][2], O[NT][2 * G][4], Z[NT][4];
     int seen[NT][2];  // keys that the row of column 2 t, 2 t + 1 sees
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
       for (int s = 0; s < 2 * G; ++s) {
-        uint32_t w[2];
-        lds_words<2>(w, sbase + uint32_t(SM::kOffQ + ((i * 2 * G + s) * 32 + lane) * 8));
-        qf[i][s][0] = w[0];
-        qf[i][s][1] = w[1];
+        words_at<2>(qf[i][s], smem + SM::kOffQ + ((i * 2 * G + s) * 32 + lane) * 8);
 #pragma unroll
         for (int k = 0; k < 4; ++k) O[i][s][k] = 0.f;
       }
-      qz[i] = lds_u32(sbase + uint32_t(SM::kOffQz + (i * 32 + lane) * 4));
+      qz[i] = word_at(smem + SM::kOffQz + (i * 32 + lane) * 4);
 #pragma unroll
       for (int k = 0; k < 4; ++k) Z[i][k] = 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = i * 8 + 2 * t + k;
         ch[i][k] = reinterpret_cast<const float*>(smem + SM::kOffRow)[r];
-        m[i][k] = kUnseen;
+        mb[i][k] = kUnseen;
         l[i][k] = 0.f;
         const int tok = (row0 + r) / a.group;
         seen[i][k] = tok < n ? len - n + tok + 1 : 0;
       }
     }
     const int all_see = len - n + row0 / a.group + 1;  // keys that every row sees
-    // V's scales are taken times 2^-es, below 1; es grows with the largest scale seen (bound 0: none yet)
-    int es = 0;
-    uint32_t es_mul = 0x3c003c00u;  // 2^-es in both halves
-    float es_bound = 0.f;
+    int es = 0;                                        // V's scales have been at most 2^es
+    float most = kBase + kSlack;                       // weights stay at or below 2^most, most = base + slack - es
+    uint32_t over = 0x7fff7fffu - 0x3c003c00u;         // added to two scales' bits, sets bit 15 of one above 2^es
 
     for (int k = 0; k < here; ++k) {
       if (!mbar_wait(full(slot), lap, a.wait_ns)) timed_out = true;
-      const int key0 = (at.tile + k) * kKeys + warp * kKv4Block;
-      const int live = len - key0;  // keys of this block (any number; <= 0: none)
-      if (live > 0) {
-        const uint32_t blk = sbase + uint32_t(slot * SM::kStage + warp * B::kBytes);
+      const int key0 = (at.tile + k) * kKeys + warp * KB * kKv4Block;
+      if (key0 < len) {
+        const unsigned char* blk0 = smem + slot * SM::kStage + warp * KB * B::kBytes;
         // S^T = K Q^T
-        uint32_t wa[G], wb[G], ksa[G / 2], ksb[G / 2];
-        lds_words<G>(wa, blk + uint32_t(g * (DH / 2) + t * G * 4));
-        lds_words<G>(wb, blk + uint32_t((g + 8) * (DH / 2) + t * G * 4));
-        lds_words<G / 2>(ksa, blk + uint32_t(B::kKScale + g * G * 2));
-        lds_words<G / 2>(ksb, blk + uint32_t(B::kKScale + (g + 8) * G * 2));
-        const uint32_t kza = lds_u32(blk + uint32_t(B::kKZero + g * G * 2 + (t % (G / 2)) * 4));
-        const uint32_t kzb = lds_u32(blk + uint32_t(B::kKZero + (g + 8) * G * 2 + (t % (G / 2)) * 4));
-        float S[NT][4];
+        float S[KB][NT][4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          float z[4] = {0.f, 0.f, 0.f, 0.f};
-          mma8(z, kza, kzb, qz[i]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) S[i][q] = z[q] * 0x1p-24f;
-        }
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-          const uint32_t ua = wa[j] >> 8, ub = wb[j] >> 8;
-          const float sa = (j & 1) ? f16_hi(ksa[j / 2]) : f16_lo(ksa[j / 2]), sb = (j & 1) ? f16_hi(ksb[j / 2]) : f16_lo(ksb[j / 2]);
+        for (int kb = 0; kb < KB; ++kb) {
+          const unsigned char* blk = blk0 + kb * B::kBytes;
+          uint32_t wa[G], wb[G], ksa[G / 2], ksb[G / 2];
+          words_at<G>(wa, blk + g * (DH / 2) + t * G * 4);
+          words_at<G>(wb, blk + (g + 8) * (DH / 2) + t * G * 4);
+          words_at<G / 2>(ksa, blk + B::kKScale + g * G * 2);
+          words_at<G / 2>(ksb, blk + B::kKScale + (g + 8) * G * 2);
+          const uint32_t kza = word_at(blk + B::kKZero + g * G * 2 + (t % (G / 2)) * 4);
+          const uint32_t kzb = word_at(blk + B::kKZero + (g + 8) * G * 2 + (t % (G / 2)) * 4);
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16(d, wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, wa[j] & 0x00f000f0u, wb[j] & 0x00f000f0u, qf[i][2 * j][0], qf[i][2 * j][1]);
-            mma16(d, ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u, qf[i][2 * j + 1][0], qf[i][2 * j + 1][1]);
-            S[i][0] = fmaf(sa, d[0], S[i][0]);
-            S[i][1] = fmaf(sa, d[1], S[i][1]);
-            S[i][2] = fmaf(sb, d[2], S[i][2]);
-            S[i][3] = fmaf(sb, d[3], S[i][3]);
+            float z[4];
+            mma8_first(z, kza, kzb, qz[i]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) S[kb][i][q] = z[q] * 0x1p-24f;
+          }
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const uint32_t ua = wa[j] >> 8, ub = wb[j] >> 8;
+            const float sa = (j & 1) ? f16_hi(ksa[j / 2]) : f16_lo(ksa[j / 2]), sb = (j & 1) ? f16_hi(ksb[j / 2]) : f16_lo(ksb[j / 2]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              float d[4];
+              mma16_first(d, wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, wa[j] & 0x00f000f0u, wb[j] & 0x00f000f0u, qf[i][2 * j][0], qf[i][2 * j][1]);
+              mma16(d, ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u, qf[i][2 * j + 1][0], qf[i][2 * j + 1][1]);
+              S[kb][i][0] = fmaf(sa, d[0], S[kb][i][0]);
+              S[kb][i][1] = fmaf(sa, d[1], S[kb][i][1]);
+              S[kb][i][2] = fmaf(sb, d[2], S[kb][i][2]);
+              S[kb][i][3] = fmaf(sb, d[3], S[kb][i][3]);
+            }
           }
         }
-        if (key0 + kKv4Block > all_see) {  // some row does not see all of the block
+        const bool tail = key0 + KB * kKv4Block > all_see;  // some row does not see all of these keys
+        if (tail) {
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (key0 + kb * kKv4Block + g + (q & 2) * 4 >= seen[i][q & 1]) S[kb][i][q] = -INFINITY;
+        }
+        // a vote: is a weight, or a scale of V, above its bound?  (lane (g, t) looks at the scales of one word)
+        bool move = false;
+        uint32_t vw[KB];
+        float p[KB][NT][4], ptop = -INFINITY;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const int f = (g / G) & 1, j = g % G;
+          vw[kb] = word_at(blk0 + kb * B::kBytes + B::kVScale + ((4 * f + t) * G + j) * 4);
+          move |= ((vw[kb] + over) & 0x80008000u) != 0u;
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (key0 + g + (q & 2) * 4 >= seen[i][q & 1]) S[i][q] = -INFINITY;
+            for (int q = 0; q < 4; q += 2) {
+              p[kb][i][q] = fmaf(S[kb][i][q], ch[i][0], mb[i][0]);
+              p[kb][i][q + 1] = fmaf(S[kb][i][q + 1], ch[i][1], mb[i][1]);
+              ptop = fmaxf(ptop, fmaxf(p[kb][i][q], p[kb][i][q + 1]));
+            }
         }
-        // V's scales and zeros; a slot that holds no token counts with zero
-        uint32_t vs[2][G], vz[2];
+        if (__any_sync(kFull, move || ptop > most)) {  // a new maximum, or larger scales: rescale what is summed so far
+          float vtop = 0.f;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          lds_words<G>(vs[f], blk + uint32_t(B::kVScale + (4 * f + t) * G * 4));
-          vz[f] = g < G ? lds_u32(blk + uint32_t(B::kVZero + ((4 * f + t) * G + g) * 4)) : 0u;
-        }
-        if (live < kKv4Block) {
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const uint32_t keep = (8 * f + 2 * t < live ? 0xffffu : 0u) | (8 * f + 2 * t + 1 < live ? 0xffff0000u : 0u);
-            vz[f] &= keep;
-#pragma unroll
-            for (int j = 0; j < G; ++j) vs[f][j] &= keep;
+          for (int kb = 0; kb < KB; ++kb) {
+            const int at2 = key0 + kb * kKv4Block + 8 * ((g / G) & 1) + 2 * t;  // slots that hold no token do not count
+            if (at2 < len) vtop = fmaxf(vtop, f16_lo(vw[kb]));
+            if (at2 + 1 < len) vtop = fmaxf(vtop, f16_hi(vw[kb]));
           }
-        }
-        uint32_t top = hmax2(vs[0][0], vs[1][0]);
-#pragma unroll
-        for (int j = 1; j < G; ++j) top = hmax2(top, hmax2(vs[0][j], vs[1][j]));
-        const float vtop = fmaxf(f16_lo(top), f16_hi(top));
-        bool move = vtop > es_bound;
-        float p[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            p[i][q] = fmaf(S[i][q], ch[i][q & 1], kBase - m[i][q & 1]);
-            move |= p[i][q] > kBase + kSlack;
-          }
-        if (__any_sync(kFull, move)) {  // a new maximum, or larger scales: rescale what is summed so far
-          const uint32_t vbits = __reduce_max_sync(kFull, __float_as_uint(fmaxf(vtop, 0.f)));
-          float fix = 1.f;
-          if (__uint_as_float(vbits) > es_bound) {
-            int e = int(vbits >> 23) - 127 + 1;  // 2^e > the largest scale
-            e = e < -14 ? -14 : e > 16 ? 16 : e;
-            fix = es_bound > 0.f ? pow2(es - e) : 1.f;
-            es = e;
-            es_bound = pow2(e);
-            es_mul = pack_f16x2(pow2(-e), pow2(-e));
-          }
+          const uint32_t vb = __reduce_max_sync(kFull, __float_as_uint(vtop));
+          int e = int(vb >> 23) - 127 + ((vb & 0x7fffffu) ? 1 : 0);  // the smallest power of two not below
+          e = e < es ? es : e > 16 ? 16 : e;
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             float al[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              float mx = fmaxf(S[i][q], S[i][q + 2]) * ch[i][q];
+              float mx = fmaxf(S[0][i][q], S[0][i][q + 2]);
+#pragma unroll
+              for (int kb = 1; kb < KB; ++kb) mx = fmaxf(mx, fmaxf(S[kb][i][q], S[kb][i][q + 2]));
+              mx *= ch[i][q];
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-              const float mn = mx > m[i][q] ? mx : m[i][q];
-              al[q] = ex2(m[i][q] - mn);
-              m[i][q] = mn;
+              const float m = fmaxf(kBase - float(es) - mb[i][q], mx), to = kBase - float(e) - m;
+              al[q] = ex2(to - mb[i][q]);
+              mb[i][q] = to;
               l[i][q] *= al[q];
               Z[i][q] *= al[q];
-              Z[i][q + 2] *= al[q];
             }
 #pragma unroll
             for (int s = 0; s < 2 * G; ++s)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) O[i][s][q] *= al[q & 1] * fix;
+              for (int q = 0; q < 4; ++q) O[i][s][q] *= al[q & 1];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) p[i][q] = fmaf(S[i][q], ch[i][q & 1], kBase - m[i][q & 1]);
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) p[kb][i][q] = fmaf(S[kb][i][q], ch[i][q & 1], mb[i][q & 1]);
           }
+          es = e;
+          most = kBase + kSlack - float(e);
+          over = 0x7fff7fffu - 0x3c003c00u - uint32_t(e) * 0x04000400u;
         }
-        uint32_t pb[NT][2];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            p[i][q] = ex2(p[i][q]);
-            l[i][q & 1] += p[i][q];
-          }
-          pb[i][0] = transposed(pack_f16x2(p[i][0], p[i][1]));
-          pb[i][1] = transposed(pack_f16x2(p[i][2], p[i][3]));
-        }
-        // O^T += V^T P^T
-        uint32_t va[G], vb[G];
-        lds_words<G>(va, blk + uint32_t(B::kV + (g * 4 + t) * G * 4));
-        lds_words<G>(vb, blk + uint32_t(B::kV + ((8 + g) * 4 + t) * G * 4));
-#pragma unroll
-        for (int i = 0; i < NT; ++i) mma16(Z[i], vz[0], 0u, vz[1], 0u, pb[i][0], pb[i][1]);
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-          const uint32_t s0 = hmul2(vs[0][j], es_mul), s1 = hmul2(vs[1][j], es_mul);
-          const uint32_t ua = va[j] >> 8, ub = vb[j] >> 8;
+        for (int kb = 0; kb < KB; ++kb) {
+          const unsigned char* blk = blk0 + kb * B::kBytes;
+          uint32_t pb[NT][2];
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            const uint32_t p0 = hmul2(pb[i][0], s0), p1 = hmul2(pb[i][1], s1);
-            mma16(O[i][2 * j], va[j] & 0x000f000fu, va[j] & 0x00f000f0u, vb[j] & 0x000f000fu, vb[j] & 0x00f000f0u, p0, p1);
-            mma16(O[i][2 * j + 1], ua & 0x000f000fu, ua & 0x00f000f0u, ub & 0x000f000fu, ub & 0x00f000f0u, p0, p1);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              p[kb][i][q] = ex2(p[kb][i][q]);
+              l[i][q & 1] += p[kb][i][q];
+            }
+            pb[i][0] = transposed(pack_f16x2(p[kb][i][0], p[kb][i][1]));
+            pb[i][1] = transposed(pack_f16x2(p[kb][i][2], p[kb][i][3]));
+          }
+          // O^T += V^T P^T; Z^T: rows g < G for the zeros, row G for ones
+          uint32_t vs[2][G], vz[2], va[G], vb[G];
+          words_at<G>(va, blk + B::kV + (g * 4 + t) * G * 4);
+          words_at<G>(vb, blk + B::kV + ((8 + g) * 4 + t) * G * 4);
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            words_at<G>(vs[f], blk + B::kVScale + (4 * f + t) * G * 4);
+            vz[f] = word_at(blk + B::kVZero + ((4 * f + t) * G + g % G) * 4);
+            if (g >= G) vz[f] = g == G ? 0x3c003c00u : 0u;
+          }
+          if (tail) {  // a slot that holds no token counts with zero
+            const int live = len - key0 - kb * kKv4Block;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const uint32_t keep = (8 * f + 2 * t < live ? 0xffffu : 0u) | (8 * f + 2 * t + 1 < live ? 0xffff0000u : 0u);
+              vz[f] &= keep;
+#pragma unroll
+              for (int j = 0; j < G; ++j) vs[f][j] &= keep;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i) mma16(Z[i], vz[0], 0u, vz[1], 0u, pb[i][0], pb[i][1]);
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const uint32_t ua = va[j] >> 8, ub = vb[j] >> 8;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              const uint32_t p0 = hmul2(pb[i][0], vs[0][j]), p1 = hmul2(pb[i][1], vs[1][j]);
+              mma16(O[i][2 * j], va[j] & 0x000f000fu, va[j] & 0x00f000f0u, vb[j] & 0x000f000fu, vb[j] & 0x00f000f0u, p0, p1);
+              mma16(O[i][2 * j + 1], ua & 0x000f000fu, ua & 0x00f000f0u, ub & 0x000f000fu, ub & 0x00f000f0u, p0, p1);
+            }
           }
         }
       }
@@ -551,19 +571,16 @@ __global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
     // ---- the four warps' states merged, then written: the rows themselves, or a part of them ----
     const bool whole = at.tile == 0 && here == at.w.tiles;
     const int part = 2 * int(blockIdx.x) + (first ? 0 : 1);
-    float* ml = reinterpret_cast<float*>(smem + SM::kOffMl);
+    float4* ml = reinterpret_cast<float4*>(smem + SM::kOffMl);
     float* ob = reinterpret_cast<float*>(smem + SM::kOffO);
-    const float unit = pow2(es + 20);  // O's unit for odd rows of a fragment; 16 times that for even ones
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[i][q] += __shfl_xor_sync(kFull, l[i][q], o);
-        if (g == 0) {
-          ml[(warp * R + i * 8 + 2 * t + q) * 2] = m[i][q];
-          ml[(warp * R + i * 8 + 2 * t + q) * 2 + 1] = l[i][q];
-        }
+        const float ones = __shfl_sync(kFull, Z[i][q], G * 4 + t);
+        if (g == 0) ml[warp * R + i * 8 + 2 * t + q] = make_float4(mb[i][q], l[i][q], ones, 0.f);
       }
       if (i > 0) named_barrier_sync(1, kWarps * 32);  // the buffer has been read
 #pragma unroll
@@ -573,8 +590,8 @@ __global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
         for (int h = 0; h < 2; ++h) {
           const float (&o)[4] = O[i][2 * j + h];
           float* d0 = ob + (warp * 8 + 2 * t) * SM::kPad + 32 * j + 4 * g + 2 * h;
-          *reinterpret_cast<float2*>(d0) = make_float2(fmaf(o[0], unit * 16.f, z0), fmaf(o[2], unit, z0));
-          *reinterpret_cast<float2*>(d0 + SM::kPad) = make_float2(fmaf(o[1], unit * 16.f, z1), fmaf(o[3], unit, z1));
+          *reinterpret_cast<float2*>(d0) = make_float2(fmaf(o[0], 0x1p24f, z0), fmaf(o[2], 0x1p20f, z0));
+          *reinterpret_cast<float2*>(d0 + SM::kPad) = make_float2(fmaf(o[1], 0x1p24f, z1), fmaf(o[3], 0x1p20f, z1));
         }
       }
       named_barrier_sync(1, kWarps * 32);
@@ -582,54 +599,49 @@ __global__ void __launch_bounds__(kThreads) k_attention_kv4(AttnArgs a) {
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         const int r = warp + 4 * rr, row = row0 + i * 8 + r;
-        float mw[kWarps], M = kUnseen, L = 0.f;
+        float4 s[kWarps], sum = make_float4(kUnseen, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          mw[w] = ml[(w * R + i * 8 + r) * 2];
-          M = fmaxf(M, mw[w]);
-        }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          mw[w] = ex2(mw[w] - M);
-          L = fmaf(mw[w], ml[(w * R + i * 8 + r) * 2 + 1], L);
+          s[w] = ml[w * R + i * 8 + r];
+          sum.x = fminf(sum.x, s[w].x);
         }
         constexpr int E = DH / 32;
         float x[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          x[e] = 0.f;
+        for (int e = 0; e < E; ++e) x[e] = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) x[e] = fmaf(mw[w], ob[(w * 8 + r) * SM::kPad + lane * E + e], x[e]);
+        for (int w = 0; w < kWarps; ++w) {
+          const float fix = ex2(sum.x - s[w].x);
+          sum.y = fmaf(fix, s[w].y, sum.y);
+          sum.z = fmaf(fix, s[w].z, sum.z);
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = fmaf(fix, ob[(w * 8 + r) * SM::kPad + lane * E + e], x[e]);
         }
         if (row < n * a.group) {
           if (whole) {
             const int tok = row / a.group, hd = at.h * a.group + row - tok * a.group;
-            const int64_t out = int64_t(at.w.s.start + tok) * a.q_heads + hd;
-            write_row<H, DH>(a, out, lane, x, M, L);
+            write_row<H, DH>(a, int64_t(at.w.s.start + tok) * a.q_heads + hd, lane, x, sum);
           } else {
             float* po = a.part_o + (int64_t(part) * R + i * 8 + r) * DH + lane * E;
 #pragma unroll
             for (int e = 0; e < E; ++e) po[e] = x[e];
-            if (lane == 0) {
-              a.part_ml[(int64_t(part) * R + i * 8 + r) * 2] = M;
-              a.part_ml[(int64_t(part) * R + i * 8 + r) * 2 + 1] = L;
-            }
+            if (lane == 0) a.part_l[int64_t(part) * R + i * 8 + r] = sum;
           }
         }
       }
     }
     first = false;
     left -= here;
-    if (left > 0) next_item(at, c, a.group, R);
+    if (left > 0) next_item<R, kKeys>(at, c, a.group);
     named_barrier_sync(1, kWarps * 32);  // Q and the merge buffers are free
   }
   if (timed_out && lane == 0) atomicOr(c.status, kStatusTimeout);
 }
 
 // One CTA per query row: merges the parts of rows whose keys were spread over several runs.
-template <bool H, int DH>
-__global__ void __launch_bounds__(128) k_attention_kv4_merge(AttnArgs a, int R) {
-  constexpr int E = DH / 32;
+template <bool H, int DH, int NT, int KB>
+__global__ void __launch_bounds__(128) k_attention_kv4_merge(AttnArgs a) {
+  constexpr int E = DH / 32, R = 8 * NT, kKeys = Smem<DH, NT, KB>::kKeys;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Kv4View& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -638,7 +650,7 @@ __global__ void __launch_bounds__(128) k_attention_kv4_merge(AttnArgs a, int R) 
   const int b = kv4_seq_of(c, i);
   if (b < 0) return;
   bool bad = false;
-  const SeqWork w = seq_work(c, b, a.group, R, bad);
+  const SeqWork w = seq_work<R, kKeys>(c, b, a.group, bad);
   if (i < w.s.start || i >= w.s.start + w.s.n) return;
   const int h = hq / a.group, rr = int(i - w.s.start) * a.group + hq - h * a.group, rb = rr / R, r = rr - rb * R;
   const Runs runs = runs_of(a.prefix[c.batch], a.runs);
@@ -646,52 +658,44 @@ __global__ void __launch_bounds__(128) k_attention_kv4_merge(AttnArgs a, int R) 
   const int c0 = runs.of(t0), c1 = runs.of(t0 + w.tiles - 1);
   if (c0 == c1) return;  // one run held all of its keys and wrote the row
   const int late = t0 > runs.first(c0) ? 1 : 0;  // the part in run c0 is not that run's first
-  float M = kUnseen, L = 0.f, x[E];
+  float4 s = make_float4(kUnseen, 0.f, 0.f, 0.f);
+  float x[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] = 0.f;
+  auto add = [&](float4 v, const float* o) {
+    const float mb = fminf(s.x, v.x), f0 = ex2(mb - s.x), f1 = ex2(mb - v.x);
+    s = make_float4(mb, fmaf(s.y, f0, v.y * f1), fmaf(s.z, f0, v.z * f1), 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = fmaf(x[e], f0, o[lane * E + e] * f1);
+  };
+#pragma unroll 4
   for (int k = c0 + warp; k <= c1; k += 4) {
     const int64_t part = int64_t(2 * k + (k == c0 ? late : 0)) * R + r;
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + part * 2);
-    const float mn = fmaxf(M, ml.x), s0 = ex2(M - mn), s1 = ex2(ml.x - mn);
-    M = mn;
-    L = fmaf(L, s0, ml.y * s1);
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = fmaf(x[e], s0, a.part_o[part * DH + lane * E + e] * s1);
+    add(a.part_l[part], a.part_o + part * DH);
   }
-  __shared__ float sm[4][2], so[4][DH];
-  if (lane == 0) {
-    sm[warp][0] = M;
-    sm[warp][1] = L;
-  }
+  __shared__ float4 sm[4];
+  __shared__ float so[4][DH];
+  if (lane == 0) sm[warp] = s;
 #pragma unroll
   for (int e = 0; e < E; ++e) so[warp][lane * E + e] = x[e];
   __syncthreads();
   if (warp) return;
-  M = fmaxf(fmaxf(sm[0][0], sm[1][0]), fmaxf(sm[2][0], sm[3][0]));
-  L = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = 0.f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float s = ex2(sm[k][0] - M);
-    L = fmaf(sm[k][1], s, L);
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = fmaf(so[k][lane * E + e], s, x[e]);
-  }
-  write_row<H, DH>(a, i * a.q_heads + hq, lane, x, M, L);
+  for (int k = 1; k < 4; ++k) add(sm[k], so[k]);
+  write_row<H, DH>(a, i * a.q_heads + hq, lane, x, s);
 }
 
 struct Plan {
-  using Main = void (*)(AttnArgs);
-  using Merge = void (*)(AttnArgs, int);
-  Main main;
-  Merge merge;
+  using Kern = void (*)(AttnArgs);
+  Kern main, merge;
   int smem, rows;
 };
+template <bool H, int DH, int NT, int KB>
+Plan plan_as() {
+  return Plan{k_attention_kv4<H, DH, NT, KB>, k_attention_kv4_merge<H, DH, NT, KB>, Smem<DH, NT, KB>::kBytes, 8 * NT};
+}
 template <bool H, int DH>
 Plan plan_of(bool wide) {
-  return wide ? Plan{k_attention_kv4<H, DH, 2>, k_attention_kv4_merge<H, DH>, Smem<DH, 2>::kBytes, 16}
-              : Plan{k_attention_kv4<H, DH, 1>, k_attention_kv4_merge<H, DH>, Smem<DH, 1>::kBytes, 8};
+  return wide ? plan_as<H, DH, 2, 1>() : plan_as<H, DH, 1, 2>();
 }
 // Tiles of 8 query rows, or of 16 where a sequence has more rows to a key/value head than 8 on average.
 Plan plan_for(int64_t batch, int64_t tokens, int q_heads, int heads, int d, int dtype) {
@@ -727,7 +731,7 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 size_t attention_kv4_scratch(int64_t batch, int64_t tokens, int q_heads, int heads, int d, const DeviceInfo& dev) {
   const Plan p = plan_for(batch, tokens, q_heads, heads, d, 1);
   const size_t parts = size_t(2) * kMaxCtasPerSm * dev.sm_count * p.rows;
-  return up256(size_t(batch + 1) * 8) + up256(parts * 8) + parts * size_t(d) * 4;
+  return up256(size_t(batch + 1) * 8) + up256(parts * 16) + parts * size_t(d) * 4;
 }
 
 cudaError_t launch_attention_kv4(const Kv4View& c, const Kv4Rows& q, void* o, float* lse, int q_heads, float scale, int dtype,
@@ -750,8 +754,8 @@ cudaError_t launch_attention_kv4(const Kv4View& c, const Kv4Rows& q, void* o, fl
   const size_t parts = size_t(2) * a.runs * p.rows;
   a.prefix = reinterpret_cast<int64_t*>(w);
   w += up256(size_t(c.batch + 1) * 8);
-  a.part_ml = reinterpret_cast<float*>(w);
-  w += up256(parts * 8);
+  a.part_l = reinterpret_cast<float4*>(w);
+  w += up256(parts * 16);
   a.part_o = reinterpret_cast<float*>(w);
   p.main<<<a.runs, kThreads, p.smem, stream>>>(a);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
@@ -765,7 +769,7 @@ cudaError_t launch_attention_kv4(const Kv4View& c, const Kv4Rows& q, void* o, fl
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, p.merge, a, p.rows);
+  return cudaLaunchKernelEx(&cfg, p.merge, a);
 }
 
 }  // namespace rwo
