@@ -214,36 +214,38 @@ __device__ __forceinline__ RunSeq run_seq(const Kv4View& c, int b, bool& bad) {
   return r;
 }
 
-// Calls f(sequence, block of it, head or other sub-task) for the units of this warp: `subs` a block.
+// Calls f(sequence, block of it, sub-task) for the units of this warp, `subs` a block; this CTA is number `part` of `parts`.
 template <class F>
-__device__ __forceinline__ void for_units(const Kv4View& c, int subs, F f) {
-  __shared__ int64_t scan[kCacheThreads / 32];
-  __shared__ int64_t where[2];  // sequence, first unit of it
+__device__ __forceinline__ void for_units(const Kv4View& c, int subs, int part, int parts, F f) {
+  __shared__ int scan[kCacheThreads / 32];
+  __shared__ int where[2];  // sequence, first unit of it
+  __shared__ int taken;         // units of this CTA's part that warps have taken: they take turns, as units differ in work
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (c.batch + kCacheThreads - 1) / kCacheThreads, b0 = min(tid * per, c.batch), b1 = min(b0 + per, c.batch);
   bool bad = false;
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += int64_t(run_seq(c, b, bad).blocks) * subs;
-  if (bad && blockIdx.x == 0) kv4_bad(c);
-  int64_t upto = mine;
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += run_seq(c, b, bad).blocks * subs;
+  if (bad && part == 0) kv4_bad(c);
+  int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(kFull, upto, o);
+    const int x = __shfl_up_sync(kFull, upto, o);
     if (lane >= o) upto += x;
   }
   if (lane == 31) scan[warp] = upto;
+  if (tid == 0) taken = kCacheThreads / 32;
   __syncthreads();
-  int64_t total = 0, before = upto - mine;
+  int total = 0, before = upto - mine;
   for (int w = 0; w < kCacheThreads / 32; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  const int64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+  const int u0 = int(int64_t(total) * part / parts), u1 = int(int64_t(total) * (part + 1) / parts);
   if (u0 >= u1) return;
   if (u0 >= before && u0 < before + mine) {
-    int64_t at = before;
+    int at = before;
     for (int b = b0; b < b1; ++b) {
-      const int64_t n = int64_t(run_seq(c, b, bad).blocks) * subs;
+      const int n = run_seq(c, b, bad).blocks * subs;
       if (u0 < at + n) {
         where[0] = b;
         where[1] = at;
@@ -253,199 +255,269 @@ __device__ __forceinline__ void for_units(const Kv4View& c, int subs, F f) {
     }
   }
   __syncthreads();
-  int b = int(where[0]);
-  int64_t at = where[1];
+  int b = where[0];
+  int at = where[1];
   RunSeq r = run_seq(c, b, bad);
-  for (int64_t u = u0 + warp; u < u1; u += kCacheThreads / 32) {
-    while (u >= at + int64_t(r.blocks) * subs) {
-      at += int64_t(r.blocks) * subs;
+  for (int u = u0 + warp; u < u1;) {
+    while (u >= at + r.blocks * subs) {
+      at += r.blocks * subs;
       r = run_seq(c, ++b, bad);
     }
-    const int x = int((u - at) / subs);
-    f(b, r, r.first + x, int((u - at) - int64_t(x) * subs));
+    const int x = (u - at) / subs;
+    f(b, r, r.first + x, u - at - x * subs);
+    int next = 0;
+    if (lane == 0) next = atomicAdd(&taken, 1);
+    u = u0 + __shfl_sync(kFull, next, 0);
   }
 }
 
-template <class D>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&f)[8]) {
-  D::unpack(*reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p) + at * 2), f);
-}
 template <class D>
 __device__ __forceinline__ void store8(void* p, int64_t at, const float (&f)[8]) {
   *reinterpret_cast<uint4*>(static_cast<unsigned char*>(p) + at * 2) = D::pack(f);
 }
 
-// Angles of elements e .. e + 7 at a position: y = x c + o s with o the partner (its sign in s).
+// a b + c d, products and sum each rounded.  (The additions are scalar: a packed product and a packed addition after it
+// come out of the compiler as one fused operation, .rn or not, which rounds once.)
+__device__ __forceinline__ float2 sum_of_products(float2 a, float2 b, float2 c, float2 d) {
+  const float2 x = __fmul2_rn(a, b), y = __fmul2_rn(c, d);
+  return make_float2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
+
+// Angles of elements e .. e + 7 at a position, as pairs (neighbours: one angle a pair, in x and y of c alone).
 struct Turn {
-  float c[8], s[8];
+  float2 c[4], s[4];
 };
 __device__ __forceinline__ Turn turn_at(const float* cs, int rot, int e, bool neighbours) {
   Turn t;
   const int half = rot >> 1;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    t.c[i] = 1.f;
-    t.s[i] = 0.f;
-  }
-  if (e >= rot) return t;
   if (neighbours) {
     const float4 c = __ldg(reinterpret_cast<const float4*>(cs + (e >> 1))), s = __ldg(reinterpret_cast<const float4*>(cs + half + (e >> 1)));
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      t.c[i] = cc[i >> 1];
-      t.s[i] = (i & 1) ? ss[i >> 1] : -ss[i >> 1];
-    }
+    t.c[0] = make_float2(c.x, c.x);
+    t.c[1] = make_float2(c.y, c.y);
+    t.c[2] = make_float2(c.z, c.z);
+    t.c[3] = make_float2(c.w, c.w);
+    t.s[0] = make_float2(s.x, s.x);
+    t.s[1] = make_float2(s.y, s.y);
+    t.s[2] = make_float2(s.z, s.z);
+    t.s[3] = make_float2(s.w, s.w);
     return t;
   }
+  const float* p = cs + (e < half ? e : e - half);
 #pragma unroll
-  for (int i = 0; i < 8; i += 4) {  // four elements lie on one side of rot / 2, a multiple of 4
-    const bool first = e + i < half;
-    const int k = first ? e + i : e + i - half;
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + k)), s = __ldg(reinterpret_cast<const float4*>(cs + half + k));
-    t.c[i] = c.x;
-    t.c[i + 1] = c.y;
-    t.c[i + 2] = c.z;
-    t.c[i + 3] = c.w;
-    t.s[i] = first ? -s.x : s.x;
-    t.s[i + 1] = first ? -s.y : s.y;
-    t.s[i + 2] = first ? -s.z : s.z;
-    t.s[i + 3] = first ? -s.w : s.w;
+  for (int i = 0; i < 4; i += 2) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(p + 2 * i)), s = __ldg(reinterpret_cast<const float4*>(p + half + 2 * i));
+    t.c[i] = make_float2(c.x, c.y);
+    t.c[i + 1] = make_float2(c.z, c.w);
+    t.s[i] = make_float2(s.x, s.y);
+    t.s[i + 1] = make_float2(s.z, s.w);
   }
   return t;
 }
-// The partners of elements e .. e + 7 of the row at `at`, x being the elements themselves.
+
+// Eight elements (packed in x) of a row rotated: y = x cos + o sin with o the partner, negated for the first of a pair.
+// Without neighbours the partners are the elements of lane `from` (rot / 2 is a multiple of 8 here); flip: their signs'
+// bits where they are second.  All lanes take part.
 template <class D>
-__device__ __forceinline__ void partners(const void* p, int64_t at, int e, int rot, bool neighbours, const float (&x)[8], float (&o)[8]) {
+__device__ __forceinline__ void turned(float2 (&f)[4], uint4 x, bool on, bool neighbours, int from, uint32_t flip, const Turn& t) {
+  uint4 w;
+  if (neighbours) {
+    w = make_uint4(__funnelshift_l(x.x, x.x, 16) ^ 0x8000u, __funnelshift_l(x.y, x.y, 16) ^ 0x8000u,
+                   __funnelshift_l(x.z, x.z, 16) ^ 0x8000u, __funnelshift_l(x.w, x.w, 16) ^ 0x8000u);
+  } else {
+    w = make_uint4(__shfl_sync(kFull, x.x, from) ^ flip, __shfl_sync(kFull, x.y, from) ^ flip, __shfl_sync(kFull, x.z, from) ^ flip,
+                   __shfl_sync(kFull, x.w, from) ^ flip);
+  }
+  D::unpack2(x, f);
+  if (on) {
+    float2 o[4];
+    D::unpack2(w, o);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = neighbours ? x[i ^ 1] : 0.f;
-  if (neighbours || e >= rot) return;
-  const int half = rot >> 1;
-#pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    const float4 y = load4<D>(p, at + (e + i < half ? e + i + half : e + i - half));
-    o[i] = y.x;
-    o[i + 1] = y.y;
-    o[i + 2] = y.z;
-    o[i + 3] = y.w;
+    for (int i = 0; i < 4; ++i) f[i] = sum_of_products(f[i], t.c[i], o[i], t.s[i]);
   }
 }
-__device__ __forceinline__ void turned(float (&x)[8], const float (&o)[8], const Turn& t, bool rotated) {
-  if (!rotated) return;
+
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// c << 8 | b << 4 | a with a and b limited to 0 .. 15.
+__device__ __forceinline__ uint32_t pack_codes(uint32_t c, int b, int a) {
+  uint32_t d;
+  asm("cvt.pack.sat.u4.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(b), "r"(a), "r"(c));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Codes of eight elements of a group that four lanes hold (nibble i: element i), its scale and zero.
+__device__ __forceinline__ uint32_t quantised8(float2 (&x)[4], __half& sh, __half& zh) {
+  float lo = fminf(min3(x[0].x, x[0].y, x[1].x), min3(x[1].y, x[2].x, x[2].y)), hi = fmaxf(max3(x[0].x, x[0].y, x[1].x), max3(x[1].y, x[2].x, x[2].y));
+  lo = min3(lo, x[3].x, x[3].y);
+  hi = max3(hi, x[3].x, x[3].y);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(o[i], t.s[i]));
+  for (int o = 2; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
+  }
+  if (lo < -65504.f || hi > 65504.f) {
+    lo = limited(lo);
+    hi = limited(hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(limited(x[i].x), limited(x[i].y));
+  }
+  zh = __float2half_rn(lo);
+  sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+  const float z = __half2float(zh), s = __half2float(sh);
+  if (!(s > 0.f)) return 0u;
+  // Adding 1.5 2^23 rounds a quotient to the nearest integer, ties to even, in the sum's low bits.  (A quotient lies in
+  // [0, 15] but for the roundings of z and s, which can take it no further than 2^18.)
+  constexpr float kRound = 12582912.f;
+  float i1;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i1) : "f"(s));
+  const float2 inv = both(i1);
+  uint32_t eight = 0;
+  float edge = 0.f;  // largest distance from the integer
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    const float2 u = __fmul2_rn(__fadd2_rn(x[i], both(-z)), inv);
+    const float2 r = __fadd2_rn(u, both(kRound)), c = __fadd2_rn(r, both(-kRound));
+    const float2 d = __fadd2_rn(u, make_float2(-c.x, -c.y));
+    edge = max3(edge, fabsf(d.x), fabsf(d.y));
+    eight = pack_codes(eight, __float_as_int(r.y) - 0x4b400000, __float_as_int(r.x) - 0x4b400000);
+  }
+  if (edge > 0.4999f) {  // next to a half-way point the division itself is needed (the quotients above are off by 2^-17 at most)
+    eight = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i)
+      eight = eight << 8 | code_of(x[i].y, z, s, i1) << 4 | code_of(x[i].x, z, s, i1);
+  }
+  return eight;
 }
 
-constexpr int kQHeads = 4;  // query heads of a unit
+constexpr int kAppendCtas = 4;  // resident on an SM: 80 registers a thread
+constexpr int kQHeads = 32;  // query heads of a warp: a token's angles are loaded once for them
 
+// CTAs that write the cache and CTAs that rotate queries take turns in the grid, so that the ones' arithmetic runs beside
+// the others' traffic.
 template <class D, int DH>
-__global__ void __launch_bounds__(kCacheThreads) k_kv4_append_runs(AppendArgs a) {
+__global__ void __launch_bounds__(kCacheThreads, kAppendCtas) k_kv4_append_runs(AppendArgs a, int kv_ctas) {
   using B = Kv4Block<DH>;
   constexpr int kLanes = DH / 8, kRows = 32 / kLanes;  // lanes a row; rows a warp moves at once
   const Kv4View& c = a.c;
   const int lane = threadIdx.x & 31, sub = lane / kLanes, e = (lane % kLanes) * 8;
-  const int j = e >> 5, t8 = (e & 31) >> 3;
   const int rot = a.cos_sin ? a.rot : 0;
-  const int q_units = (a.q_heads + kQHeads - 1) / kQHeads;
-  for_units(c, 2 * c.heads + q_units, [&](int b, const RunSeq& rs, int blk, int what) {
+  const bool neighbours = a.neighbours, second = e >= (rot >> 1);
+  const int partner = second ? lane - rot / 16 : lane + rot / 16;
+  const uint32_t flip = second ? 0u : 0x80008000u;
+  const int q_ctas = int(gridDim.x) - kv_ctas, mixed = 2 * min(q_ctas, kv_ctas), id = int(blockIdx.x);
+  const bool q_turn = id < mixed ? id & 1 : q_ctas > kv_ctas;
+  const int part = id < mixed ? id >> 1 : id - mixed / 2;
+  // Pointers are made once and stepped from row to row: 64-bit products for every row had been half of the instructions.
+  if (q_turn) {  // a warp takes kQHeads heads of a token, kRows at once
+    const int chunks = (a.q_heads + kQHeads - 1) / kQHeads;
+    const int64_t w = int64_t(part) * (kCacheThreads / 32) + (threadIdx.x >> 5), i = w / chunks;
+    if (i >= c.tokens) return;
+    const int b = kv4_seq_of(c, i);
+    if (b < 0) return;
+    bool bad = false;
+    const Kv4Seq s = kv4_seq(c, b, bad);
+    const int pos = s.len - (s.start + s.n - int(i));
+    if (bad || pos < 0 || (rot && pos >= a.positions)) return;  // (the CTAs that write the cache report these)
+    if (kv4_block_at(c, b, pos, B::kBytes) < 0) return;
+    Turn t;
+    if (e < rot) t = turn_at(a.cos_sin + int64_t(pos) * rot, rot, e, neighbours);
+    int h = int(w - i * chunks) * kQHeads + sub;
+    const int h1 = min(int(w - i * chunks) * kQHeads + kQHeads, a.q_heads);
+    const unsigned char* from = static_cast<const unsigned char*>(a.q.p) + (i * a.q.token + h * a.q.head + e) * 2;
+    unsigned char* to = const_cast<unsigned char*>(static_cast<const unsigned char*>(a.q_out.p)) + (i * a.q_out.token + h * a.q_out.head + e) * 2;
+    const int64_t step = a.q.head * (2 * kRows), step_out = a.q_out.head * (2 * kRows);
+    uint4 next = make_uint4(0u, 0u, 0u, 0u);
+    if (h < h1) next = *reinterpret_cast<const uint4*>(from);
+    while (__any_sync(kFull, h < h1)) {
+      uint4 x = next;
+      from += step;
+      if (h + kRows < h1) next = *reinterpret_cast<const uint4*>(from);  // on its way while this row is turned
+      if (rot) {
+        float2 f[4];
+        turned<D>(f, x, e < rot, neighbours, partner, flip, t);  // (shuffles: a row's lanes have its elements before one is written)
+        x = D::pack2(f);
+      }
+      if (h < h1) *reinterpret_cast<uint4*>(to) = x;
+      to += step_out;
+      h += kRows;
+    }
+    return;
+  }
+  const int kv_units = c.heads;
+  for_units(c, 2 * c.heads, part, kv_ctas, [&](int b, const RunSeq& rs, int blk, int what) {
     const int64_t at = kv4_block_at(c, b, blk * kKv4Block, B::kBytes);
     const int p0 = max(rs.s.len - rs.s.n, blk * kKv4Block), p1 = min(rs.s.len, (blk + 1) * kKv4Block);
-    if (at < 0 || (a.cos_sin && p1 > a.positions)) {
+    const int last = a.cos_sin && p1 > a.positions ? int(a.positions) : p1;  // positions [p0, last) are handled
+    if (at < 0 || last < p1) {
       if (lane == 0) kv4_bad(c);
       if (at < 0) return;
     }
-    const int last = a.cos_sin && p1 > a.positions ? int(a.positions) : p1;  // positions [p0, last) are handled
-    const int64_t row0 = int64_t(rs.s.start) + rs.s.n - rs.s.len;             // row of position 0
-    if (what >= 2 * c.heads) {  // queries: kRows heads at once, the angles loaded once a token
-      const int h0 = (what - 2 * c.heads) * kQHeads;
-      for (int p = p0; p < last; ++p) {
-        Turn t;
-        if (rot) t = turn_at(a.cos_sin + int64_t(p) * rot, rot, e, a.neighbours);
-        float x[kQHeads / kRows > 0 ? kQHeads / kRows : 1][8];
-#pragma unroll
-        for (int k = 0; k < kQHeads / kRows; ++k) {
-          const int h = h0 + k * kRows + sub;
-          if (h >= a.q_heads) continue;
-          const int64_t from = (row0 + p) * a.q.token + h * a.q.head;
-          float o[8];
-          load8<D>(a.q.p, from + e, x[k]);
-          if (rot) {
-            partners<D>(a.q.p, from, e, rot, a.neighbours, x[k], o);
-            turned(x[k], o, t, e < rot);
-          }
-        }
-        __syncwarp();  // q may be rotated in place: every lane has its partners
-#pragma unroll
-        for (int k = 0; k < kQHeads / kRows; ++k) {
-          const int h = h0 + k * kRows + sub;
-          if (h < a.q_heads) store8<D>(const_cast<void*>(a.q_out.p), (row0 + p) * a.q_out.token + h * a.q_out.head + e, x[k]);
-        }
-      }
-      return;
-    }
-    const bool is_v = what >= c.heads;
+    const int64_t row0 = int64_t(rs.s.start) + rs.s.n - rs.s.len;  // row of position 0
+    const bool is_v = what >= kv_units;
     const int h = is_v ? what - c.heads : what;
     const Kv4Rows& src = is_v ? a.v : a.k;
+    const int turn = is_v ? 0 : rot, j = e >> 5, t8 = (e & 31) >> 3;
     unsigned char* out = c.data + at + int64_t(h) * c.page_blocks * B::kBytes;
-#pragma unroll 2
-    for (int r0 = 0; r0 < kKv4Block; r0 += kRows) {  // token r of the block
-      const int r = r0 + sub, p = blk * kKv4Block + r;
+    const int first = blk * kKv4Block + sub;  // this lane's first position
+    const unsigned char* from = static_cast<const unsigned char*>(src.p) + ((row0 + first) * src.token + h * src.head + e) * 2;
+    const float* cs = a.cos_sin + int64_t(first) * rot;
+    uint4 next = make_uint4(0u, 0u, 0u, 0u);
+    if (first >= p0 && first < last) next = *reinterpret_cast<const uint4*>(from);
+#pragma unroll 1
+    for (int r = sub; r < kKv4Block; r += kRows) {  // kRows tokens of the block
+      const int p = blk * kKv4Block + r;
       const bool on = p >= p0 && p < last;
-      if (!__any_sync(kFull, on)) continue;
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (on) {
-        const int64_t from = (row0 + p) * src.token + h * src.head;
-        load8<D>(src.p, from + e, x);
-        if (!is_v && e < rot) {
-          float o[8];
-          partners<D>(src.p, from, e, rot, a.neighbours, x, o);
-          turned(x, o, turn_at(a.cos_sin + int64_t(p) * rot, rot, e, a.neighbours), true);
+      const uint4 x = next;
+      from += src.token * (2 * kRows);
+      if (r + kRows < kKv4Block && p + kRows >= p0 && p + kRows < last) next = *reinterpret_cast<const uint4*>(from);  // on its way meanwhile
+      if (__any_sync(kFull, on)) {
+        float2 f[4];
+        if (turn) {
+          Turn t;
+          if (on && e < turn) t = turn_at(cs, rot, e, neighbours);
+          turned<D>(f, x, on && e < turn, neighbours, partner, flip, t);
+        } else {
+          D::unpack2(x, f);
         }
-      }
-      float lo = 65504.f, hi = -65504.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = limited(x[i]);
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-      }
-#pragma unroll
-      for (int o = 2; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-      }
-      const __half zh = __float2half_rn(lo), sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-      const float z = __half2float(zh), s = __half2float(sh);
-      uint32_t eight = 0;
-      if (s > 0.f) {
-        const float inv = __frcp_rn(s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) eight |= code_of(x[i], z, s, inv) << (4 * i);
-      }
-      if (!is_v) {
-        if (on) {
-          reinterpret_cast<uint32_t*>(out)[r * (DH / 8) + B::G * t8 + j] = eight;
-          if (t8 == 0) {
-            reinterpret_cast<__half*>(out + B::kKScale)[r * B::G + j] = sh;
-            reinterpret_cast<__half*>(out + B::kKZero)[r * B::G + j] = zh;
+        __half sh, zh;
+        const uint32_t eight = quantised8(f, sh, zh);
+        if (!is_v) {
+          if (on) {
+            reinterpret_cast<uint32_t*>(out)[r * (DH / 8) + B::G * t8 + j] = eight;
+            if (t8 == 0) {
+              reinterpret_cast<__half*>(out + B::kKScale)[r * B::G + j] = sh;
+              reinterpret_cast<__half*>(out + B::kKZero)[r * B::G + j] = zh;
+            }
+          }
+        } else {  // a word holds four elements of two tokens: the lanes of an even and an odd token make one each
+          const uint32_t other = __shfl_xor_sync(kFull, eight, kLanes);
+          const bool odd = r & 1;
+          const bool pair = __shfl_xor_sync(kFull, on ? 1 : 0, kLanes) && on;
+          const int fh = r >> 3, tt = (r & 7) >> 1;
+          uint32_t* w = reinterpret_cast<uint32_t*>(out + B::kV) + ((fh * 8 + 2 * t8) * 4 + tt) * B::G + j;  // g = 2 t8; g + 1 is 4 G further
+          if (pair) {
+            w[odd ? 4 * B::G : 0] = odd ? (other >> 16) | (eight & 0xffff0000u) : (eight & 0xffffu) | (other << 16);
+          } else if (on) {
+            reinterpret_cast<uint16_t*>(w)[odd] = uint16_t(eight);
+            reinterpret_cast<uint16_t*>(w + 4 * B::G)[odd] = uint16_t(eight >> 16);
+          }
+          if (on && t8 == 0) {
+            reinterpret_cast<__half*>(out + B::kVScale)[((r >> 1) * B::G + j) * 2 + odd] = sh;
+            reinterpret_cast<__half*>(out + B::kVZero)[((r >> 1) * B::G + j) * 2 + odd] = zh;
           }
         }
-      } else {  // a word holds four elements of two tokens: the lanes of an even and an odd token make one each
-        const uint32_t other = __shfl_xor_sync(kFull, eight, kLanes);
-        const bool odd = r & 1, both = __shfl_xor_sync(kFull, on ? 1 : 0, kLanes) && on;
-        const int f = r >> 3, t = (r & 7) >> 1;
-        uint32_t* w = reinterpret_cast<uint32_t*>(out + B::kV) + ((f * 8 + 2 * t8) * 4 + t) * B::G + j;  // g = 2 t8; g + 1 is 4 G further
-        if (both) {
-          w[odd ? 4 * B::G : 0] = odd ? (other >> 16) | (eight & 0xffff0000u) : (eight & 0xffffu) | (other << 16);
-        } else if (on) {
-          reinterpret_cast<uint16_t*>(w)[odd] = uint16_t(eight);
-          reinterpret_cast<uint16_t*>(w + 4 * B::G)[odd] = uint16_t(eight >> 16);
-        }
-        if (on && t8 == 0) {
-          reinterpret_cast<__half*>(out + B::kVScale)[((r >> 1) * B::G + j) * 2 + odd] = sh;
-          reinterpret_cast<__half*>(out + B::kVZero)[((r >> 1) * B::G + j) * 2 + odd] = zh;
-        }
       }
+      cs += kRows * rot;
     }
   });
 }
@@ -456,7 +528,7 @@ __global__ void __launch_bounds__(kCacheThreads) k_kv4_gather_runs(GatherArgs a)
   constexpr int G = B::G;
   const Kv4View& c = a.c;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  for_units(c, c.heads, [&](int b, const RunSeq& rs, int blk, int h) {
+  for_units(c, c.heads, int(blockIdx.x), int(gridDim.x), [&](int b, const RunSeq& rs, int blk, int h) {
     int64_t at = kv4_block_at(c, b, blk * kKv4Block, B::kBytes);
     if (at < 0) {
       if (lane == 0) kv4_bad(c);
@@ -507,9 +579,15 @@ int grid_for(int64_t warps, const DeviceInfo& dev) {
 }
 
 // Runs of at least 4 tokens a sequence on average go by blocks of 16, fewer by single rows.
-bool in_runs(const Kv4View& c) { return c.cu && c.tokens >= 4 * int64_t(c.batch); }
-int grid_for_runs(const Kv4View& c, int subs, const DeviceInfo& dev) {
-  return grid_for((c.tokens / kKv4Block + 2 * int64_t(c.batch)) * subs, dev);
+// Units are counted in 32 bits.
+int64_t run_units(const Kv4View& c, int subs) { return (c.tokens / kKv4Block + 2 * int64_t(c.batch)) * subs; }
+bool in_runs(const Kv4View& c, int subs) { return c.cu && c.tokens >= 4 * int64_t(c.batch) && run_units(c, subs) < (int64_t(1) << 31); }
+// There a lane's eight elements have their partners in one other lane: rot / 2 is a multiple of 8, or pairs are neighbours.
+bool whole_lanes(const float* cos_sin, int rot, bool neighbours) { return !cos_sin || neighbours || rot % 16 == 0; }
+// As many CTAs as are resident at once (`per_sm`), fewer where there is not a unit a warp.
+int grid_for_runs(const Kv4View& c, int subs, int per_sm, const DeviceInfo& dev) {
+  const int64_t few = (run_units(c, subs) + 7) / 8, most = int64_t(dev.sm_count) * per_sm;
+  return int(few < most ? few : most);
 }
 
 }  // namespace
@@ -518,13 +596,16 @@ cudaError_t launch_kv4_append(const Kv4View& c, const Kv4Rows& k, const Kv4Rows&
                               int q_heads, const float* cos_sin, int64_t positions, int rot, bool neighbours, int dtype,
                               cudaStream_t stream, const DeviceInfo& dev) {
   const AppendArgs a{c, k, v, q, q_out, cos_sin, positions, q_heads, rot, neighbours ? 1 : 0};
-  using Kern = void (*)(AppendArgs);
-  if (in_runs(c)) {
+  const int64_t q_ctas = (c.tokens * ((q_heads + kQHeads - 1) / kQHeads) + kCacheThreads / 32 - 1) / (kCacheThreads / 32);
+  if (in_runs(c, 2 * c.heads) && whole_lanes(cos_sin, rot, neighbours)) {
+    using Kern = void (*)(AppendArgs, int);
     const Kern kern = dtype == 2 ? (c.d == 64 ? (Kern)k_kv4_append_runs<F16, 64> : (Kern)k_kv4_append_runs<F16, 128>)
                                  : (c.d == 64 ? (Kern)k_kv4_append_runs<BF16, 64> : (Kern)k_kv4_append_runs<BF16, 128>);
-    kern<<<grid_for_runs(c, 2 * c.heads + (q_heads + kQHeads - 1) / kQHeads, dev), kCacheThreads, 0, stream>>>(a);
+    const int kv_ctas = grid_for_runs(c, 2 * c.heads, 3, dev);
+    kern<<<unsigned(kv_ctas + q_ctas), kCacheThreads, 0, stream>>>(a, kv_ctas);
     return cudaGetLastError();
   }
+  using Kern = void (*)(AppendArgs);
   const int per = c.d == 64 ? 2 : 1, rows = 2 * c.heads + q_heads;
   const int grid = grid_for(c.tokens * ((rows + per - 1) / per), dev);
   const Kern kern = dtype == 2 ? (c.d == 64 ? (Kern)k_kv4_append<F16, 64> : (Kern)k_kv4_append<F16, 128>)
@@ -537,10 +618,10 @@ cudaError_t launch_kv4_gather(const Kv4View& c, const Kv4Rows& k, const Kv4Rows&
                               const DeviceInfo& dev) {
   const GatherArgs a{c, k, v};
   using Kern = void (*)(GatherArgs);
-  if (in_runs(c)) {
+  if (in_runs(c, c.heads)) {
     const Kern kern = dtype == 2 ? (c.d == 64 ? (Kern)k_kv4_gather_runs<F16, 64> : (Kern)k_kv4_gather_runs<F16, 128>)
                                  : (c.d == 64 ? (Kern)k_kv4_gather_runs<BF16, 64> : (Kern)k_kv4_gather_runs<BF16, 128>);
-    kern<<<grid_for_runs(c, c.heads, dev), kCacheThreads, 0, stream>>>(a);
+    kern<<<grid_for_runs(c, c.heads, 5, dev), kCacheThreads, 0, stream>>>(a);
     return cudaGetLastError();
   }
   const int per = c.d == 64 ? 2 : 1;
