@@ -1,19 +1,24 @@
 // kernel_logits.cu -- penalties, biases and masks on logits, fused with the softmax that follows.
 //
 // For token j of row r, with c the times it was generated and "seen" whether it is in the prompt or was generated:
-//     l = x;  seen: l = l > 0 ? l / repetition : l repetition;  c > 0: l -= frequency c + presence;  l += biases;
-//     l *= scale;  mask bit clear: l = -inf
+//     l = x;  seen: l = l > 0 ? l / repetition (times the rounded reciprocal) : l repetition;
+//     c > 0: l -= frequency c + presence;  l += biases;  l *= scale;  mask bit clear: l = -inf
 // and y = l, softmax(l) or log softmax(l) with the row's online (m, d) state.
 //
-// What bounds it: x is read once and y written once.  A thread-block cluster owns a row; a CTA holds its part of it in
-// registers from the read to the write.  The few tokens that occur in the row's lists are dealt with apart from the
-// many that do not: each has a word in shared memory, set to zero, then
+// What bounds it: x is read once from HBM and y written once.  A thread-block cluster owns a row (one CTA where there are
+// rows enough), each CTA a part of it; the part is streamed twice, once for the state and once for the output, the
+// second time from L2, where the rows in work (a few hundred of up to half a MB) stay.  Holding the part on chip between
+// the two (registers, 16384 elements a CTA, eight CTAs a row) cost more in barriers between CTAs than the second
+// reading: 256 rows of 131072 bf16 logits took 156 us that way.
+//
+// The few tokens that occur in the row's lists are dealt with before the streaming.  A bit map over the part's elements
+// says which they are, a running count over its words numbers them, and each has a word in shared memory that becomes
 //     bits 20-30: bias_count - index of its first bias (integer maximum);  bit 31: in the prompt;  bits 0-19: c
-// (integer sums: the order of the atomics does not matter), then replaced by l before scale and mask, worked out once,
-// by the first thread that takes the token's bit.  A second bit map tells the pass over all elements which of them to
-// take from there, so that pass looks at one bit an element.  Biases of one token add up in the order of the list.
-// CTA states are merged over distributed shared memory in the order of the ranks.  Rows longer than a cluster holds are
-// taken in chunks, read twice and their lists looked at twice.
+// (integer sums: the order of the atomics does not matter) and then the masked l before scale, worked out once, one token
+// a thread.  Streaming looks at one bit an element.  Biases of one token add up in the order of the list.
+// Where the listed tokens of a part may be more than shared memory holds, the part is taken in chunks.
+#include <atomic>
+
 #include "device_common.cuh"
 #include "logits.h"
 
@@ -21,279 +26,390 @@ namespace rwo {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kChunk = 16384;  // elements of a CTA's part that are held (32 a thread)
-constexpr int kVals = kChunk / kThreads;
 constexpr uint32_t kSeen = 1u << 31;
 constexpr uint32_t kCount = (1u << 20) - 1;
+constexpr uint32_t kField = 2047u << 20;
 constexpr int kMaxCluster = 16;
+constexpr int kMaxListed = 16384;     // words of a chunk's listed tokens
+constexpr int kMaxChunk = 1 << 18;    // elements of a chunk: bit map and running count are 6 bytes for 32 elements
 
 struct Args {
   LogitsProblem p;
   unsigned* status;
-  int chunks;   // chunks of a CTA's part
-  int counted;  // tokens or biases are given
+  int log2_ranks;
+  int chunk;      // vectors of a chunk
+  int chunks;     // chunks of a part
+  int listed;     // words of listed tokens, 0 where no tokens and biases are given
+  int map_words;  // words of the bit map
+  int mask_words;  // words of the mask for a chunk
 };
 
 struct Smem {
   State warp[kThreads / 32];
   State ranks[kMaxCluster];
-  int twice;                       // some token has several biases
+  int sums[kThreads / 32];
+  int twice;  // some token has several biases
   int pad[3];
-  uint32_t listed[kChunk / 32];    // elements whose value is in `words`
-  uint32_t taken[kChunk / 32];     // elements that a thread has taken on itself
-  int bias_id[kMaxBias];
-  float bias_value[kMaxBias];
 };
-constexpr int kSmemWords = (sizeof(Smem) + 127) / 128 * 128;
+
+// Dynamic shared memory behind Smem: words and ids of the listed tokens, bit map, mask, ids and values of the biases,
+// running count.
+__host__ __device__ inline size_t smem_bytes(int listed, int map_words, int mask_words, int bias_count) {
+  return sizeof(Smem) + size_t(listed) * 8 + size_t(map_words) * 6 + size_t(mask_words) * 4 + size_t(bias_count) * 8;
+}
+
+// A vector's elements where bit i of `bits` is set, -inf elsewhere: on the packed words, before they are widened.
+template <class D>
+__device__ __forceinline__ uint4 only(uint4 v, uint32_t bits) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (D::kBytes == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(bits & (1u << i))) w[i] = D::kNegInfWord;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      // bit k of four becomes the top bit of byte k, and a byte permutation spreads top bits over two bytes each
+      const uint32_t tops = ((bits >> (2 * i)) & 15u) * 0x10204080u;
+      uint32_t k0, k1;
+      asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(k0) : "r"(tops));
+      asm("prmt.b32 %0, %1, 0, 0xbbaa;" : "=r"(k1) : "r"(tops));
+      w[i] = (w[i] & k0) | (D::kNegInfWord & ~k0);
+      w[i + 1] = (w[i + 1] & k1) | (D::kNegInfWord & ~k1);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 enum { kLogits = 0, kSoftmax = 1, kLogSoftmax = 2 };
 
 template <class D, int OUT>
-__global__ void __launch_bounds__(kThreads, 2) k_logits(Args a) {
-  extern __shared__ __align__(128) unsigned char smem_raw[];
+__global__ void __launch_bounds__(kThreads, 2) k_logits(const __grid_constant__ Args a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  constexpr int V = D::kVec;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-  uint32_t* words = reinterpret_cast<uint32_t*>(smem_raw + kSmemWords);
-  constexpr int V = D::kVec, K = kVals / V;  // vectors a thread holds
   const LogitsProblem& p = a.p;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = cluster_ctarank();
-  uint32_t ranks;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem_raw + sizeof(Smem));
+  int* ids = reinterpret_cast<int*>(words + a.listed);
+  uint32_t* map = words + 2 * a.listed;
+  uint32_t* allowed = map + a.map_words;
+  int* bias_id = reinterpret_cast<int*>(allowed + a.mask_words);
+  float* bias_value = reinterpret_cast<float*>(bias_id + p.bias_count);
+  uint16_t* below = reinterpret_cast<uint16_t*>(bias_value + p.bias_count);  // listed tokens in the map's words before
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = int(p.N);
+  const int rank = int(cluster_ctarank()), ranks = 1 << a.log2_ranks;
   const int64_t r = cluster_id_x();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  const unsigned char* xr = static_cast<const unsigned char*>(p.x) + r * p.x_pitch * D::kBytes;
-  unsigned char* yr = static_cast<unsigned char*>(p.y) + r * p.y_pitch * D::kBytes;
-  // places count from the 16-byte boundary at or below the row's start: element j is place j + off
-  const int N = int(p.N), off = int((reinterpret_cast<uintptr_t>(xr) & 15u) / D::kBytes);
-  const bool same = ((reinterpret_cast<uintptr_t>(yr) ^ reinterpret_cast<uintptr_t>(xr)) & 15u) == 0;
-  const int vecs = (N + off + V - 1) / V, per = (vecs + int(ranks) - 1) / int(ranks);
-  const int v0 = min(per * int(rank), vecs), v1 = min(v0 + per, vecs);
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
-  const float scale = p.scale ? __ldg(p.scale + r) : 1.f;
-  int n_tokens = 0, n_prompt = 0;
-  if (p.tokens) {
-    n_tokens = __ldg(p.token_lens + r);
-    n_prompt = p.prompt_lens ? __ldg(p.prompt_lens + r) : 0;
-    if (n_tokens < 0 || n_tokens > p.token_pitch || n_prompt < 0 || n_prompt > n_tokens) {
-      if (tid == 0) atomicOr(a.status, kStatusBadIndex);
-      n_tokens = n_tokens < 0 ? 0 : n_tokens > p.token_pitch ? int(p.token_pitch) : n_tokens;
-    }
-  }
-  const int32_t* toks = p.tokens ? p.tokens + r * p.token_pitch : nullptr;
+  const unsigned char* x = static_cast<const unsigned char*>(p.x) + r * p.x_pitch * D::kBytes;
+  unsigned char* y = static_cast<unsigned char*>(p.y) + r * p.y_pitch * D::kBytes;
   const uint32_t* mask = p.mask ? p.mask + r * p.mask_pitch : nullptr;
+  const int32_t* toks = p.tokens ? p.tokens + r * p.token_pitch : nullptr;
+  // The row as whole 16-byte vectors, with the few elements before its first boundary (rank 0) and behind its last (the
+  // last rank), which threads 0 .. and 32 .. of those CTAs take one each.
+  const int off = int((reinterpret_cast<uintptr_t>(x) & 15u) / D::kBytes), front = off ? min(V - off, N) : 0;
+  const int vecs = (N - front) / V, back = N - front - vecs * V, per = (vecs + ranks - 1) >> a.log2_ranks;
+  const int v0 = min(per * rank, vecs), v1 = min(v0 + per, vecs);
+  const bool whole = ((reinterpret_cast<uintptr_t>(y) ^ reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
+  const float scale = p.scale ? __ldg(p.scale + r) : 1.f;
 
-  // The listed tokens of elements [j0, j0 + n): their values before scale and mask into `words`, their bits into `listed`.
-  // j0 may be negative (places before the row); ids are not.
-  auto lists = [&](int j0, int n) {
-    __syncthreads();  // the last chunk's words have been read
-    for (int i = tid; i < kChunk / 32; i += kThreads) sm.listed[i] = sm.taken[i] = 0u;
+  if (tid == 0 && v1 > v0) {  // the part on its way to L2 while the lists are looked through
+    const unsigned char* from = x + (int64_t(v0) * V + front) * D::kBytes;
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(uint32_t(min(v1 - v0, kMaxChunk / V)) * 16u) : "memory");
+  }
+  // The mask of vectors [c0, c0 + n) into shared memory, from the word of the first element on.
+  auto masks = [&](int c0, int n) {
+    const int e0 = front + c0 * V, w0 = e0 >> 5, w1 = n ? (e0 + n * V - 1) >> 5 : w0 - 1;
+    __syncthreads();  // the last chunk's have been read
+    for (int i = tid; i <= w1 - w0; i += kThreads) allowed[i] = __ldg(mask + w0 + i);
+    __syncthreads();
+  };
+
+  // The listed tokens among vectors [c0, c0 + n) and this part's single elements.  Place of element id in the map: 32 for
+  // the first vector's first, the elements before it below that.
+  auto lists = [&](int c0, int n) {
+    constexpr int kAhead = 16;
+    int ahead[kAhead];  // the first tokens are on their way while shared memory is cleared, without waiting for their count
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) ahead[k] = toks && tid + k * kThreads < p.token_pitch ? __ldg(toks + tid + k * kThreads) : -1;
+    int n_tokens = 0, n_prompt = 0;
+    if (toks) {
+      n_tokens = __ldg(p.token_lens + r);
+      n_prompt = p.prompt_lens ? __ldg(p.prompt_lens + r) : 0;
+      if (n_tokens < 0 || n_tokens > p.token_pitch || n_prompt < 0 || n_prompt > n_tokens) {
+        if (tid == 0) atomicOr(a.status, kStatusBadIndex);
+        n_tokens = n_tokens < 0 ? 0 : n_tokens > p.token_pitch ? int(p.token_pitch) : n_tokens;
+      }
+    }
+    const int base = front + c0 * V - 32;  // element of place 0
+    const int e0 = rank == 0 && c0 == v0 ? 0 : base + 32, e1 = rank == ranks - 1 && c0 + n == v1 ? N : base + 32 + n * V;
+    const int used = (n * V + 32 + V + 31) / 32;  // of the map's words
+    __syncthreads();  // the last chunk's have been read
+    for (int i = tid; i < used; i += kThreads) map[i] = 0u;
+    for (int i = tid; i < a.listed; i += kThreads) words[i] = 0u;
     if (tid == 0) sm.twice = 0;
+    __syncthreads();
+    auto set = [&](int at) {
+      const uint32_t bit = 1u << (at & 31);
+      if (!(map[at >> 5] & bit)) atomicOr(&map[at >> 5], bit);
+    };
     for (int i = tid; i < p.bias_count; i += kThreads) {
       const int id = __ldg(p.bias_ids + r * p.bias_count + i);
-      sm.bias_id[i] = id < N ? id : -1;
-      sm.bias_value[i] = __ldg(p.bias_values + r * p.bias_count + i);
+      const bool here = id >= e0 && id < e1 && id < N;
+      bias_id[i] = here ? id : -1;
+      bias_value[i] = __ldg(p.bias_values + r * p.bias_count + i);
+      if (here) set(id - base);
       if (id >= N) atomicOr(a.status, kStatusBadIndex);
-      else if (id >= 0 && uint32_t(id - j0) < uint32_t(n)) words[id - j0] = 0u;
     }
     auto each_token = [&](auto f) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = tid + k * kThreads;
+        if (i < n_tokens && ahead[k] >= e0 && ahead[k] < e1) f(i, ahead[k]);
+      }
 #pragma unroll 4
-      for (int i = tid; i < n_tokens; i += kThreads) {
+      for (int i = tid + kAhead * kThreads; i < n_tokens; i += kThreads) {
         const int id = __ldg(toks + i);
-        if (id >= 0 && id < N && uint32_t(id - j0) < uint32_t(n)) f(id - j0, i, id);
+        if (id >= e0 && id < e1) f(i, id);
+        else if (id >= N) atomicOr(a.status, kStatusBadIndex);
       }
     };
-#pragma unroll 4
-    for (int i = tid; i < n_tokens; i += kThreads) {
-      const int id = __ldg(toks + i);
-      if (id >= N) atomicOr(a.status, kStatusBadIndex);
-      else if (id >= 0 && uint32_t(id - j0) < uint32_t(n)) words[id - j0] = 0u;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (tid + k * kThreads < n_tokens && ahead[k] >= N) atomicOr(a.status, kStatusBadIndex);
+    each_token([&](int, int id) { set(id - base); });
+    __syncthreads();
+    // the running count: every thread a run of words
+    const int each = (used + kThreads - 1) / kThreads, w0 = min(tid * each, used), w1 = min(w0 + each, used);
+    int sum = 0;
+    for (int w = w0; w < w1; ++w) sum += __popc(map[w]);
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int s = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += s;
+    }
+    if (lane == 31) sm.sums[warp] = upto;
+    __syncthreads();
+    int count = 0, before = upto - sum;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sm.sums[w];
+      count += sm.sums[w];
+    }
+    for (int w = w0; w < w1; ++w) {
+      below[w] = uint16_t(before);
+      before += __popc(map[w]);
     }
     __syncthreads();
+    auto number = [&](int at) { return int(below[at >> 5]) + __popc(map[at >> 5] & ((1u << (at & 31)) - 1u)); };
     if (p.bias_count) {
-      for (int i = tid; i < p.bias_count; i += kThreads) {
-        const int id = sm.bias_id[i];
-        if (id >= 0 && uint32_t(id - j0) < uint32_t(n)) atomicMax(&words[id - j0], uint32_t(p.bias_count - i) << 20);
-      }
+      for (int i = tid; i < p.bias_count; i += kThreads)
+        if (bias_id[i] >= 0) {
+          const int k = number(bias_id[i] - base);
+          ids[k] = bias_id[i];
+          atomicMax(&words[k], uint32_t(p.bias_count - i) << 20);
+        }
       __syncthreads();
+      for (int i = tid; i < p.bias_count; i += kThreads)
+        if (bias_id[i] >= 0 && int((words[number(bias_id[i] - base)] & kField) >> 20) != p.bias_count - i) sm.twice = 1;
+      // (counts, added from here on, leave that field alone)
     }
-    each_token([&](int at, int i, int) {
-      if (i < n_prompt) atomicOr(&words[at], kSeen);
-      else atomicAdd(&words[at], 1u);
+    each_token([&](int i, int id) {
+      const int k = number(id - base);
+      ids[k] = id;
+      if (i < n_prompt) atomicOr(&words[k], kSeen);
+      else atomicAdd(&words[k], 1u);
     });
-    for (int i = tid; i < p.bias_count; i += kThreads) {
-      const int id = sm.bias_id[i];
-      if (id >= 0 && uint32_t(id - j0) < uint32_t(n) && int((words[id - j0] >> 20) & 2047u) != p.bias_count - i) sm.twice = 1;
-    }
-    __syncthreads();
-    const float rep = p.repetition ? __ldg(p.repetition + r) : 1.f;
+    const float rep = p.repetition ? __ldg(p.repetition + r) : 1.f, rep_inv = __frcp_rn(rep);
     const float freq = p.frequency ? __ldg(p.frequency + r) : 0.f, pres = p.presence ? __ldg(p.presence + r) : 0.f;
-    auto settle = [&](int at, int id) {
-      const uint32_t bit = 1u << (at & 31);
-      if (sm.taken[at >> 5] & bit) return;
-      if (atomicOr(&sm.taken[at >> 5], bit) & bit) return;
-      const uint32_t w = words[at], c = w & kCount;
-      float l = D::load1(xr, id);
-      if ((w & kSeen) || c) l = l > 0.f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < count; i += kThreads) {
+      const int id = ids[i];
+      const uint32_t w = words[i], c = w & kCount;
+      float l = D::load1(x, id);
+      if ((w & kSeen) || c) l = __fmul_rn(l, l > 0.f ? rep_inv : rep);
       if (c) l = __fsub_rn(l, __fadd_rn(__fmul_rn(freq, float(c)), pres));
-      if (const int field = int((w >> 20) & 2047u)) {
+      if (const int field = int((w & kField) >> 20)) {
         const int first = p.bias_count - field;
-        float sum = sm.bias_value[first];
+        float add = bias_value[first];
         if (sm.twice)
           for (int k = first + 1; k < p.bias_count; ++k)
-            if (sm.bias_id[k] == id) sum = __fadd_rn(sum, sm.bias_value[k]);
-        l = __fadd_rn(l, sum);
+            if (bias_id[k] == id) add = __fadd_rn(add, bias_value[k]);
+        l = __fadd_rn(l, add);
       }
-      words[at] = __float_as_uint(l);
-      atomicOr(&sm.listed[at >> 5], bit);
-    };
-    each_token([&](int at, int, int id) { settle(at, id); });
-    for (int i = tid; i < p.bias_count; i += kThreads) {
-      const int id = sm.bias_id[i];
-      if (id >= 0 && uint32_t(id - j0) < uint32_t(n)) settle(id - j0, id);
+      words[i] = __float_as_uint(mask && !((__ldg(mask + (id >> 5)) >> (id & 31)) & 1u) ? -INFINITY : l);
     }
     __syncthreads();
   };
-
-  float val[kVals];
-  // Loads vectors c0 .. of the part, up to kChunk elements, and processes them.
-  auto process = [&](int c0) {
-    const int c1 = min(c0 + kChunk / V, v1);
-    uint4 raw[K];
+  // The value of the single element id (in the map at place `at`).
+  auto single = [&](int id, int at) {
+    float l = D::load1(x, id);
+    if (a.listed && ((map[at >> 5] >> (at & 31)) & 1u))
+      l = __uint_as_float(words[int(below[at >> 5]) + __popc(map[at >> 5] & ((1u << (at & 31)) - 1u))]);
+    l = __fmul_rn(l, scale);
+    return mask && !((__ldg(mask + (id >> 5)) >> (id & 31)) & 1u) ? -INFINITY : l;
+  };
+  // Streams chunk [c0, c0 + n): f(values, vector) for each vector, g(value, element) for this thread's single element.
+  auto stream = [&](int c0, int n, auto f, auto g) {
+    constexpr int kAhead = 4;
+    const unsigned char* from = x + (int64_t(c0) * V + front) * D::kBytes;
+    for (int i0 = tid; i0 < n; i0 += kAhead * kThreads) {
+      uint4 raw[kAhead];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = c0 + tid + k * kThreads, j = v * V - off;
-      if (v < c1 && j >= 0 && j + V <= N) raw[k] = ld16(xr + int64_t(j) * D::kBytes);
-    }
-    if (a.counted) lists(c0 * V - off, (c1 - c0) * V);
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + k * kThreads < n) raw[k] = ld16(from + int64_t(i0 + k * kThreads) * 16);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = c0 + tid + k * kThreads, j = v * V - off;
-      float f[V];
-      if (v < c1 && j >= 0 && j + V <= N) {
-        D::unpack(raw[k], f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = v < c1 && j + i >= 0 && j + i < N ? D::load1(xr, j + i) : -INFINITY;
-      }
-      if (a.counted) {
-        const int at = (tid + k * kThreads) * V;  // v - c0
-        const uint32_t bits = sm.listed[at >> 5] >> (at & 31);
-        if (bits & ((1u << V) - 1u)) {
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if ((bits >> i) & 1u) f[i] = __uint_as_float(words[at + i]);
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * kThreads;
+        if (i >= n) break;
+        float l[V];
+        if (mask) {
+          const int e = ((front + c0 * V) & 31) + i * V, sh = e & 31;
+          uint32_t bits = allowed[e >> 5] >> sh;
+          if (front && sh + V > 32) bits |= allowed[(e >> 5) + 1] << (32 - sh);
+          raw[k] = only<D>(raw[k], bits);
         }
-      }
+        D::unpack(raw[k], l);
+        if (a.listed) {
+          const int w = 1 + (i * V >> 5), sh = i * V & 31;
+          const uint32_t m = map[w], mine = (m >> sh) & ((1u << V) - 1u);
+          if (mine) {
+            const uint32_t* at = words + below[w] + __popc(m & ((1u << sh) - 1u));
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = __fmul_rn(f[i], scale);
-      if (mask && v < c1) {
-        const int lo = max(j, 0), w0 = lo >> 5, sh = lo & 31;
-        const uint32_t a0 = __ldg(mask + w0), a1 = sh + V > 32 && w0 < ((N - 1) >> 5) ? __ldg(mask + w0 + 1) : 0u;
-        const uint32_t bits = __funnelshift_r(a0, a1, uint32_t(sh)) << (lo - j);  // bit i: element j + i
+            for (int q = 0; q < V; ++q)
+              if (mine & (1u << q)) l[q] = __uint_as_float(*at++);
+          }
+        }
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (!((bits >> i) & 1u)) f[i] = -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) val[k * V + i] = f[i];
-    }
-  };
-  // Writes the values held, those of the vectors from c0 on; f maps a processed value to the output.
-  auto write = [&](int c0, auto f) {
-    const int c1 = min(c0 + kChunk / V, v1);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = c0 + tid + k * kThreads, j = v * V - off;
-      if (v >= c1) continue;
-      float o[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = f(val[k * V + i]);
-      if (same && j >= 0 && j + V <= N) {
-        st_stream16(yr + int64_t(j) * D::kBytes, D::pack(o));
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (j + i >= 0 && j + i < N) D::store1(yr, j + i, o[i]);
+        for (int q = 0; q < V; ++q) l[q] = __fmul_rn(l[q], scale);
+        f(l, c0 + i);
       }
     }
+    if (rank == 0 && c0 == v0 && tid < front) g(single(tid, 32 - front + tid), tid);
+    if (rank == ranks - 1 && c0 + n == v1 && tid >= 32 && tid - 32 < back) g(single(N - back + tid - 32, 32 + n * V + tid - 32), N - back + tid - 32);
   };
-  auto chunk_at = [&](int c) { return min(v0 + c * (kChunk / V), v1); };
+  auto put = [&](const float (&o)[V], int v) {
+    unsigned char* to = y + (int64_t(v) * V + front) * D::kBytes;
+    if (whole) {
+      st_stream16(to, D::pack(o));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) D::store1(to, i, o[i]);
+    }
+  };
 
-  // The row's state.  A softmax's values become e^(l - m) of this thread's own maximum m: one exponential an element.
   State s = empty_state();
-  float mine = 0.f;
   const bool state = OUT != kLogits || p.lse;
   for (int c = 0; c < a.chunks; ++c) {
-    process(chunk_at(c));
-    if (OUT == kLogits) write(chunk_at(c), [](float v) { return v; });
-    if (!state) continue;
-    float m = val[0];
+    const int c0 = min(v0 + c * a.chunk, v1), n = min(a.chunk, v1 - c0);
+    if (c > 0 && n == 0) break;
+    if (mask) masks(c0, n);
+    if (a.listed) lists(c0, n);
+    stream(
+        c0, n,
+        [&](const float (&l)[V], int v) {
+          if (OUT == kLogits) put(l, v);
+          if (!state) return;
+          float m = l[0];
 #pragma unroll
-    for (int i = 1; i < kVals; ++i) m = fmaxf(m, val[i]);
-    mine = safe_max(m);
-    float2 d = make_float2(0.f, 0.f);
+          for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+          m = fmaxf(m, s.m);
+          const float ms = safe_max(m);
+          float2 d = make_float2(__fmul_rn(s.d, exp_diff(s.m, ms)), 0.f);
 #pragma unroll
-    for (int i = 0; i < kVals; i += 2) {
-      const float2 e = exp_diff2(make_float2(val[i], val[i + 1]), make_float2(-mine, -mine));
-      d = __fadd2_rn(d, e);
-      if (OUT == kSoftmax) {
-        val[i] = e.x;
-        val[i + 1] = e.y;
-      }
-    }
-    s = merge(s, State{m, d.x + d.y});
+          for (int i = 0; i < V; i += 2) d = __fadd2_rn(d, exp_diff2(make_float2(l[i], l[i + 1]), make_float2(-ms, -ms)));
+          s = State{m, d.x + d.y};
+        },
+        [&](float l, int id) {
+          if (OUT == kLogits) D::store1(y, id, l);
+          s = merge(s, State{l, l == -INFINITY ? 0.f : 1.f});
+        });
   }
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the cluster runs
+  if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
   if (!state) return;
   s = group_merge_nary(s, sm.warp, kThreads / 32, warp, lane, [] { __syncthreads(); });
-  if (tid < int(ranks)) st_cluster_f32x2(map_to_rank(smem_addr(&sm.ranks[rank]), uint32_t(tid)), s.m, s.d);
-  cluster_sync();
-  s = sm.ranks[0];
-  for (uint32_t k = 1; k < ranks; ++k) s = merge(s, sm.ranks[k]);
+  if (ranks > 1) {
+    if (tid < ranks) st_cluster_f32x2(map_to_rank(smem_addr(&sm.ranks[rank]), uint32_t(tid)), s.m, s.d);
+    cluster_sync();
+    s = sm.ranks[0];
+    for (int k = 1; k < ranks; ++k) s = merge(s, sm.ranks[k]);
+  }
   if (rank == 0 && tid == 0 && p.lse) p.lse[r] = lse_of(s);
   if (OUT == kLogits) return;
   const float ms = safe_max(s.m), inv = safe_inv(s.d);
   const LogNorm ln = log_norm(s);
-  if (OUT == kSoftmax && a.chunks == 1) {
-    const float fix = __fmul_rn(exp_diff(mine, ms), inv);
-    write(v0, [&](float e) { return __fmul_rn(e, fix); });
-    return;
-  }
   for (int c = 0; c < a.chunks; ++c) {
-    if (a.chunks > 1) process(chunk_at(c));
-    if (OUT == kSoftmax) write(chunk_at(c), [&](float v) { return __fmul_rn(exp_diff(v, ms), inv); });
-    else write(chunk_at(c), [&](float v) { return log_prob(v, ln); });
+    const int c0 = min(v0 + c * a.chunk, v1), n = min(a.chunk, v1 - c0);
+    if (c > 0 && n == 0) break;
+    if (mask && a.chunks > 1) masks(c0, n);
+    if (a.listed && a.chunks > 1) lists(c0, n);
+    stream(
+        c0, n,
+        [&](const float (&l)[V], int v) {
+          float o[V];
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            if (OUT == kSoftmax) {
+              const float2 e = __fmul2_rn(exp_diff2(make_float2(l[i], l[i + 1]), make_float2(-ms, -ms)), make_float2(inv, inv));
+              o[i] = e.x;
+              o[i + 1] = e.y;
+            } else {
+              o[i] = log_prob(l[i], ln);
+              o[i + 1] = log_prob(l[i + 1], ln);
+            }
+          }
+          put(o, v);
+        },
+        [&](float l, int id) { D::store1(y, id, OUT == kSoftmax ? __fmul_rn(exp_diff(l, ms), inv) : log_prob(l, ln)); });
   }
 }
 
 template <class D>
 cudaError_t launch_for(const LogitsProblem& p, const DeviceInfo& dev) {
-  // The smallest cluster whose CTAs hold their parts; larger ones while SMs would stay idle and a part is above 2048
-  // elements.  A part is a whole number of 16-byte vectors; rows that do not begin on one may need one more.
-  const bool even = (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0 && (p.M == 1 || p.x_pitch % D::kVec == 0);
-  const int64_t vecs = (p.N + (even ? D::kVec - 1 : 2 * D::kVec - 2)) / D::kVec;
-  int ranks = 1;
-  while (ranks < kMaxCluster && (vecs + ranks - 1) / ranks * D::kVec > kChunk) ranks *= 2;
-  while (ranks < kMaxCluster && p.M * ranks < dev.sm_count && p.N / ranks > 4096) ranks *= 2;
-  const int64_t per = (vecs + ranks - 1) / ranks;
+  // One CTA a row where that gives every SM one; else more while a CTA's part is above 2048 elements.  (256 rows of 131072
+  // bf16 logits: one CTA a row 77 us, two 86, four 105: a row's lists are looked through by each of its CTAs.)
+  const int64_t vecs = (p.N + D::kVec - 1) / D::kVec;
+  int log2 = 0;
+  while ((1 << log2) < kMaxCluster && (p.M << log2) < dev.sm_count && (p.N >> log2) > 4096) ++log2;
   Args a;
   a.p = p;
   a.status = dev.status;
-  a.chunks = int((per * D::kVec + kChunk - 1) / kChunk);
-  a.counted = p.tokens || p.bias_count ? 1 : 0;
+  const bool counted = p.tokens || p.bias_count;
+  // a part is one chunk, unless its listed tokens or its map may not fit
+  const int64_t entries = (p.tokens ? p.token_pitch : 0) + p.bias_count;
+  int64_t most = !counted || entries <= kMaxListed ? kMaxChunk : kMaxListed - 16;
+  while ((1 << log2) < kMaxCluster && (counted || p.mask) && (((vecs - 1) >> log2) + 1) * D::kVec > most) ++log2;
+  const int64_t per = ((vecs - 1) >> log2) + 1, room = counted || p.mask ? most / D::kVec : per;
+  a.log2_ranks = log2;
+  a.chunk = int(per < room ? per : room);
+  a.chunks = int((per + a.chunk - 1) / a.chunk);
+  const int64_t elements = int64_t(a.chunk) * D::kVec + 16;
+  a.listed = counted ? int((entries < elements ? entries : elements) + 3) / 4 * 4 : 0;
+  a.map_words = counted ? (a.chunk * D::kVec + 32 + D::kVec + 31) / 32 : 0;
+  a.mask_words = p.mask ? a.chunk * D::kVec / 32 + 3 : 0;
   using Kern = void (*)(Args);
   const Kern kern = p.out == kLogits ? (Kern)k_logits<D, kLogits> : p.out == kSoftmax ? (Kern)k_logits<D, kSoftmax> : (Kern)k_logits<D, kLogSoftmax>;
-  cudaError_t err = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemWords + kChunk * 4);
-  if (err == cudaSuccess) err = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (err != cudaSuccess) return err;
+  // the kernel's limits are set once per device
+  constexpr int kDevices = 64;
+  static std::atomic<bool> ready[kDevices][3];
+  std::atomic<bool>& done = ready[dev.device % kDevices][p.out];
+  if (!done.load(std::memory_order_acquire)) {
+    cudaError_t err = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           int(smem_bytes(kMaxListed, kMaxChunk / 32 + 4, kMaxChunk / 32 + 3, kMaxBias)));
+    if (err == cudaSuccess) err = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err != cudaSuccess) return err;
+    done.store(true, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.M * ranks));
+  cfg.gridDim = dim3(unsigned(p.M << log2));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = size_t(kSmemWords + (a.counted ? kChunk * 4 : 0));
+  cfg.dynamicSmemBytes = smem_bytes(a.listed, a.map_words, a.mask_words, p.bias_count);
   cfg.stream = p.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(ranks);
+  attr[0].val.clusterDim.x = 1u << log2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import row_wise_online_gb300 as _rwo
 
@@ -88,8 +89,22 @@ def _on(index, stream):
     import torch
 
     if stream is None and torch.cuda.current_device() == index:
-        return _Here(torch.cuda.current_stream(index).cuda_stream)
+        return _Here(_raw_stream(index))
     return _switched(index, stream)
+
+
+def _raw_stream(index):
+    """The device's current stream as a pointer (torch's own short way where it has one: 0.1 us instead of 1.4)."""
+    import torch
+
+    short = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return short(index) if short else torch.cuda.current_stream(index).cuda_stream
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(index, *sizes):
+    """Of device ``index``, which is current: a function of the sizes and the device alone."""
+    return _rwo.capi().attention_kv4_workspace(*sizes)
 
 
 def _rows(t, name, heads, tokens, dim, dtype, index):
@@ -201,7 +216,7 @@ def attention_kv4_workspace(batch: int, tokens: int, num_heads: int, num_kv_head
 
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(device):
-        n = int(_rwo.capi().attention_kv4_workspace(batch, tokens, num_heads, num_kv_heads, head_dim))
+        n = _workspace_bytes(torch.cuda.current_device(), batch, tokens, num_heads, num_kv_heads, head_dim)
         if n < 0:
             raise _rwo.SoftmaxError(_rwo.ERR_UNSUPPORTED, "attention_kv4_workspace")
         return torch.empty(n, dtype=torch.uint8, device=device)
@@ -231,7 +246,7 @@ def attention_kv4(q, cache, page_table, seq_lens, cu_tokens=None, o=None, lse_ou
             o = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
         op = _tensor(o, "o", q.dtype, (T, heads, d), index)
         if workspace is None:
-            n = lib.attention_kv4_workspace(page_table.shape[0], T, heads, cache.shape[1], d)
+            n = _workspace_bytes(index, page_table.shape[0], T, heads, cache.shape[1], d)
             workspace = torch.empty(max(n, 0), dtype=torch.uint8, device=q.device)
         st = lib.attention_kv4(c, qr, op, lse, heads, 0.0 if scale is None else float(scale), dt, workspace.data_ptr(),
                                        workspace.numel(), s)

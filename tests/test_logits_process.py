@@ -145,6 +145,32 @@ def test_rows_longer_than_a_cluster_holds(out):
     check(s, y, lse, out, BF)
 
 
+@pytest.mark.parametrize("out", ["logits", "softmax", "log_softmax"])
+@pytest.mark.parametrize("N,L,K,mask", [(400003, 20000, 9, True), (300000, 70000, 0, False), (5000011, 40, 3, True)])
+def test_parts_taken_in_chunks(N, L, K, mask, out):
+    """More listed tokens, or a longer mask, than a CTA holds for its part; also in place, where the second pass reads what
+    the first has not changed."""
+    s = make(1, N, BF, seed=7, L=L, K=K, mask=mask)
+    lse = torch.empty(1, device="cuda")
+    a = args(s)
+    x = s["x"].cuda()
+    y = rwo.logits_process_rows(x, out=out, lse_out=lse, **a)
+    assert rwo.get_status() == rwo.OK
+    check(s, y, lse, out, BF)
+    rwo.logits_process_rows(x, y=x, out=out, **a)
+    assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("M", [77, 151, 152, 400])
+def test_row_counts_around_the_sms(M):
+    """One CTA a row, two, or more rows than are resident."""
+    s = make(M, 20011, FP, seed=M, L=300, K=20, mask=True)
+    lse = torch.empty(M, device="cuda")
+    y = rwo.logits_process_rows(s["x"].cuda(), lse_out=lse, **args(s))
+    assert rwo.get_status() == rwo.OK
+    check(s, y, lse, "softmax", FP)
+
+
 def test_many_rows_and_no_options():
     s = make(700, 4100, FP, seed=8, params=False)
     lse = torch.empty(700, device="cuda")
