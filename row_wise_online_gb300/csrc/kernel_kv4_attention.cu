@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
   using B = Kv4Block<DH>;
   using SM = Smem<DH, NT, KB>;
   constexpr int G = B::G, R = SM::R, kKeys = SM::kKeys, kStages = SM::kStages;
+  constexpr bool kQInSmem = NT * DH > 128;  // Q's fragments are read again for every stage: their 32 registers are short
   extern __shared__ __align__(128) unsigned char smem[];
   const Kv4View& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -269,15 +270,19 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
   bool timed_out = false;
 
   if (warp == kWarps) {
-    // ---- producer: one lane a block of the stage; the next stage's pages are looked up while a slot is waited for ----
+    // ---- producer: a copy for each run of blocks that lie together in a page, by the lane of the run's first block; the
+    // next stage's pages are looked up while a slot is waited for ----
     const uint64_t policy = policy_evict_first();
-    auto block_of = [&]() -> int64_t {  // byte offset of this lane's block in the cursor's tile; -1: no key in it
-      const int key = at.tile * kKeys + lane * kKv4Block;
-      if (lane >= SM::kBlocks || key >= at.w.s.len) return -1;
-      int64_t off = kv4_block_at(c, at.b, key, B::kBytes);
+    uint32_t bytes = 0;                   // of this lane's next copy
+    auto block_of = [&]() -> int64_t {    // and where it starts; -1: this lane has none
+      const int blk = at.tile * SM::kBlocks + lane, in_page = blk % c.page_blocks;
+      const int n = min(min(SM::kBlocks - lane, (at.w.s.len + kKv4Block - 1) / kKv4Block - blk), c.page_blocks - in_page);
+      if (n <= 0 || (lane && in_page)) return -1;
+      bytes = uint32_t(n * B::kBytes);
+      int64_t off = kv4_block_at(c, at.b, blk * kKv4Block, B::kBytes);
       if (off < 0) {  // no page: the status says so, and page 0 stands in
         kv4_bad(c);
-        off = 0;
+        off = int64_t(in_page) * B::kBytes;
       }
       return off + int64_t(at.h) * c.page_blocks * B::kBytes;
     };
@@ -286,18 +291,20 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
     int64_t issued = 0, off = block_of();
     while (left > 0) {
       const int64_t now = off;
+      const uint32_t size = now >= 0 ? bytes : 0u;
+      // whole blocks of the tile that hold a key
+      const int blocks = max(0, min(SM::kBlocks, (at.w.s.len + kKv4Block - 1) / kKv4Block - at.tile * SM::kBlocks));
       if (--left > 0) {
         if (++at.tile == at.w.tiles) next_item<R, kKeys>(at, c, a.group);
         off = block_of();
       }
-      const int n = __popc(__ballot_sync(kFull, now >= 0));
       if (issued >= kStages && !mbar_wait(empty(slot), lap ^ 1u, a.wait_ns)) timed_out = true;
       if (lane == 0) {
-        if (n) mbar_arrive_expect_tx(full(slot), uint32_t(n * B::kBytes));
+        if (blocks) mbar_arrive_expect_tx(full(slot), uint32_t(blocks * B::kBytes));
         else mbar_arrive(full(slot));
       }
       __syncwarp();
-      if (now >= 0) bulk_g2s(sbase + uint32_t(slot * SM::kStage + lane * B::kBytes), c.data + now, uint32_t(B::kBytes), full(slot), policy);
+      if (size) bulk_g2s(sbase + uint32_t(slot * SM::kStage + lane * B::kBytes), c.data + now, size, full(slot), policy);
       ++issued;
       if (++slot == kStages) {
         slot = 0;
@@ -375,13 +382,19 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
     }
     named_barrier_sync(1, kWarps * 32);
     uint32_t qf[NT][2 * G][2], qz[NT];
+    auto load_q = [&] {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int s = 0; s < 2 * G; ++s) words_at<2>(qf[i][s], smem + SM::kOffQ + ((i * 2 * G + s) * 32 + lane) * 8);
+    };
+    if (!kQInSmem) load_q();
     float ch[NT][2], mb[NT][2], l[NT][2], O[NT][2 * G][4], Z[NT][4];
     int seen[NT][2];  // keys that the row of column 2 t, 2 t + 1 sees
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
       for (int s = 0; s < 2 * G; ++s) {
-        words_at<2>(qf[i][s], smem + SM::kOffQ + ((i * 2 * G + s) * 32 + lane) * 8);
 #pragma unroll
         for (int k = 0; k < 4; ++k) O[i][s][k] = 0.f;
       }
@@ -409,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
       if (key0 < len) {
         const unsigned char* blk0 = smem + slot * SM::kStage + warp * KB * B::kBytes;
         // S^T = K Q^T
+        if (kQInSmem) load_q();
         float S[KB][NT][4];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
@@ -695,7 +709,7 @@ Plan plan_as() {
 }
 template <bool H, int DH>
 Plan plan_of(bool wide) {
-  return wide ? plan_as<H, DH, 2, 1>() : plan_as<H, DH, 1, 2>();
+  return wide ? plan_as<H, DH, 2, 2>() : plan_as<H, DH, 1, 2>();
 }
 // Tiles of 8 query rows, or of 16 where a sequence has more rows to a key/value head than 8 on average.
 Plan plan_for(int64_t batch, int64_t tokens, int q_heads, int heads, int d, int dtype) {
