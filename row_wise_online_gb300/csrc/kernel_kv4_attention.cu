@@ -33,7 +33,7 @@
 namespace rwo {
 namespace {
 
-constexpr int kWarps = 4;                     // consumer warps
+constexpr int kWarps = 4;                     // consumer warps (the scan and the merges below are written for four)
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr float kBase = 9.f, kSlack = 6.f;    // log2 of the maximum's weight, and by how much a score may exceed it
 constexpr float kUnseen = 1e30f;              // mb of a row that has seen no key
@@ -147,8 +147,8 @@ __device__ __forceinline__ void next_item(Cursor& k, const Kv4View& c, int group
 template <int DH, int NT, int KB>
 struct Smem {
   using B = Kv4Block<DH>;
-  static constexpr int kStages = KB * DH >= 256 ? 2 : DH == 128 ? 4 : 6 / KB;
-  static constexpr int kCtas = NT == 2 ? (DH == 64 ? 3 : 2) : DH == 64 ? 4 : 3;  // resident on an SM: bounds the registers
+  static constexpr int kStages = DH == 64 ? 3 : 2;
+  static constexpr int kCtas = NT == 2 ? (DH == 64 ? 3 : 2) : 3;  // resident on an SM: bounds the registers
   static constexpr int kBlocks = kWarps * KB;            // of a stage
   static constexpr int kKeys = kBlocks * kKv4Block;
   static constexpr int R = 8 * NT;                       // query rows of a tile
@@ -652,20 +652,23 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
   if (timed_out && lane == 0) atomicOr(c.status, kStatusTimeout);
 }
 
-// One CTA per query row: merges the parts of rows whose keys were spread over several runs.
+// Merges the parts of rows whose keys were spread over several runs: `split` of a CTA's four warps a row (four where rows
+// are few, and their parts many; else one).
 template <bool H, int DH, int NT, int KB>
-__global__ void __launch_bounds__(128) k_attention_kv4_merge(AttnArgs a) {
+__global__ void __launch_bounds__(128) k_attention_kv4_merge(AttnArgs a, int split) {
   constexpr int E = DH / 32, R = 8 * NT, kKeys = Smem<DH, NT, KB>::kKeys;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Kv4View& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t i = int64_t(blockIdx.x) / a.q_heads;
-  const int hq = int(int64_t(blockIdx.x) - i * a.q_heads);
-  const int b = kv4_seq_of(c, i);
-  if (b < 0) return;
+  const int64_t x = int64_t(blockIdx.x) * (4 / split) + (split == 4 ? 0 : warp), i = x / a.q_heads;
+  const int hq = int(x - i * a.q_heads), share = split == 4 ? warp : 0;
+  // what the main kernel does not write is read before it is waited for
+  const int b = i < c.tokens ? kv4_seq_of(c, i) : -1;
   bool bad = false;
-  const SeqWork w = seq_work<R, kKeys>(c, b, a.group, bad);
-  if (i < w.s.start || i >= w.s.start + w.s.n) return;
+  SeqWork w;
+  w.s.n = 0;
+  if (b >= 0) w = seq_work<R, kKeys>(c, b, a.group, bad);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (b < 0 || i < w.s.start || i >= w.s.start + w.s.n) return;
   const int h = hq / a.group, rr = int(i - w.s.start) * a.group + hq - h * a.group, rb = rr / R, r = rr - rb * R;
   const Runs runs = runs_of(a.prefix[c.batch], a.runs);
   const int64_t t0 = a.prefix[b] + (int64_t(h) * w.row_blocks + rb) * w.tiles;
@@ -673,34 +676,36 @@ __global__ void __launch_bounds__(128) k_attention_kv4_merge(AttnArgs a) {
   if (c0 == c1) return;  // one run held all of its keys and wrote the row
   const int late = t0 > runs.first(c0) ? 1 : 0;  // the part in run c0 is not that run's first
   float4 s = make_float4(kUnseen, 0.f, 0.f, 0.f);
-  float x[E];
+  float o[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = 0.f;
-  auto add = [&](float4 v, const float* o) {
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  auto add = [&](float4 v, const float* p) {
     const float mb = fminf(s.x, v.x), f0 = ex2(mb - s.x), f1 = ex2(mb - v.x);
     s = make_float4(mb, fmaf(s.y, f0, v.y * f1), fmaf(s.z, f0, v.z * f1), 0.f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = fmaf(x[e], f0, o[lane * E + e] * f1);
+    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f0, p[lane * E + e] * f1);
   };
 #pragma unroll 4
-  for (int k = c0 + warp; k <= c1; k += 4) {
+  for (int k = c0 + share; k <= c1; k += split) {
     const int64_t part = int64_t(2 * k + (k == c0 ? late : 0)) * R + r;
     add(a.part_l[part], a.part_o + part * DH);
   }
-  __shared__ float4 sm[4];
-  __shared__ float so[4][DH];
-  if (lane == 0) sm[warp] = s;
+  if (split == 4) {
+    __shared__ float4 sm[4];
+    __shared__ float so[4][DH];
+    if (lane == 0) sm[warp] = s;
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = x[e];
-  __syncthreads();
-  if (warp) return;
-  for (int k = 1; k < 4; ++k) add(sm[k], so[k]);
-  write_row<H, DH>(a, i * a.q_heads + hq, lane, x, s);
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+    __syncthreads();
+    if (warp) return;
+    for (int k = 1; k < 4; ++k) add(sm[k], so[k]);
+  }
+  write_row<H, DH>(a, i * a.q_heads + hq, lane, o, s);
 }
 
 struct Plan {
-  using Kern = void (*)(AttnArgs);
-  Kern main, merge;
+  void (*main)(AttnArgs);
+  void (*merge)(AttnArgs, int);
   int smem, rows;
 };
 template <bool H, int DH, int NT, int KB>
@@ -709,7 +714,7 @@ Plan plan_as() {
 }
 template <bool H, int DH>
 Plan plan_of(bool wide) {
-  return wide ? plan_as<H, DH, 2, 2>() : plan_as<H, DH, 1, 2>();
+  return wide ? plan_as<H, DH, 2, 2>() : plan_as<H, DH, 1, 256 / DH>();
 }
 // Tiles of 8 query rows, or of 16 where a sequence has more rows to a key/value head than 8 on average.
 Plan plan_for(int64_t batch, int64_t tokens, int q_heads, int heads, int d, int dtype) {
@@ -775,7 +780,9 @@ cudaError_t launch_attention_kv4(const Kv4View& c, const Kv4Rows& q, void* o, fl
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   // the merge is launched while the last runs finish, and waits for them itself
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(c.tokens * q_heads));
+  const int64_t rows = c.tokens * q_heads;
+  const int split = rows <= 4 * int64_t(dev.sm_count) ? 4 : 1;
+  cfg.gridDim = dim3(unsigned((rows + 4 / split - 1) / (4 / split)));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -783,7 +790,7 @@ cudaError_t launch_attention_kv4(const Kv4View& c, const Kv4Rows& q, void* o, fl
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, p.merge, a);
+  return cudaLaunchKernelEx(&cfg, p.merge, a, split);
 }
 
 }  // namespace rwo
