@@ -15,7 +15,10 @@
 // says which they are, a running count over its words numbers them, and each has a word in shared memory that becomes
 //     bits 20-30: bias_count - index of its first bias (integer maximum);  bit 31: in the prompt;  bits 0-19: c
 // (integer sums: the order of the atomics does not matter) and then the masked l before scale, worked out once, one token
-// a thread.  Streaming looks at one bit an element.  Biases of one token add up in the order of the list.
+// a thread.  Streaming treats listed tokens as masked; their values join the state from the list, and their outputs are
+// written over the streamed ones at the end.  So a streamed element costs a mask bit and nothing else (256 rows of 131072
+// bf16 logits with 8192 tokens of history, 64 biases and a mask: 62 us; looking each vector up in the map, in both
+// passes, 72).  The scale is folded into the exponent.  Biases of one token add up in the order of the list.
 // Where the listed tokens of a part may be more than shared memory holds, the part is taken in chunks.
 #include <atomic>
 
@@ -111,20 +114,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_logits(const __grid_constant__ 
   const int vecs = (N - front) / V, back = N - front - vecs * V, per = (vecs + ranks - 1) >> a.log2_ranks;
   const int v0 = min(per * rank, vecs), v1 = min(v0 + per, vecs);
   const bool whole = ((reinterpret_cast<uintptr_t>(y) ^ reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
-  const float scale = p.scale ? __ldg(p.scale + r) : 1.f;
+  const float scale = p.scale ? __ldg(p.scale + r) : 1.f, slope = __fmul_rn(scale, kLog2e);
+  const bool masked = a.mask_words > 0;
 
   if (tid == 0 && v1 > v0) {  // the part on its way to L2 while the lists are looked through
     const unsigned char* from = x + (int64_t(v0) * V + front) * D::kBytes;
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(uint32_t(min(v1 - v0, kMaxChunk / V)) * 16u) : "memory");
   }
-  // The mask of vectors [c0, c0 + n) into shared memory, from the word of the first element on.
-  auto masks = [&](int c0, int n) {
-    const int e0 = front + c0 * V, w0 = e0 >> 5, w1 = n ? (e0 + n * V - 1) >> 5 : w0 - 1;
-    __syncthreads();  // the last chunk's have been read
-    for (int i = tid; i <= w1 - w0; i += kThreads) allowed[i] = __ldg(mask + w0 + i);
-    __syncthreads();
-  };
-
+  int listed = 0;  // tokens on the chunk's list
   // The listed tokens among vectors [c0, c0 + n) and this part's single elements.  Place of element id in the map: 32 for
   // the first vector's first, the elements before it below that.
   auto lists = [&](int c0, int n) {
@@ -191,11 +188,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_logits(const __grid_constant__ 
     }
     if (lane == 31) sm.sums[warp] = upto;
     __syncthreads();
-    int count = 0, before = upto - sum;
+    int before = upto - sum;
+    listed = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += sm.sums[w];
-      count += sm.sums[w];
+      listed += sm.sums[w];
     }
     for (int w = w0; w < w1; ++w) {
       below[w] = uint16_t(before);
@@ -225,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_logits(const __grid_constant__ 
     const float freq = p.frequency ? __ldg(p.frequency + r) : 0.f, pres = p.presence ? __ldg(p.presence + r) : 0.f;
     __syncthreads();
 #pragma unroll 4
-    for (int i = tid; i < count; i += kThreads) {
+    for (int i = tid; i < listed; i += kThreads) {
       const int id = ids[i];
       const uint32_t w = words[i], c = w & kCount;
       float l = D::load1(x, id);
@@ -243,15 +241,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_logits(const __grid_constant__ 
     }
     __syncthreads();
   };
-  // The value of the single element id (in the map at place `at`).
-  auto single = [&](int id, int at) {
-    float l = D::load1(x, id);
-    if (a.listed && ((map[at >> 5] >> (at & 31)) & 1u))
-      l = __uint_as_float(words[int(below[at >> 5]) + __popc(map[at >> 5] & ((1u << (at & 31)) - 1u))]);
-    l = __fmul_rn(l, scale);
-    return mask && !((__ldg(mask + (id >> 5)) >> (id & 31)) & 1u) ? -INFINITY : l;
+  // The elements of vectors [c0, c0 + n) that are streamed, bit by bit from the word of the first one's index on: allowed
+  // by the mask, and not listed.
+  auto masks = [&](int c0, int n) {
+    const int e0 = front + c0 * V, w0 = e0 >> 5, w1 = n ? (e0 + n * V - 1) >> 5 : w0 - 1, sh = e0 & 31;
+    if (!a.listed) __syncthreads();  // the last chunk's have been read (lists() waits too)
+    for (int i = tid; i <= w1 - w0; i += kThreads) {
+      uint32_t bits = mask ? __ldg(mask + w0 + i) : 0xffffffffu;
+      // bit k of word i is element 32 (w0 + i) + k, at place 32 i + k + 32 - sh of the map
+      if (a.listed) bits &= ~(sh ? __funnelshift_r(map[i], i < (n * V + 32 + V - 1) / 32 ? map[i + 1] : 0u, 32 - sh) : map[i + 1]);
+      allowed[i] = bits;
+    }
+    __syncthreads();
   };
-  // Streams chunk [c0, c0 + n): f(values, vector) for each vector, g(value, element) for this thread's single element.
+  // The single element id (in the map at place `at`), masked.
+  auto single = [&](int id, int at) {
+    if (a.listed && ((map[at >> 5] >> (at & 31)) & 1u)) return -INFINITY;
+    return mask && !((__ldg(mask + (id >> 5)) >> (id & 31)) & 1u) ? -INFINITY : D::load1(x, id);
+  };
+  // Streams chunk [c0, c0 + n), masked and before scale: f(values, vector) for each vector, g(value, element) for this
+  // thread's single element.
   auto stream = [&](int c0, int n, auto f, auto g) {
     constexpr int kAhead = 4;
     const unsigned char* from = x + (int64_t(c0) * V + front) * D::kBytes;
@@ -264,26 +273,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_logits(const __grid_constant__ 
       for (int k = 0; k < kAhead; ++k) {
         const int i = i0 + k * kThreads;
         if (i >= n) break;
-        float l[V];
-        if (mask) {
+        if (masked) {
           const int e = ((front + c0 * V) & 31) + i * V, sh = e & 31;
           uint32_t bits = allowed[e >> 5] >> sh;
           if (front && sh + V > 32) bits |= allowed[(e >> 5) + 1] << (32 - sh);
           raw[k] = only<D>(raw[k], bits);
         }
+        float l[V];
         D::unpack(raw[k], l);
-        if (a.listed) {
-          const int w = 1 + (i * V >> 5), sh = i * V & 31;
-          const uint32_t m = map[w], mine = (m >> sh) & ((1u << V) - 1u);
-          if (mine) {
-            const uint32_t* at = words + below[w] + __popc(m & ((1u << sh) - 1u));
-#pragma unroll
-            for (int q = 0; q < V; ++q)
-              if (mine & (1u << q)) l[q] = __uint_as_float(*at++);
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < V; ++q) l[q] = __fmul_rn(l[q], scale);
         f(l, c0 + i);
       }
     }
@@ -300,76 +297,94 @@ __global__ void __launch_bounds__(kThreads, 2) k_logits(const __grid_constant__ 
     }
   };
 
-  State s = empty_state();
+  // Outputs of the listed tokens, over what was streamed there.
+  auto put_listed = [&](auto g) {
+    if (!a.listed) return;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < listed; i += kThreads) D::store1(y, ids[i], g(__uint_as_float(words[i])));
+  };
+
+  State s = empty_state();  // of l before scale
   const bool state = OUT != kLogits || p.lse;
   for (int c = 0; c < a.chunks; ++c) {
     const int c0 = min(v0 + c * a.chunk, v1), n = min(a.chunk, v1 - c0);
     if (c > 0 && n == 0) break;
-    if (mask) masks(c0, n);
     if (a.listed) lists(c0, n);
+    if (masked) masks(c0, n);
+    auto one = [&](float l) { s = merge(s, State{l, l == -INFINITY ? 0.f : 1.f}, slope); };
     stream(
         c0, n,
-        [&](const float (&l)[V], int v) {
-          if (OUT == kLogits) put(l, v);
-          if (!state) return;
-          float m = l[0];
+        [&](float (&l)[V], int v) {
+          if (state) {
+            float m = l[0];
 #pragma unroll
-          for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
-          m = fmaxf(m, s.m);
-          const float ms = safe_max(m);
-          float2 d = make_float2(__fmul_rn(s.d, exp_diff(s.m, ms)), 0.f);
+            for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+            m = fmaxf(m, s.m);
+            const float ms = safe_max(m);
+            float2 d = make_float2(__fmul_rn(s.d, exp_diff(s.m, ms, slope)), 0.f);
 #pragma unroll
-          for (int i = 0; i < V; i += 2) d = __fadd2_rn(d, exp_diff2(make_float2(l[i], l[i + 1]), make_float2(-ms, -ms)));
-          s = State{m, d.x + d.y};
+            for (int i = 0; i < V; i += 2) d = __fadd2_rn(d, exp_diff2(make_float2(l[i], l[i + 1]), make_float2(-ms, -ms), slope));
+            s = State{m, d.x + d.y};
+          }
+          if (OUT == kLogits) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) l[i] = __fmul_rn(l[i], scale);
+            put(l, v);
+          }
         },
         [&](float l, int id) {
-          if (OUT == kLogits) D::store1(y, id, l);
-          s = merge(s, State{l, l == -INFINITY ? 0.f : 1.f});
+          if (OUT == kLogits) D::store1(y, id, __fmul_rn(l, scale));
+          one(l);
         });
+    if (a.listed && state)
+      for (int i = tid; i < listed; i += kThreads) one(__uint_as_float(words[i]));
+    if (OUT == kLogits) put_listed([&](float l) { return __fmul_rn(l, scale); });
   }
   if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
   if (!state) return;
-  s = group_merge_nary(s, sm.warp, kThreads / 32, warp, lane, [] { __syncthreads(); });
+  s = group_merge_nary(s, sm.warp, kThreads / 32, warp, lane, [] { __syncthreads(); }, slope);
   if (ranks > 1) {
     if (tid < ranks) st_cluster_f32x2(map_to_rank(smem_addr(&sm.ranks[rank]), uint32_t(tid)), s.m, s.d);
     cluster_sync();
     s = sm.ranks[0];
-    for (int k = 1; k < ranks; ++k) s = merge(s, sm.ranks[k]);
+    for (int k = 1; k < ranks; ++k) s = merge(s, sm.ranks[k], slope);
   }
-  if (rank == 0 && tid == 0 && p.lse) p.lse[r] = lse_of(s);
+  if (rank == 0 && tid == 0 && p.lse) p.lse[r] = lse_of(scaled_state(s, scale));
   if (OUT == kLogits) return;
   const float ms = safe_max(s.m), inv = safe_inv(s.d);
   const LogNorm ln = log_norm(s);
+  auto output = [&](float l) { return OUT == kSoftmax ? __fmul_rn(exp_diff(l, ms, slope), inv) : log_prob(l, ln, scale); };
   for (int c = 0; c < a.chunks; ++c) {
     const int c0 = min(v0 + c * a.chunk, v1), n = min(a.chunk, v1 - c0);
     if (c > 0 && n == 0) break;
-    if (mask && a.chunks > 1) masks(c0, n);
     if (a.listed && a.chunks > 1) lists(c0, n);
+    if (masked && a.chunks > 1) masks(c0, n);
     stream(
         c0, n,
-        [&](const float (&l)[V], int v) {
-          float o[V];
+        [&](float (&l)[V], int v) {
 #pragma unroll
           for (int i = 0; i < V; i += 2) {
             if (OUT == kSoftmax) {
-              const float2 e = __fmul2_rn(exp_diff2(make_float2(l[i], l[i + 1]), make_float2(-ms, -ms)), make_float2(inv, inv));
-              o[i] = e.x;
-              o[i + 1] = e.y;
+              const float2 e = __fmul2_rn(exp_diff2(make_float2(l[i], l[i + 1]), make_float2(-ms, -ms), slope), make_float2(inv, inv));
+              l[i] = e.x;
+              l[i + 1] = e.y;
             } else {
-              o[i] = log_prob(l[i], ln);
-              o[i + 1] = log_prob(l[i + 1], ln);
+              l[i] = output(l[i]);
+              l[i + 1] = output(l[i + 1]);
             }
           }
-          put(o, v);
+          put(l, v);
         },
-        [&](float l, int id) { D::store1(y, id, OUT == kSoftmax ? __fmul_rn(exp_diff(l, ms), inv) : log_prob(l, ln)); });
+        [&](float l, int id) { D::store1(y, id, output(l)); });
+    put_listed(output);
   }
 }
 
 template <class D>
 cudaError_t launch_for(const LogitsProblem& p, const DeviceInfo& dev) {
   // One CTA a row where that gives every SM one; else more while a CTA's part is above 2048 elements.  (256 rows of 131072
-  // bf16 logits: one CTA a row 77 us, two 86, four 105: a row's lists are looked through by each of its CTAs.)
+  // bf16 logits: one CTA a row 62 us, two 70: a row's lists are looked through by each of its CTAs.)
   const int64_t vecs = (p.N + D::kVec - 1) / D::kVec;
   int log2 = 0;
   while ((1 << log2) < kMaxCluster && (p.M << log2) < dev.sm_count && (p.N >> log2) > 4096) ++log2;
@@ -388,7 +403,7 @@ cudaError_t launch_for(const LogitsProblem& p, const DeviceInfo& dev) {
   const int64_t elements = int64_t(a.chunk) * D::kVec + 16;
   a.listed = counted ? int((entries < elements ? entries : elements) + 3) / 4 * 4 : 0;
   a.map_words = counted ? (a.chunk * D::kVec + 32 + D::kVec + 31) / 32 : 0;
-  a.mask_words = p.mask ? a.chunk * D::kVec / 32 + 3 : 0;
+  a.mask_words = p.mask || counted ? a.chunk * D::kVec / 32 + 3 : 0;
   using Kern = void (*)(Args);
   const Kern kern = p.out == kLogits ? (Kern)k_logits<D, kLogits> : p.out == kSoftmax ? (Kern)k_logits<D, kSoftmax> : (Kern)k_logits<D, kLogSoftmax>;
   // the kernel's limits are set once per device
