@@ -399,7 +399,8 @@ __device__ __forceinline__ uint32_t quantised8(float2 (&x)[4], __half& sh, __hal
   return eight;
 }
 
-constexpr int kAppendCtas = 4;  // resident on an SM: 80 registers a thread
+constexpr int kAppendCtas = 4;  // resident on an SM: 64 registers a thread (15714 prompt tokens: 85 us; with three, 96)
+constexpr int kDepth = 2;       // rows that a lane loads ahead (1: 87 us, 3: 93)
 constexpr int kQHeads = 32;  // query heads of a warp: a token's angles are loaded once for them
 
 // CTAs that write the cache and CTAs that rotate queries take turns in the grid, so that the ones' arithmetic runs beside
@@ -436,12 +437,17 @@ __global__ void __launch_bounds__(kCacheThreads, kAppendCtas) k_kv4_append_runs(
     const unsigned char* from = static_cast<const unsigned char*>(a.q.p) + (i * a.q.token + h * a.q.head + e) * 2;
     unsigned char* to = const_cast<unsigned char*>(static_cast<const unsigned char*>(a.q_out.p)) + (i * a.q_out.token + h * a.q_out.head + e) * 2;
     const int64_t step = a.q.head * (2 * kRows), step_out = a.q_out.head * (2 * kRows);
-    uint4 next = make_uint4(0u, 0u, 0u, 0u);
-    if (h < h1) next = *reinterpret_cast<const uint4*>(from);
+    uint4 next[kDepth];  // rows on their way while earlier ones are turned
+#pragma unroll
+    for (int m = 0; m < kDepth; ++m)
+      if (h + m * kRows < h1) next[m] = *reinterpret_cast<const uint4*>(from + m * step);
+#pragma unroll 1
     while (__any_sync(kFull, h < h1)) {
-      uint4 x = next;
+      uint4 x = next[0];
+#pragma unroll
+      for (int m = 1; m < kDepth; ++m) next[m - 1] = next[m];
+      if (h + kDepth * kRows < h1) next[kDepth - 1] = *reinterpret_cast<const uint4*>(from + kDepth * step);
       from += step;
-      if (h + kRows < h1) next = *reinterpret_cast<const uint4*>(from);  // on its way while this row is turned
       if (rot) {
         float2 f[4];
         turned<D>(f, x, e < rot, neighbours, partner, flip, t);  // (shuffles: a row's lanes have its elements before one is written)
@@ -471,15 +477,22 @@ __global__ void __launch_bounds__(kCacheThreads, kAppendCtas) k_kv4_append_runs(
     const int first = blk * kKv4Block + sub;  // this lane's first position
     const unsigned char* from = static_cast<const unsigned char*>(src.p) + ((row0 + first) * src.token + h * src.head + e) * 2;
     const float* cs = a.cos_sin + int64_t(first) * rot;
-    uint4 next = make_uint4(0u, 0u, 0u, 0u);
-    if (first >= p0 && first < last) next = *reinterpret_cast<const uint4*>(from);
+    const int64_t step = src.token * (2 * kRows);
+    uint4 next[kDepth];  // rows on their way while earlier ones are quantised
+#pragma unroll
+    for (int m = 0; m < kDepth; ++m) {
+      next[m] = make_uint4(0u, 0u, 0u, 0u);
+      if (first + m * kRows >= p0 && first + m * kRows < last) next[m] = *reinterpret_cast<const uint4*>(from + m * step);
+    }
 #pragma unroll 1
     for (int r = sub; r < kKv4Block; r += kRows) {  // kRows tokens of the block
-      const int p = blk * kKv4Block + r;
+      const int p = blk * kKv4Block + r, then = p + kDepth * kRows;
       const bool on = p >= p0 && p < last;
-      const uint4 x = next;
-      from += src.token * (2 * kRows);
-      if (r + kRows < kKv4Block && p + kRows >= p0 && p + kRows < last) next = *reinterpret_cast<const uint4*>(from);  // on its way meanwhile
+      const uint4 x = next[0];
+#pragma unroll
+      for (int m = 1; m < kDepth; ++m) next[m - 1] = next[m];
+      if (r + kDepth * kRows < kKv4Block && then >= p0 && then < last) next[kDepth - 1] = *reinterpret_cast<const uint4*>(from + kDepth * step);
+      from += step;
       if (__any_sync(kFull, on)) {
         float2 f[4];
         if (turn) {
