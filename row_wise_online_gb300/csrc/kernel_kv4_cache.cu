@@ -199,47 +199,53 @@ __global__ void __launch_bounds__(kCacheThreads) k_kv4_gather(GatherArgs a) {
 // lookups are made once for the block and whole words move.  The blocks that the call's tokens touch form one list over
 // the sequences, cut into equal parts, one a CTA; each CTA finds its part by a scan over the sequences.
 
-// The blocks of sequence b's new tokens: positions [len - n, len).  Tokens before the sequence's start have none.
+// The blocks of sequence b's new tokens: positions [len - n, len).  Tokens before the sequence's start have none, nor has
+// a sequence whose length or offsets are out of range.
 struct RunSeq {
   Kv4Seq s;
   int first, blocks;  // first block, how many
 };
 __device__ __forceinline__ RunSeq run_seq(const Kv4View& c, int b, bool& bad) {
   RunSeq r;
-  r.s = kv4_seq(c, b, bad);
+  bool wrong = false;
+  r.s = kv4_seq(c, b, wrong);
   const int p0 = r.s.len - r.s.n;
-  if (p0 < 0) bad = true;
+  bad |= wrong || p0 < 0;
   r.first = max(p0, 0) / kKv4Block;
-  r.blocks = r.s.n > 0 && r.s.len > 0 ? (r.s.len - 1) / kKv4Block - r.first + 1 : 0;
+  r.blocks = !wrong && r.s.n > 0 && r.s.len > 0 ? (r.s.len - 1) / kKv4Block - r.first + 1 : 0;
   return r;
 }
 
 // Calls f(sequence, block of it, sub-task) for the units of this warp, `subs` a block; this CTA is number `part` of `parts`.
 template <class F>
 __device__ __forceinline__ void for_units(const Kv4View& c, int subs, int part, int parts, F f) {
-  __shared__ int scan[kCacheThreads / 32];
+  __shared__ int64_t scan[kCacheThreads / 32];
   __shared__ int where[2];  // sequence, first unit of it
-  __shared__ int taken;         // units of this CTA's part that warps have taken: they take turns, as units differ in work
+  __shared__ int taken;     // units of this CTA's part that warps have taken: they take turns, as units differ in work
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (c.batch + kCacheThreads - 1) / kCacheThreads, b0 = min(tid * per, c.batch), b1 = min(b0 + per, c.batch);
   bool bad = false;
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += run_seq(c, b, bad).blocks * subs;
-  if (bad && part == 0) kv4_bad(c);
-  int upto = mine;
+  int64_t sum = 0;
+  for (int b = b0; b < b1; ++b) sum += int64_t(run_seq(c, b, bad).blocks) * subs;
+  int64_t upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kFull, upto, o);
+    const int64_t x = __shfl_up_sync(kFull, upto, o);
     if (lane >= o) upto += x;
   }
   if (lane == 31) scan[warp] = upto;
   if (tid == 0) taken = kCacheThreads / 32;
   __syncthreads();
-  int total = 0, before = upto - mine;
+  int64_t all = 0, below = upto - sum;
   for (int w = 0; w < kCacheThreads / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
+    if (w < warp) below += scan[w];
+    all += scan[w];
   }
+  // Offsets that ascend give fewer units than 2^31 (the host saw to that); where some descend, sequences overlap and may not.
+  const bool many = all >= (int64_t(1) << 31);
+  if ((bad || many) && part == 0) kv4_bad(c);
+  if (many) return;
+  const int total = int(all), before = int(below), mine = int(sum);
   const int u0 = int(int64_t(total) * part / parts), u1 = int(int64_t(total) * (part + 1) / parts);
   if (u0 >= u1) return;
   if (u0 >= before && u0 < before + mine) {
@@ -613,8 +619,9 @@ int grid_for(int64_t warps, const DeviceInfo& dev) {
   return int(blocks < most ? blocks : most);
 }
 
-// Runs of at least 4 tokens a sequence on average go by blocks of 16, fewer by single rows.
-// Units are counted in 32 bits.
+// Runs of at least 4 tokens a sequence on average go by blocks of 16, fewer by single rows: a block's lookups and the scan
+// are shared by its tokens.  (128 sequences of 1 token: 2.2 us read back by rows; 154480 tokens in 4 sequences: 375 by rows,
+// 131 by blocks.)  Units are counted in 32 bits.
 int64_t run_units(const Kv4View& c, int subs) { return (c.tokens / kKv4Block + 2 * int64_t(c.batch)) * subs; }
 bool in_runs(const Kv4View& c, int subs) { return c.cu && c.tokens >= 4 * int64_t(c.batch) && run_units(c, subs) < (int64_t(1) << 31); }
 // There a lane's eight elements have their partners in one other lane: rot / 2 is a multiple of 8, or pairs are neighbours.

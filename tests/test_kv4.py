@@ -330,6 +330,54 @@ def test_bad_pages_lengths_and_offsets_are_reported():
         assert rwo.get_status() == rwo.ERR_INVALID_ARG
 
 
+def test_bad_lengths_among_runs_of_tokens():
+    """The same where sequences bring many tokens: one too long for its table, one of negative length, one shorter than its
+    rows, a page that is none, positions without angles."""
+    d, heads = 128, 2
+    lens, news = [40, 40, 40, 40, 90], [20, 20, 20, 30, 90]
+    c, table = pool([40, 40, 40, 40, 90], heads, 16, d, seed=5)
+    table[3, 1] = 10 ** 6
+    cu, told = dev(cu_of(news)), [10 ** 6, -7, 9, 40, 90]
+    before = torch.from_numpy(c.data).cuda()
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn(180, heads, d, generator=gen, device="cuda").to(BF) for _ in range(2))
+    q = torch.randn(180, 3, d, generator=gen, device="cuda").to(BF)
+    cs = torch.ones(80, 64, device="cuda")
+    data, out = before.clone(), torch.full((180, 3, d), 5.0, dtype=BF, device="cuda")
+    rwo.kv4_append(k, v, data, dev(table), dev(told), cu_tokens=cu, q=q, q_out=out, cos_sin=cs)
+    assert rwo.get_status() == rwo.ERR_INVALID_ARG
+    # sequence 2 (9 tokens for 20 rows): its last 9 rows; 3: positions 10 .. 15 and 32 ..; 4: positions below 80
+    written = [i for i in range(180) if 51 <= i < 60 or 60 <= i < 66 or 82 <= i < 90 or 90 <= i < 170]
+    where = [(2, i - 51) for i in range(51, 60)] + [(3, 10 + i - 60) for i in range(60, 66)] + \
+            [(3, 10 + i - 60) for i in range(82, 90)] + [(4, i - 90) for i in range(90, 170)]
+    kf, vf, ones = k.float().cpu().numpy(), v.float().cpu().numpy(), np.ones(64, np.float32)
+    for i, (b, pos) in zip(written, where):
+        for h in range(heads):
+            c.put(table[b], pos, h, rotate(kf[i, h], ones, False), vf[i, h])
+    assert np.array_equal(data.cpu().numpy(), c.data)
+    touched = (out != 5).flatten(1).any(1).cpu().numpy()
+    assert list(np.flatnonzero(touched)) == written
+    ks, vs = (torch.full((180, heads, d), 5.0, dtype=BF, device="cuda") for _ in range(2))
+    rwo.kv4_gather(data, dev(table), dev(told), cu_tokens=cu, k=ks, v=vs)
+    assert rwo.get_status() == rwo.ERR_INVALID_ARG
+    touched = (ks != 5).flatten(1).any(1).cpu().numpy()
+    assert list(np.flatnonzero(touched)) == written + list(range(170, 180))  # (reading back needs no angles)
+
+
+def test_offsets_that_descend_do_not_overflow():
+    """Offsets 0, T, 0, T, ...: half of the sequences claim every row, more units than 32 bits count."""
+    T, B, heads, d = 200000, 20000, 16, 64
+    data = rwo.kv4_cache_empty(1, heads, T, d)
+    k = torch.zeros(T, heads, d, dtype=BF, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = T
+    lens = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    table = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    rwo.kv4_append(k, k, data, table, lens, cu_tokens=cu)
+    assert rwo.get_status() == rwo.ERR_INVALID_ARG
+    assert not data.any()
+
+
 def test_binding_errors():
     data = rwo.kv4_cache_empty(4, 2, 16, 64)
     tab, ln = dev([[0]]), dev([3])
