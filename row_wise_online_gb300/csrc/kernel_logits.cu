@@ -28,7 +28,7 @@
 namespace rwo {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kMostThreads = 512;
 constexpr uint32_t kSeen = 1u << 31;
 constexpr uint32_t kCount = (1u << 20) - 1;
 constexpr uint32_t kField = 2047u << 20;
@@ -48,9 +48,9 @@ struct Args {
 };
 
 struct Smem {
-  State warp[kThreads / 32];
+  State warp[kMostThreads / 32];
   State ranks[kMaxCluster];
-  int sums[kThreads / 32];
+  int sums[kMostThreads / 32];
   int twice;  // some token has several biases
   int pad[3];
 };
@@ -86,8 +86,8 @@ __device__ __forceinline__ uint4 only(uint4 v, uint32_t bits) {
 
 enum { kLogits = 0, kSoftmax = 1, kLogSoftmax = 2 };
 
-template <class D, int OUT>
-__global__ void __launch_bounds__(kThreads, 2) k_logits(const __grid_constant__ Args a) {
+template <class D, int OUT, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   constexpr int V = D::kVec;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
@@ -405,11 +405,20 @@ cudaError_t launch_for(const LogitsProblem& p, const DeviceInfo& dev) {
   a.map_words = counted ? (a.chunk * D::kVec + 32 + D::kVec + 31) / 32 : 0;
   a.mask_words = p.mask || counted ? a.chunk * D::kVec / 32 + 3 : 0;
   using Kern = void (*)(Args);
-  const Kern kern = p.out == kLogits ? (Kern)k_logits<D, kLogits> : p.out == kSoftmax ? (Kern)k_logits<D, kSoftmax> : (Kern)k_logits<D, kLogSoftmax>;
+  // Clusters of four and more take CTAs of 256 threads, of which more clusters are resident at once (37 rows of 131072 bf16
+  // logits over clusters of 8: 14 us against 22 with 512 threads); fewer, larger parts are better served by 512 (100 rows over
+  // clusters of 2: 25 against 26; 256 rows, one CTA each: 44 against 58, with 1000 tokens of history).
+  const bool few = log2 >= 2;
+  const Kern kern = few ? (p.out == kLogits    ? (Kern)k_logits<D, kLogits, 256>
+                           : p.out == kSoftmax ? (Kern)k_logits<D, kSoftmax, 256>
+                                               : (Kern)k_logits<D, kLogSoftmax, 256>)
+                        : (p.out == kLogits    ? (Kern)k_logits<D, kLogits, 512>
+                           : p.out == kSoftmax ? (Kern)k_logits<D, kSoftmax, 512>
+                                               : (Kern)k_logits<D, kLogSoftmax, 512>);
   // the kernel's limits are set once per device
   constexpr int kDevices = 64;
-  static std::atomic<bool> ready[kDevices][3];
-  std::atomic<bool>& done = ready[dev.device % kDevices][p.out];
+  static std::atomic<bool> ready[kDevices][6];
+  std::atomic<bool>& done = ready[dev.device % kDevices][p.out * 2 + (few ? 1 : 0)];
   if (!done.load(std::memory_order_acquire)) {
     cudaError_t err = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            int(smem_bytes(kMaxListed, kMaxChunk / 32 + 4, kMaxChunk / 32 + 3, kMaxBias)));
@@ -419,7 +428,7 @@ cudaError_t launch_for(const LogitsProblem& p, const DeviceInfo& dev) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.M << log2));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(few ? 256 : 512);
   cfg.dynamicSmemBytes = smem_bytes(a.listed, a.map_words, a.mask_words, p.bias_count);
   cfg.stream = p.stream;
   cudaLaunchAttribute attr[1];
