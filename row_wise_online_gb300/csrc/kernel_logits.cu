@@ -16,9 +16,12 @@
 //     bits 20-30: bias_count - index of its first bias (integer maximum);  bit 31: in the prompt;  bits 0-19: c
 // (integer sums: the order of the atomics does not matter) and then the masked l before scale, worked out once, one token
 // a thread.  Streaming treats listed tokens as masked; their values join the state from the list, and their outputs are
-// written over the streamed ones at the end.  So a streamed element costs a mask bit and nothing else (256 rows of 131072
-// bf16 logits with 8192 tokens of history, 64 biases and a mask: 62 us; looking each vector up in the map, in both
-// passes, 72).  The scale is folded into the exponent.  Biases of one token add up in the order of the list.
+// written over the streamed ones at the end.  So a streamed element costs a mask bit and nothing else: 256 rows of 131072
+// bf16 logits with 8192 tokens of history, 64 biases and a mask take 59 us (11 more when each vector is looked up in the
+// map, in both passes).  The lists are 18 of these and the mask 10; the bytes alone would be 22.  Latency bounds it: with
+// two CTAs of 512 threads on an SM, one's work on its lists is covered only by the other's streaming.  (Fetching the part
+// into L2 while the lists are looked through: 61; the streaming then waits for the same bytes.)
+// The scale is folded into the exponent.  Biases of one token add up in the order of the list.
 // Where the listed tokens of a part may be more than shared memory holds, the part is taken in chunks.
 #include <atomic>
 
@@ -117,10 +120,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
   const float scale = p.scale ? __ldg(p.scale + r) : 1.f, slope = __fmul_rn(scale, kLog2e);
   const bool masked = a.mask_words > 0;
 
-  if (tid == 0 && v1 > v0) {  // the part on its way to L2 while the lists are looked through
-    const unsigned char* from = x + (int64_t(v0) * V + front) * D::kBytes;
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(uint32_t(min(v1 - v0, kMaxChunk / V)) * 16u) : "memory");
-  }
   int listed = 0;  // tokens on the chunk's list
   // The listed tokens among vectors [c0, c0 + n) and this part's single elements.  Place of element id in the map: 32 for
   // the first vector's first, the elements before it below that.
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
 template <class D>
 cudaError_t launch_for(const LogitsProblem& p, const DeviceInfo& dev) {
   // One CTA a row where that gives every SM one; else more while a CTA's part is above 2048 elements.  (256 rows of 131072
-  // bf16 logits: one CTA a row 62 us, two 70: a row's lists are looked through by each of its CTAs.)
+  // bf16 logits: one CTA a row 59 us, two 70: a row's lists are looked through by each of its CTAs.)
   const int64_t vecs = (p.N + D::kVec - 1) / D::kVec;
   int log2 = 0;
   while ((1 << log2) < kMaxCluster && (p.M << log2) < dev.sm_count && (p.N >> log2) > 4096) ++log2;
