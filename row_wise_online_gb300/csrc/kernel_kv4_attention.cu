@@ -4,7 +4,11 @@
 // j that the token sees, k_j = s c + z and v_j = s c + z per group of 32 elements; LSE = m ln 2 + ln l.
 //
 // What bounds it: the cache is read once (1.25 d bytes a token and head), every query head of a key/value head shares
-// the read, so HBM bandwidth is the floor; the work per byte (two products, 4-bit codes) has to stay below it.
+// the read, so HBM bandwidth is the floor; the work per byte (two products, 4-bit codes) has to stay below it.  Measured:
+// 8 query heads a key/value head, d = 128, one token each: 2 x 131072 keys 109 us (floor 99), 64 x 4608 keys on average
+// 126 (110): 0.87-0.91 of the copy rate.  d = 64 with 8 rows a head is bound by instruction issue (64 sequences: 83 us, floor 55),
+// and so are 16 rows and more (32 sequences of 4 drafted tokens, 32 rows: d = 64 62 us, floor 12; d = 128 91, floor 25):
+// for a score the scales, the exponent and the conversion cost more slots than the two products.
 //
 // * The products take codes, not values.  A code at bit 0 or 4 of a half word is the fp16 subnormal c 2^-24 or c 2^-20
 //   (exact), so A operands are made with one AND each, and the powers of two go into the other operand or the
@@ -19,9 +23,9 @@
 //   cancels; l, for the LSE, sums the weights before rounding, in fp32.
 // * A weight is p = 2^(score + mb), fp16 for the product: mb puts the running maximum at 2^(9 - e) and moves only when a
 //   score exceeds it by 2^6, or a scale of V exceeds 2^e (e = 0 at first, so V up to 15 in magnitude), so that p s stays
-//   below 2^15.  One vote per 32 keys replaces a maximum over lanes.  fp16's rounding is 2^-11 of a weight (bf16 would
+//   below 2^15.  One vote per 32 or 64 keys replaces a maximum over lanes.  fp16's rounding is 2^-11 of a weight (bf16 would
 //   be 2^-8); weights down to 2^-33 of the largest still count.
-// * A CTA is 4 consumer warps and a producer warp, which keeps a ring of stages (cp.async.bulk of one or two blocks per
+// * A CTA is 4 consumer warps and a producer warp, which keeps a ring of stages (cp.async.bulk of one to four blocks per
 //   consumer warp) ahead of them.  The tiles of all sequences and heads form one list, cut into equal runs, one per
 //   resident CTA: long and short sequences mix without imbalance.  A run that ends inside a (sequence, head) leaves its
 //   state (m, l, O) in the workspace; a second kernel merges such states in the order of the runs.

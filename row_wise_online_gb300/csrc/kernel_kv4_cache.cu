@@ -8,7 +8,10 @@
 // k_kv4_gather: s c + z of the same tokens, rounded once to bf16 or fp16.
 //
 // A row (one head of one token) is d / 4 lanes of 4 elements; a group is 8 lanes, its minimum and maximum three
-// shuffles.  Both are bound by the bytes that they move.
+// shuffles.  Few tokens are taken row by row, where latency bounds (128 rows: 4.7 us in, 2.2 back); longer runs a block of 16
+// tokens at a time, so that the cache is touched in whole blocks.  Reading back is bound by bytes: 154480 tokens of 8 heads of
+// 128 take 131 us (floor 123).  Writing is bound by issue and bytes alike (58% and 47% busy): 15714 tokens of 8 heads of 128
+// with 32 rotated query heads take 85 us (the bytes alone 52).
 #include "kv4.cuh"
 
 namespace rwo {
