@@ -5,9 +5,9 @@
 //
 // What bounds it: the cache is read once (1.25 d bytes a token and head), every query head of a key/value head shares
 // the read, so HBM bandwidth is the floor; the work per byte (two products, 4-bit codes) has to stay below it.  Measured:
-// 8 query heads a key/value head, d = 128, one token each: 2 x 131072 keys 109 us (floor 99), 64 x 4608 keys on average
-// 126 (110): 0.87-0.91 of the copy rate.  d = 64 with 8 rows a head is bound by instruction issue (64 sequences: 83 us, floor 55),
-// and so are 16 rows and more (32 sequences of 4 drafted tokens, 32 rows: d = 64 62 us, floor 12; d = 128 91, floor 25):
+// 8 query heads a key/value head, d = 128, one token each: 2 x 131072 keys 107 us (floor 99), 64 x 4608 keys on average
+// 125 (110): 0.88-0.92 of the copy rate.  d = 64 with 8 rows a head is bound by instruction issue (64 sequences: 82 us, floor 55),
+// and so are 16 rows and more (32 sequences of 4 drafted tokens, 32 rows: d = 64 62 us, floor 12; d = 128 89, floor 25):
 // for a score the scales, the exponent and the conversion cost more slots than the two products.
 //
 // * The products take codes, not values.  A code at bit 0 or 4 of a half word is the fp16 subnormal c 2^-24 or c 2^-20
@@ -84,6 +84,24 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Two fp32 operations an instruction, on neighbours of an accumulator: what does not go through the matrix pipe is short of
+// issue slots (16 rows a head, d = 128: 214 -> 211 us; one token, 8 rows: 126.4 -> 124.6).
+__device__ __forceinline__ void fma2(float& x0, float& x1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(x0), "=f"(x1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& x0, float& x1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(x0), "=f"(x1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float& x0, float& x1, float a0, float a1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(a0), "f"(a1));
+}
+
 // n consecutive 32-bit words.
 template <int n>
 __device__ __forceinline__ void words_at(uint32_t (&w)[n], const unsigned char* p) {
@@ -113,7 +131,7 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4View& c, int b, int group, 
   SeqWork w;
   w.s = kv4_seq(c, b, bad);
   w.row_blocks = (w.s.n * group + R - 1) / R;
-  w.tiles = (w.s.len + KEYS - 1) / KEYS;
+  w.tiles = int((unsigned(w.s.len) + KEYS - 1) / KEYS);
   if (w.tiles < 1) w.tiles = 1;
   return w;
 }
@@ -443,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
             float z[4];
             mma8_first(z, kza, kzb, qz[i]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) S[kb][i][q] = z[q] * 0x1p-24f;
+            for (int q = 0; q < 4; q += 2) mul2(S[kb][i][q], S[kb][i][q + 1], z[q], z[q + 1], 0x1p-24f, 0x1p-24f);
           }
 #pragma unroll
           for (int j = 0; j < G; ++j) {
@@ -454,10 +472,8 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
               float d[4];
               mma16_first(d, wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, wa[j] & 0x00f000f0u, wb[j] & 0x00f000f0u, qf[i][2 * j][0], qf[i][2 * j][1]);
               mma16(d, ua & 0x000f000fu, ub & 0x000f000fu, ua & 0x00f000f0u, ub & 0x00f000f0u, qf[i][2 * j + 1][0], qf[i][2 * j + 1][1]);
-              S[kb][i][0] = fmaf(sa, d[0], S[kb][i][0]);
-              S[kb][i][1] = fmaf(sa, d[1], S[kb][i][1]);
-              S[kb][i][2] = fmaf(sb, d[2], S[kb][i][2]);
-              S[kb][i][3] = fmaf(sb, d[3], S[kb][i][3]);
+              fma2(S[kb][i][0], S[kb][i][1], sa, sa, d[0], d[1], S[kb][i][0], S[kb][i][1]);
+              fma2(S[kb][i][2], S[kb][i][3], sb, sb, d[2], d[3], S[kb][i][2], S[kb][i][3]);
             }
           }
         }
@@ -484,8 +500,7 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
           for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int q = 0; q < 4; q += 2) {
-              p[kb][i][q] = fmaf(S[kb][i][q], ch[i][0], mb[i][0]);
-              p[kb][i][q + 1] = fmaf(S[kb][i][q + 1], ch[i][1], mb[i][1]);
+              fma2(p[kb][i][q], p[kb][i][q + 1], S[kb][i][q], S[kb][i][q + 1], ch[i][0], ch[i][1], mb[i][0], mb[i][1]);
               ptop = fmaxf(ptop, fmaxf(p[kb][i][q], p[kb][i][q + 1]));
             }
         }
@@ -537,10 +552,9 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              p[kb][i][q] = ex2(p[kb][i][q]);
-              l[i][q & 1] += p[kb][i][q];
-            }
+            for (int q = 0; q < 4; ++q) p[kb][i][q] = ex2(p[kb][i][q]);
+            add2(l[i][0], l[i][1], p[kb][i][0], p[kb][i][1]);
+            add2(l[i][0], l[i][1], p[kb][i][2], p[kb][i][3]);
             pb[i][0] = transposed(pack_f16x2(p[kb][i][0], p[kb][i][1]));
             pb[i][1] = transposed(pack_f16x2(p[kb][i][2], p[kb][i][3]));
           }
