@@ -17,10 +17,10 @@
 // (integer sums: the order of the atomics does not matter) and then the masked l before scale, worked out once, one token
 // a thread.  Streaming treats listed tokens as masked; their values join the state from the list, and their outputs are
 // written over the streamed ones at the end.  So a streamed element costs a mask bit and nothing else: 256 rows of 131072
-// bf16 logits with 8192 tokens of history, 64 biases and a mask take 59 us (11 more when each vector is looked up in the
-// map, in both passes).  The lists are 18 of these and the mask 10; the bytes alone would be 22.  Latency bounds it: with
+// bf16 logits with 8192 tokens of history, 64 biases and a mask take 57 us (11 more when each vector is looked up in the
+// map, in both passes).  The lists are 17 of these and the mask 10; the bytes alone would be 22.  Latency bounds it: with
 // two CTAs of 512 threads on an SM, one's work on its lists is covered only by the other's streaming.  (Fetching the part
-// into L2 while the lists are looked through: 61; the streaming then waits for the same bytes.)
+// into L2 while the lists are looked through: 2 more; the streaming then waits for the same bytes.)
 // The scale is folded into the exponent.  Biases of one token add up in the order of the list.
 // Where the listed tokens of a part may be more than shared memory holds, the part is taken in chunks.
 #include <atomic>
@@ -120,25 +120,40 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
   const float scale = p.scale ? __ldg(p.scale + r) : 1.f, slope = __fmul_rn(scale, kLog2e);
   const bool masked = a.mask_words > 0;
 
-  int listed = 0;  // tokens on the chunk's list
+  int n_tokens = 0, n_prompt = 0;
+  if (toks) {
+    n_tokens = __ldg(p.token_lens + r);
+    n_prompt = p.prompt_lens ? __ldg(p.prompt_lens + r) : 0;
+  }
+  int listed = 0, base = 0, e0 = 0, e1 = 0;  // tokens on the chunk's list; element of place 0; the chunk's elements
+  // f(i, id) for this thread's tokens i, id = -1 behind the last.  Some are loaded at once: sixteen and no branches where rows
+  // are many (256 rows: 57.7 us against 58.3 with them), four where they are few and a launch fetches its instructions anew
+  // (one row: 8.6 us against 9.0 with sixteen).
+  auto each_token = [&](auto f) {
+    constexpr bool kMany = kThreads == kMostThreads;
+    constexpr int kAhead = kMany ? 16 : 4;
+    for (int i0 = tid; i0 < n_tokens; i0 += kAhead * kThreads) {
+      int ahead[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) ahead[k] = i0 + k * kThreads < n_tokens ? __ldg(toks + i0 + k * kThreads) : -1;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (!kMany && i0 + k * kThreads >= n_tokens) break;
+        f(i0 + k * kThreads, ahead[k]);
+      }
+    }
+  };
+  auto number = [&](int at) { return int(below[at >> 5]) + __popc(map[at >> 5] & ((1u << (at & 31)) - 1u)); };
   // The listed tokens among vectors [c0, c0 + n) and this part's single elements.  Place of element id in the map: 32 for
   // the first vector's first, the elements before it below that.
   auto lists = [&](int c0, int n) {
-    constexpr int kAhead = 16;
-    int ahead[kAhead];  // the first tokens are on their way while shared memory is cleared, without waiting for their count
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) ahead[k] = toks && tid + k * kThreads < p.token_pitch ? __ldg(toks + tid + k * kThreads) : -1;
-    int n_tokens = 0, n_prompt = 0;
-    if (toks) {
-      n_tokens = __ldg(p.token_lens + r);
-      n_prompt = p.prompt_lens ? __ldg(p.prompt_lens + r) : 0;
-      if (n_tokens < 0 || n_tokens > p.token_pitch || n_prompt < 0 || n_prompt > n_tokens) {
-        if (tid == 0) atomicOr(a.status, kStatusBadIndex);
-        n_tokens = n_tokens < 0 ? 0 : n_tokens > p.token_pitch ? int(p.token_pitch) : n_tokens;
-      }
+    if (n_tokens < 0 || n_tokens > p.token_pitch || n_prompt < 0 || n_prompt > n_tokens) {
+      if (tid == 0) atomicOr(a.status, kStatusBadIndex);
+      n_tokens = n_tokens < 0 ? 0 : n_tokens > p.token_pitch ? int(p.token_pitch) : n_tokens;
     }
-    const int base = front + c0 * V - 32;  // element of place 0
-    const int e0 = rank == 0 && c0 == v0 ? 0 : base + 32, e1 = rank == ranks - 1 && c0 + n == v1 ? N : base + 32 + n * V;
+    base = front + c0 * V - 32;
+    e0 = rank == 0 && c0 == v0 ? 0 : base + 32;
+    e1 = rank == ranks - 1 && c0 + n == v1 ? N : base + 32 + n * V;
     const int used = (n * V + 32 + V + 31) / 32;  // of the map's words
     __syncthreads();  // the last chunk's have been read
     for (int i = tid; i < used; i += kThreads) map[i] = 0u;
@@ -157,23 +172,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
       if (here) set(id - base);
       if (id >= N) atomicOr(a.status, kStatusBadIndex);
     }
-    auto each_token = [&](auto f) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int i = tid + k * kThreads;
-        if (i < n_tokens && ahead[k] >= e0 && ahead[k] < e1) f(i, ahead[k]);
-      }
-#pragma unroll 4
-      for (int i = tid + kAhead * kThreads; i < n_tokens; i += kThreads) {
-        const int id = __ldg(toks + i);
-        if (id >= e0 && id < e1) f(i, id);
-        else if (id >= N) atomicOr(a.status, kStatusBadIndex);
-      }
-    };
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (tid + k * kThreads < n_tokens && ahead[k] >= N) atomicOr(a.status, kStatusBadIndex);
-    each_token([&](int, int id) { set(id - base); });
+    each_token([&](int, int id) {
+      if (id >= e0 && id < e1) set(id - base);
+      else if (id >= N) atomicOr(a.status, kStatusBadIndex);
+    });
     __syncthreads();
     // the running count: every thread a run of words
     const int each = (used + kThreads - 1) / kThreads, w0 = min(tid * each, used), w1 = min(w0 + each, used);
@@ -199,7 +201,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
       before += __popc(map[w]);
     }
     __syncthreads();
-    auto number = [&](int at) { return int(below[at >> 5]) + __popc(map[at >> 5] & ((1u << (at & 31)) - 1u)); };
+  };
+  // Their counts, and from these their values.
+  auto values = [&] {
     if (p.bias_count) {
       for (int i = tid; i < p.bias_count; i += kThreads)
         if (bias_id[i] >= 0) {
@@ -213,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
       // (counts, added from here on, leave that field alone)
     }
     each_token([&](int i, int id) {
+      if (id < e0 || id >= e1) return;
       const int k = number(id - base);
       ids[k] = id;
       if (i < n_prompt) atomicOr(&words[k], kSeen);
@@ -309,7 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
   for (int c = 0; c < a.chunks; ++c) {
     const int c0 = min(v0 + c * a.chunk, v1), n = min(a.chunk, v1 - c0);
     if (c > 0 && n == 0) break;
-    if (a.listed) lists(c0, n);
+    if (a.listed) {
+      lists(c0, n);
+      values();
+    }
     if (masked) masks(c0, n);
     auto one = [&](float l) { s = merge(s, State{l, l == -INFINITY ? 0.f : 1.f}, slope); };
     stream(
@@ -357,7 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
   for (int c = 0; c < a.chunks; ++c) {
     const int c0 = min(v0 + c * a.chunk, v1), n = min(a.chunk, v1 - c0);
     if (c > 0 && n == 0) break;
-    if (a.listed && a.chunks > 1) lists(c0, n);
+    if (a.listed && a.chunks > 1) {
+      lists(c0, n);
+      values();
+    }
     if (masked && a.chunks > 1) masks(c0, n);
     stream(
         c0, n,
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
 template <class D>
 cudaError_t launch_for(const LogitsProblem& p, const DeviceInfo& dev) {
   // One CTA a row where that gives every SM one; else more while a CTA's part is above 2048 elements.  (256 rows of 131072
-  // bf16 logits: one CTA a row 59 us, two 70: a row's lists are looked through by each of its CTAs.)
+  // bf16 logits: one CTA a row 57 us, two 70: a row's lists are looked through by each of its CTAs.)
   const int64_t vecs = (p.N + D::kVec - 1) / D::kVec;
   int log2 = 0;
   while ((1 << log2) < kMaxCluster && (p.M << log2) < dev.sm_count && (p.N >> log2) > 4096) ++log2;
