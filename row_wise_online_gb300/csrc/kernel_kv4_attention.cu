@@ -5,9 +5,9 @@
 //
 // What bounds it: the cache is read once (1.25 d bytes a token and head), every query head of a key/value head shares
 // the read, so HBM bandwidth is the floor; the work per byte (two products, 4-bit codes) has to stay below it.  Measured:
-// 8 query heads a key/value head, d = 128, one token each: 2 x 131072 keys 107 us (floor 99), 64 x 4608 keys on average
+// 8 query heads a key/value head, d = 128, one token each: 2 x 131072 keys 107 us (floor 99), 64 x 9000 keys on average
 // 125 (110): 0.88-0.92 of the copy rate.  d = 64 with 8 rows a head is bound by instruction issue (64 sequences: 82 us, floor 55),
-// and so are 16 rows and more (32 sequences of 4 drafted tokens, 32 rows: d = 64 62 us, floor 12; d = 128 89, floor 25):
+// and so are 16 rows and more (16 sequences of 8191 keys and 4 drafted tokens, 32 rows: d = 64 62 us, floor 12; d = 128 89, floor 25):
 // for a score the scales, the exponent and the conversion cost more slots than the two products.
 //
 // * The products take codes, not values.  A code at bit 0 or 4 of a half word is the fp16 subnormal c 2^-24 or c 2^-20
@@ -734,7 +734,11 @@ template <bool H, int DH>
 Plan plan_of(bool wide) {
   return wide ? plan_as<H, DH, 2, 2>() : plan_as<H, DH, 1, 256 / DH>();
 }
-// Tiles of 8 query rows, or of 16 where a sequence has more rows to a key/value head than 8 on average.
+// Tiles of 8 query rows, or of 16 where a sequence has more rows to a key/value head than 8 on average: a tile's rows share
+// what a code costs (32 rows a head, d = 64: 62 us with tiles of 16, 83 with 8; d = 128: 91 against 113; tiles of 32 run out
+// of registers, 85).  A warp takes 32 keys at once; at d = 64 with 8 rows, 64, in three CTAs an SM (82 us against 95 with 32
+// keys in four or five).  CTAs without a producer, each warp copying its own blocks, make room for a fourth, which
+// is slower: what the registers spill no longer stays in L1 (d = 64, 16 rows: 62 -> 96 us).
 Plan plan_for(int64_t batch, int64_t tokens, int q_heads, int heads, int d, int dtype) {
   const bool wide = tokens * (q_heads / heads) > 8 * batch;
   if (d == 64) return dtype == 2 ? plan_of<true, 64>(wide) : plan_of<false, 64>(wide);
