@@ -6,8 +6,8 @@
 // What bounds it: the cache is read once (1.25 d bytes a token and head), every query head of a key/value head shares
 // the read, so HBM bandwidth is the floor; the work per byte (two products, 4-bit codes) has to stay below it.  Measured:
 // 8 query heads a key/value head, d = 128, one token each: 2 x 131072 keys 107 us (floor 99), 64 x 9000 keys on average
-// 125 (110): 0.88-0.92 of the copy rate.  d = 64 with 8 rows a head is bound by instruction issue (64 sequences: 82 us, floor 55),
-// and so are 16 rows and more (16 sequences of 8191 keys and 4 drafted tokens, 32 rows: d = 64 62 us, floor 12; d = 128 89, floor 25):
+// 125 (110): 0.88-0.92 of the copy rate.  d = 64 with 8 rows a head is bound by instruction issue (64 sequences: 79 us, floor 55),
+// and so are 16 rows and more (16 sequences of 8191 keys and 4 drafted tokens, 32 rows: d = 64 61 us, floor 12; d = 128 90, floor 25):
 // for a score the scales, the exponent and the conversion cost more slots than the two products.
 //
 // * The products take codes, not values.  A code at bit 0 or 4 of a half word is the fp16 subnormal c 2^-24 or c 2^-20
@@ -347,59 +347,58 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
   int slot = 0;
   uint32_t lap = 0;
   bool first = true;
+  constexpr int E = DH / 32;  // elements of a row a lane, E lane .. E lane + E - 1
   while (left > 0) {
     const int here = int(left < at.w.tiles - at.tile ? left : at.w.tiles - at.tile);
     const int n = at.w.s.n, len = at.w.s.len, row0 = at.rb * R;
     // Q rows of the item as operand fragments; row r is head h G + r % G of token r / G
-    for (int r = warp; r < R; r += kWarps) {
-      const int rr = row0 + r;
-      float x[DH / 32];
-      constexpr int E = DH / 32;  // elements a lane, E lane .. E lane + E - 1
-      if (rr < n * a.group) {
-        const int tok = rr / a.group, hd = at.h * a.group + rr - tok * a.group;
-        const unsigned char* p = static_cast<const unsigned char*>(a.q.p) + (int64_t(at.w.s.start + tok) * a.q.token + int64_t(hd) * a.q.head) * 2 + lane * E * 2;
-        if constexpr (E == 4) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-          x[0] = elem_to_f32<H>(w.x, 0);
-          x[1] = elem_to_f32<H>(w.x, 1);
-          x[2] = elem_to_f32<H>(w.y, 0);
-          x[3] = elem_to_f32<H>(w.y, 1);
-        } else {
-          const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
-          x[0] = elem_to_f32<H>(w, 0);
-          x[1] = elem_to_f32<H>(w, 1);
+    // (A warp's rows are loaded at once: 16 rows a head 210 -> 206 us, d = 64 82 -> 79; at d = 128 with 8 rows one by one,
+    // where more registers cost the loop over the keys 1%.)
+    constexpr int kOnce = NT == 1 && DH == 128 ? 1 : R / kWarps;
+#pragma unroll 1
+    for (int r0 = warp; r0 < R; r0 += kOnce * kWarps) {
+      uint32_t rows[kOnce][E / 2];
+#pragma unroll
+      for (int k = 0; k < kOnce; ++k) {
+        const int rr = row0 + r0 + k * kWarps, tok = rr / a.group, hd = at.h * a.group + rr - tok * a.group;
+        const unsigned char* p = static_cast<const unsigned char*>(a.q.p) + (int64_t(at.w.s.start + tok) * a.q.token + int64_t(hd) * a.q.head) * 2;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) rows[k][e] = tok < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + lane * (E / 2) + e) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < kOnce; ++k) {
+        const int r = r0 + k * kWarps;
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = elem_to_f32<H>(rows[k][e / 2], e & 1);
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) mx = fmaxf(mx, fabsf(x[i]));
+        // the row's power of two: the largest element lands in [2^5, 2^6)
+        const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(mx));
+        int ex = int(top >> 23) - 127;
+        ex = ex < -90 ? -90 : ex > 90 ? 90 : ex;
+        const float to = pow2(5 - ex);
+        if (lane == 0) reinterpret_cast<float*>(smem + SM::kOffRow)[r] = a.scale * pow2(ex - 5 + 24);
+        float sum = 0.f;
+        __half* qf = reinterpret_cast<__half*>(smem + SM::kOffQ);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int e = lane * E + i, j = e >> 5, w = e & 31, tt = w >> 3, nn = w & 7;
+          const __half hv = __float2half_rn(x[i] * to * ((nn & 1) ? 0.0625f : 1.f));
+          qf[(((((r >> 3) * 2 * G + 2 * j + ((nn & 3) >> 1)) * 32 + (r & 7) * 4 + tt) * 2 + (nn & 1)) * 2) + (nn >> 2)] = hv;
+          sum += __half2float(hv) * ((nn & 1) ? 16.f : 1.f);
         }
-      } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = 0.f;
-      }
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) mx = fmaxf(mx, fabsf(x[i]));
-      // the row's power of two: the largest element lands in [2^5, 2^6)
-      const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(mx));
-      int ex = int(top >> 23) - 127;
-      ex = ex < -90 ? -90 : ex > 90 ? 90 : ex;
-      const float to = pow2(5 - ex);
-      if (lane == 0) reinterpret_cast<float*>(smem + SM::kOffRow)[r] = a.scale * pow2(ex - 5 + 24);
-      float sum = 0.f;
-      __half* qf = reinterpret_cast<__half*>(smem + SM::kOffQ);
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int e = lane * E + i, j = e >> 5, w = e & 31, tt = w >> 3, nn = w & 7;
-        const __half hv = __float2half_rn(x[i] * to * ((nn & 1) ? 0.0625f : 1.f));
-        qf[(((((r >> 3) * 2 * G + 2 * j + ((nn & 3) >> 1)) * 32 + (r & 7) * 4 + tt) * 2 + (nn & 1)) * 2) + (nn >> 2)] = hv;
-        sum += __half2float(hv) * ((nn & 1) ? 16.f : 1.f);
-      }
-#pragma unroll
-      for (int o = 1; o < 32 / G; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      if (lane % (32 / G) == 0) {
-        const int j = lane / (32 / G);
-        const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
-        __half* qz = reinterpret_cast<__half*>(smem + SM::kOffQz) + ((r >> 3) * 32 + (r & 7) * 4) * 2;
-        qz[j] = hi;
-        qz[G + j] = lo;
-        if (G == 2) qz[4 + j] = qz[6 + j] = __ushort_as_half(0);
+        for (int o = 1; o < 32 / G; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        if (lane % (32 / G) == 0) {
+          const int j = lane / (32 / G);
+          const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
+          __half* qz = reinterpret_cast<__half*>(smem + SM::kOffQz) + ((r >> 3) * 32 + (r & 7) * 4) * 2;
+          qz[j] = hi;
+          qz[G + j] = lo;
+          if (G == 2) qz[4 + j] = qz[6 + j] = __ushort_as_half(0);
+        }
       }
     }
     named_barrier_sync(1, kWarps * 32);
@@ -637,7 +636,6 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
           s[w] = ml[w * R + i * 8 + r];
           sum.x = fminf(sum.x, s[w].x);
         }
-        constexpr int E = DH / 32;
         float x[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = 0.f;
@@ -736,7 +734,7 @@ Plan plan_of(bool wide) {
 }
 // Tiles of 8 query rows, or of 16 where a sequence has more rows to a key/value head than 8 on average: a tile's rows share
 // what a code costs (32 rows a head, d = 64: 62 us with tiles of 16, 83 with 8; d = 128: 91 against 113; tiles of 32 run out
-// of registers, 85).  A warp takes 32 keys at once; at d = 64 with 8 rows, 64, in three CTAs an SM (82 us against 95 with 32
+// of registers, 85).  A warp takes 32 keys at once; at d = 64 with 8 rows, 64, in three CTAs an SM (then 82 us against 95 with 32
 // keys in four or five).  CTAs without a producer, each warp copying its own blocks, make room for a fourth, which
 // is slower: what the registers spill no longer stays in L1 (d = 64, 16 rows: 62 -> 96 us).
 Plan plan_for(int64_t batch, int64_t tokens, int q_heads, int heads, int d, int dtype) {
