@@ -6,8 +6,8 @@
 // What bounds it: the cache is read once (1.25 d bytes a token and head), every query head of a key/value head shares
 // the read, so HBM bandwidth is the floor; the work per byte (two products, 4-bit codes) has to stay below it.  Measured:
 // 8 query heads a key/value head, d = 128, one token each: 2 x 131072 keys 107 us (floor 99), 64 x 9000 keys on average
-// 125 (110): 0.88-0.92 of the copy rate.  d = 64 with 8 rows a head is bound by instruction issue (64 sequences: 79 us, floor 55),
-// and so are 16 rows and more (16 sequences of 8191 keys and 4 drafted tokens, 32 rows: d = 64 61 us, floor 12; d = 128 90, floor 25):
+// 121 (110): 0.91-0.92 of the copy rate.  d = 64 with 8 rows a head is bound by instruction issue (64 sequences: 72 us, floor 55),
+// and so are 16 rows and more (16 sequences of 8191 keys and 4 drafted tokens, 32 rows: d = 64 60 us, floor 12; d = 128 88, floor 25):
 // for a score the scales, the exponent and the conversion cost more slots than the two products.
 //
 // * The products take codes, not values.  A code at bit 0 or 4 of a half word is the fp16 subnormal c 2^-24 or c 2^-20
@@ -27,7 +27,7 @@
 //   be 2^-8); weights down to 2^-33 of the largest still count.
 // * A CTA is 4 consumer warps and a producer warp, which keeps a ring of stages (cp.async.bulk of one to four blocks per
 //   consumer warp) ahead of them.  The tiles of all sequences and heads form one list, cut into equal runs, one per
-//   resident CTA: long and short sequences mix without imbalance.  A run that ends inside a (sequence, head) leaves its
+//   resident CTA: long and short sequences mix without imbalance (an item's own start and end count as two tiles).  A run that ends inside a (sequence, head) leaves its
 //   state (m, l, O) in the workspace; a second kernel merges such states in the order of the runs.
 // Every wait is bounded; a wait that runs out sets the status word.
 #include <atomic>
@@ -49,10 +49,11 @@ struct AttnArgs {
   float* lse;        // [tokens][q_heads] or null
   int q_heads, group;
   float scale;       // scale * log2 e
-  int64_t* prefix;   // [batch + 1]: first tile of each sequence in the list (workspace)
+  int64_t* prefix;   // [batch + 1]: first place of each sequence in the list (workspace)
   float4* part_l;    // [2 grid][rows]: mb, l, sum of the rounded weights
   float* part_o;     // [2 grid][rows][d]
   int runs;          // CTAs of the main kernel
+  int lead;          // places before an item's tiles in the list
   uint64_t wait_ns;
 };
 
@@ -135,14 +136,16 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4View& c, int b, int group, 
   if (w.tiles < 1) w.tiles = 1;
   return w;
 }
-__device__ __forceinline__ int64_t seq_tiles(const SeqWork& w, int heads) { return int64_t(heads) * w.row_blocks * w.tiles; }
+// The list has `lead` places before each (sequence, head, block of rows)'s tiles, for the time that its start and its end take
+// (queries, merge): runs of equal length then take equal time.
+__device__ __forceinline__ int64_t seq_places(const SeqWork& w, int heads, int lead) { return int64_t(heads) * w.row_blocks * (w.tiles + lead); }
 
-// The list of W tiles is cut into `n` runs: run i is [first(i), first(i + 1)).
+// The list of W places is cut into `n` runs: run i is [first(i), first(i + 1)).
 struct Runs {
   int64_t W;
   int n;
   __device__ __forceinline__ int64_t first(int i) const { return W * i / n; }
-  __device__ __forceinline__ int of(int64_t tile) const { return int(((tile + 1) * n - 1) / W); }
+  __device__ __forceinline__ int of(int64_t place) const { return int(((place + 1) * n - 1) / W); }
 };
 __device__ __forceinline__ Runs runs_of(int64_t W, int runs) { return Runs{W, int(W < 1 ? 1 : W < runs ? W : runs)}; }
 
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
   const int per = (c.batch + 127) / 128, b0 = tid < 128 ? min(tid * per, c.batch) : c.batch, b1 = tid < 128 ? min(b0 + per, c.batch) : c.batch;
   bool bad = false;
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_tiles(seq_work<R, kKeys>(c, b, a.group, bad), c.heads);
+  for (int b = b0; b < b1; ++b) mine += seq_places(seq_work<R, kKeys>(c, b, a.group, bad), c.heads, a.lead);
   if (bad && blockIdx.x == 0) kv4_bad(c);
   int64_t before = mine;
 #pragma unroll
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
     int64_t p = before;
     for (int b = b0; b < b1; ++b) {
       a.prefix[b] = p;
-      p += seq_tiles(seq_work<R, kKeys>(c, b, a.group, bad), c.heads);
+      p += seq_places(seq_work<R, kKeys>(c, b, a.group, bad), c.heads, a.lead);
     }
     if (tid == 0) a.prefix[c.batch] = W;
   }
@@ -269,13 +272,13 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
     int64_t p = before;
     for (int b = b0; b < b1; ++b) {
       const SeqWork w = seq_work<R, kKeys>(c, b, a.group, bad);
-      const int64_t n = seq_tiles(w, c.heads);
+      const int64_t n = seq_places(w, c.heads, a.lead);
       if (run0 < p + n) {
-        const int64_t x = run0 - p, item = x / w.tiles;
+        const int64_t x = run0 - p, item = x / (w.tiles + a.lead);
         start[0] = b;
         start[1] = int(item / w.row_blocks);
         start[2] = int(item % w.row_blocks);
-        start[3] = int(x - item * w.tiles);
+        start[3] = int(x - item * (w.tiles + a.lead)) - a.lead;
         break;
       }
       p += n;
@@ -286,9 +289,10 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
   at.b = start[0];
   at.h = start[1];
   at.rb = start[2];
-  at.tile = start[3];
+  at.tile = max(start[3], 0);
   at.w = seq_work<R, kKeys>(c, at.b, a.group, bad);
-  int64_t left = run1 - run0;  // tiles of the run that remain
+  int64_t left = run1 - run0 + min(start[3], 0);  // of the run: tiles of this item, and the places behind it
+  if (left <= 0) return;
   bool timed_out = false;
 
   if (warp == kWarps) {
@@ -317,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
       // whole blocks of the tile that hold a key
       const int blocks = max(0, min(SM::kBlocks, (at.w.s.len + kKv4Block - 1) / kKv4Block - at.tile * SM::kBlocks));
       if (--left > 0) {
-        if (++at.tile == at.w.tiles) next_item<R, kKeys>(at, c, a.group);
-        off = block_of();
+        if (++at.tile == at.w.tiles && (left -= a.lead) > 0) next_item<R, kKeys>(at, c, a.group);
+        if (left > 0) off = block_of();
       }
       if (issued >= kStages && !mbar_wait(empty(slot), lap ^ 1u, a.wait_ns)) timed_out = true;
       if (lane == 0) {
@@ -662,21 +666,25 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
     }
     first = false;
     left -= here;
+    if (left > 0) left -= a.lead;
     if (left > 0) next_item<R, kKeys>(at, c, a.group);
     named_barrier_sync(1, kWarps * 32);  // Q and the merge buffers are free
   }
   if (timed_out && lane == 0) atomicOr(c.status, kStatusTimeout);
 }
 
-// Merges the parts of rows whose keys were spread over several runs: `split` of a CTA's four warps a row (four where rows
-// are few, and their parts many; else one).
+// Merges the parts of rows whose keys were spread over several runs, in the order of the runs: eight warps a row, a CTA each,
+// where rows are few and their parts many (one sequence of 16384 keys, 57 parts a row: 15.2 us with four warps, 13.8 with
+// eight; sixteen 13.3, but short sequences lose 0.4), else one, four rows a CTA.
+constexpr int kMergeWarps = 8;
+constexpr int kMergeAhead = 4;  // parts that a warp loads at once
 template <bool H, int DH, int NT, int KB>
-__global__ void __launch_bounds__(128) k_attention_kv4_merge(AttnArgs a, int split) {
+__global__ void __launch_bounds__(kMergeWarps * 32) k_attention_kv4_merge(AttnArgs a, int split) {
   constexpr int E = DH / 32, R = 8 * NT, kKeys = Smem<DH, NT, KB>::kKeys;
   const Kv4View& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t x = int64_t(blockIdx.x) * (4 / split) + (split == 4 ? 0 : warp), i = x / a.q_heads;
-  const int hq = int(x - i * a.q_heads), share = split == 4 ? warp : 0;
+  const int64_t x = split > 1 ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 4 + warp, i = x / a.q_heads;
+  const int hq = int(x - i * a.q_heads), share = split > 1 ? warp : 0;
   // what the main kernel does not write is read before it is waited for
   const int b = i < c.tokens ? kv4_seq_of(c, i) : -1;
   bool bad = false;
@@ -687,34 +695,67 @@ __global__ void __launch_bounds__(128) k_attention_kv4_merge(AttnArgs a, int spl
   if (b < 0 || i < w.s.start || i >= w.s.start + w.s.n) return;
   const int h = hq / a.group, rr = int(i - w.s.start) * a.group + hq - h * a.group, rb = rr / R, r = rr - rb * R;
   const Runs runs = runs_of(a.prefix[c.batch], a.runs);
-  const int64_t t0 = a.prefix[b] + (int64_t(h) * w.row_blocks + rb) * w.tiles;
-  const int c0 = runs.of(t0), c1 = runs.of(t0 + w.tiles - 1);
+  const int64_t t0 = a.prefix[b] + (int64_t(h) * w.row_blocks + rb) * (w.tiles + a.lead);
+  const int c0 = runs.of(t0 + a.lead), c1 = runs.of(t0 + a.lead + w.tiles - 1);
   if (c0 == c1) return;  // one run held all of its keys and wrote the row
   const int late = t0 > runs.first(c0) ? 1 : 0;  // the part in run c0 is not that run's first
   float4 s = make_float4(kUnseen, 0.f, 0.f, 0.f);
   float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  auto add = [&](float4 v, const float* p) {
-    const float mb = fminf(s.x, v.x), f0 = ex2(mb - s.x), f1 = ex2(mb - v.x);
-    s = make_float4(mb, fmaf(s.y, f0, v.y * f1), fmaf(s.z, f0, v.z * f1), 0.f);
+  for (int k0 = c0 + share; k0 <= c1; k0 += kMergeAhead * split) {
+    float4 v[kMergeAhead];
+    float x[kMergeAhead][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f0, p[lane * E + e] * f1);
-  };
-#pragma unroll 4
-  for (int k = c0 + share; k <= c1; k += split) {
-    const int64_t part = int64_t(2 * k + (k == c0 ? late : 0)) * R + r;
-    add(a.part_l[part], a.part_o + part * DH);
+    for (int k = 0; k < kMergeAhead; ++k) {  // absent parts weigh nothing
+      const int run = k0 + k * split;
+      const int64_t part = int64_t(2 * run + (run == c0 ? late : 0)) * R + r;
+      v[k] = make_float4(kUnseen, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[k][e] = 0.f;
+      if (run <= c1) {
+        v[k] = a.part_l[part];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[k][e] = a.part_o[part * DH + lane * E + e];
+      }
+    }
+    float mb = s.x;
+#pragma unroll
+    for (int k = 0; k < kMergeAhead; ++k) mb = fminf(mb, v[k].x);
+    const float old = ex2(mb - s.x);
+    s = make_float4(mb, s.y * old, s.z * old, 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= old;
+#pragma unroll
+    for (int k = 0; k < kMergeAhead; ++k) {
+      const float fix = ex2(mb - v[k].x);
+      s.y = fmaf(fix, v[k].y, s.y);
+      s.z = fmaf(fix, v[k].z, s.z);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(fix, x[k][e], o[e]);
+    }
   }
-  if (split == 4) {
-    __shared__ float4 sm[4];
-    __shared__ float so[4][DH];
+  if (split > 1) {
+    __shared__ float4 sm[kMergeWarps];
+    __shared__ float so[kMergeWarps][DH];
     if (lane == 0) sm[warp] = s;
 #pragma unroll
     for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
     __syncthreads();
     if (warp) return;
-    for (int k = 1; k < 4; ++k) add(sm[k], so[k]);
+    float mb = kUnseen;
+    for (int k = 0; k < split; ++k) mb = fminf(mb, sm[k].x);
+    s = make_float4(mb, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < split; ++k) {
+      const float fix = ex2(mb - sm[k].x);
+      s.y = fmaf(fix, sm[k].y, s.y);
+      s.z = fmaf(fix, sm[k].z, s.z);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(fix, so[k][lane * E + e], o[e]);
+    }
   }
   write_row<H, DH>(a, i * a.q_heads + hq, lane, o, s);
 }
@@ -789,6 +830,11 @@ cudaError_t launch_attention_kv4(const Kv4View& c, const Kv4Rows& q, void* o, fl
   a.scale = scale * kLog2e;
   a.runs = per_sm * dev.sm_count;
   a.wait_ns = exchange_wait_limit_ns();
+  // Two places where a run is likely to hold several (sequence, head, block of rows)s (64 ragged sequences of 8 heads: 126 -> 121 us,
+  // d = 64 79 -> 72; 128 of at most 700 keys 29 -> 23; 16 rows a head 203 -> 187, with one place 194); none where it is one or
+  // two of a few (one sequence of 16384 keys: 13.8 us, with two 14.4).
+  const int64_t items = c.heads * (c.batch > c.tokens * a.group / p.rows ? int64_t(c.batch) : c.tokens * a.group / p.rows);
+  a.lead = 2 * items >= a.runs ? 2 : 0;
   unsigned char* w = static_cast<unsigned char*>(scratch);
   const size_t parts = size_t(2) * a.runs * p.rows;
   a.prefix = reinterpret_cast<int64_t*>(w);
@@ -801,9 +847,9 @@ cudaError_t launch_attention_kv4(const Kv4View& c, const Kv4Rows& q, void* o, fl
   // the merge is launched while the last runs finish, and waits for them itself
   cudaLaunchConfig_t cfg = {};
   const int64_t rows = c.tokens * q_heads;
-  const int split = rows <= 4 * int64_t(dev.sm_count) ? 4 : 1;
-  cfg.gridDim = dim3(unsigned((rows + 4 / split - 1) / (4 / split)));
-  cfg.blockDim = dim3(128);
+  const int split = rows <= 4 * int64_t(dev.sm_count) ? kMergeWarps : 1;
+  cfg.gridDim = dim3(unsigned(split > 1 ? rows : (rows + 3) / 4));
+  cfg.blockDim = dim3(split > 1 ? kMergeWarps * 32 : 128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
