@@ -27,8 +27,9 @@
 //   be 2^-8); weights down to 2^-33 of the largest still count.
 // * A CTA is 4 consumer warps and a producer warp, which keeps a ring of stages (cp.async.bulk of one to four blocks per
 //   consumer warp) ahead of them.  The tiles of all sequences and heads form one list, cut into equal runs, one per
-//   resident CTA: long and short sequences mix without imbalance (an item's own start and end count as two tiles).  A run that ends inside a (sequence, head) leaves its
-//   state (m, l, O) in the workspace; a second kernel merges such states in the order of the runs.
+//   resident CTA: long and short sequences mix without imbalance (an item's own start and end count as two tiles).  A
+//   run that ends inside a (sequence, head) leaves its state (m, l, O) in the workspace; a second kernel merges such
+//   states in the order of the runs.
 // Every wait is bounded; a wait that runs out sets the status word.
 #include <atomic>
 

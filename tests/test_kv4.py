@@ -256,6 +256,17 @@ def test_many_sequences():
     check_attention(c, table, lens, [1] * 300, 2, FP, seed=8, cu_given=False)
 
 
+@pytest.mark.parametrize("dt,d,group", [(BF, 128, 8), (FP, 128, 16), (BF, 64, 4), (BF, 64, 16)])
+@pytest.mark.parametrize("most,batch", [(900, 150), (3000, 60)])
+def test_many_ragged_sequences(most, batch, dt, d, group):
+    """More (sequence, head)s than runs, of one to many tiles: runs that start and end at any place, and some between."""
+    rng = np.random.default_rng(most + d + group)
+    lens = [int(n) for n in rng.integers(0, most, batch)]
+    news = [int(n) for n in rng.integers(0, 4, batch)]
+    c, table = pool(lens, 4, 32, d, seed=batch, width=-(-most // 32))
+    check_attention(c, table, lens, news, 4 * group, dt, seed=group)
+
+
 def test_results_do_not_change_from_call_to_call():
     lens = [5000, 700]
     c, table = pool(lens, 2, 16, 128, seed=4)
