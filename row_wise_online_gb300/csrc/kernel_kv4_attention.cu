@@ -86,6 +86,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// a b + c, rounded once.
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 // Two fp32 operations an instruction, on neighbours of an accumulator: what does not go through the matrix pipe is short of
 // issue slots (16 rows a head, d = 128: 214 -> 211 us; one token, 8 rows: 126.4 -> 124.6).
 __device__ __forceinline__ void fma2(float& x0, float& x1, float a0, float a1, float b0, float b1, float c0, float c1) {
@@ -589,7 +595,9 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
             const uint32_t ua = va[j] >> 8, ub = vb[j] >> 8;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-              const uint32_t p0 = hmul2(pb[i][0], vs[0][j]), p1 = hmul2(pb[i][1], vs[1][j]);
+              const uint32_t p0 = hmul2(pb[i][0], vs[0][j]);
+              // fp16 results show these roundings: what one loses, the next takes up
+              const uint32_t p1 = H ? hfma2(pb[i][1], vs[1][j], hfma2(pb[i][0], vs[0][j], p0 ^ 0x80008000u)) : hmul2(pb[i][1], vs[1][j]);
               mma16(O[i][2 * j], va[j] & 0x000f000fu, va[j] & 0x00f000f0u, vb[j] & 0x000f000fu, vb[j] & 0x00f000f0u, p0, p1);
               mma16(O[i][2 * j + 1], ua & 0x000f000fu, ua & 0x00f000f0u, ub & 0x000f000fu, ub & 0x00f000f0u, p0, p1);
             }
