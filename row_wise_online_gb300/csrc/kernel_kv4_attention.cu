@@ -607,6 +607,13 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
             vz[f] = word_at(blk + B::kVZero + ((4 * f + t) * G + g % G) * 4);
             if (g >= G) vz[f] = g == G ? 0x3c003c00u : 0u;
           }
+          uint32_t takes[NT];  // halves whose second token has a weight
+#pragma unroll
+          for (int i = 0; i < NT; ++i) takes[i] = kFull;
+          if (H && tail) {  // (0 times the code of an unseen token is 0: a remainder times it would not be)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) takes[i] = (pb[i][1] & 0xffffu ? 0xffffu : 0u) | (pb[i][1] >> 16 ? 0xffff0000u : 0u);
+          }
           if (tail) {  // a slot that holds no token counts with zero
             const int live = len - key0 - kb * kKv4Block;
 #pragma unroll
@@ -625,8 +632,9 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
               const uint32_t p0 = hmul2(pb[i][0], vs[0][j]);
-              // fp16 results show these roundings: what one loses, the next takes up
-              const uint32_t p1 = H ? hfma2(pb[i][1], vs[1][j], hfma2(pb[i][0], vs[0][j], p0 ^ 0x80008000u)) : hmul2(pb[i][1], vs[1][j]);
+              // fp16 results show these roundings: what one loses, the next takes up, if the row sees its token
+              const uint32_t p1 = H ? hfma2(pb[i][1], vs[1][j], hfma2(pb[i][0] & takes[i], vs[0][j], (p0 ^ 0x80008000u) & takes[i]))
+                                    : hmul2(pb[i][1], vs[1][j]);
               mma16(O[i][2 * j], va[j] & 0x000f000fu, va[j] & 0x00f000f0u, vb[j] & 0x000f000fu, vb[j] & 0x00f000f0u, p0, p1);
               mma16(O[i][2 * j + 1], ua & 0x000f000fu, ua & 0x00f000f0u, ub & 0x000f000fu, ub & 0x00f000f0u, p0, p1);
             }

@@ -6,7 +6,7 @@ import torch
 
 import row_wise_online_gb300 as rwo
 from kv4_reference import Cache
-from test_kv4 import BF, cu_of, dev, pool
+from test_kv4 import BF, FP, cu_of, dev, pool
 
 pytestmark = pytest.mark.gpu
 SHAPES = [(128, 2, 1), (128, 2, 8), (128, 1, 16), (64, 2, 4), (64, 1, 12)]  # d, kv heads, query heads of each
@@ -50,7 +50,7 @@ def results(data, table, lens, news, q):
 
 
 @pytest.mark.parametrize("d,heads,group", SHAPES)
-@pytest.mark.parametrize("dt", [BF])
+@pytest.mark.parametrize("dt", [BF, FP])
 @pytest.mark.parametrize("drafts", [1, 3])
 def test_slots_that_hold_no_token(drafts, dt, d, heads, group):
     rng = np.random.default_rng(d + group)
@@ -69,7 +69,7 @@ def test_slots_that_hold_no_token(drafts, dt, d, heads, group):
 
 
 @pytest.mark.parametrize("d,heads,group", SHAPES)
-@pytest.mark.parametrize("dt", [BF])
+@pytest.mark.parametrize("dt", [BF, FP])
 @pytest.mark.parametrize("change", ["codes of values", "keys and values", "queries"])
 def test_later_tokens(change, dt, d, heads, group):
     lens = [9, 33, 64, 100, 260, 700, 131, 1500, 40, 18]
