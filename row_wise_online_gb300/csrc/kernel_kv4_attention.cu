@@ -49,7 +49,7 @@ struct AttnArgs {
   unsigned char* o;  // [tokens][q_heads][d]
   float* lse;        // [tokens][q_heads] or null
   int q_heads, group;
-  float scale;       // scale * log2 e
+  float scale;
   int64_t* prefix;   // [batch + 1]: first place of each sequence in the list (workspace)
   float4* part_l;    // [2 grid][rows]: mb, l, sum of the rounded weights
   float* part_o;     // [2 grid][rows][d]
@@ -394,9 +394,11 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
         // the row's power of two: the largest element lands in [2^5, 2^6)
         const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(mx));
         int ex = int(top >> 23) - 127;
-        ex = ex < -90 ? -90 : ex > 90 ? 90 : ex;
+        ex = ex < -122 ? -122 : ex;
         const float to = pow2(5 - ex);
-        if (lane == 0) reinterpret_cast<float*>(smem + SM::kOffRow)[r] = a.scale * pow2(ex - 5 + 24);
+        // (neither 0 nor infinite, so that -inf, where a key is hidden, stays -inf, and 0, where q is, 0)
+        const float factor = a.scale * pow2(ex) * (kLog2e * 0x1p19f);
+        if (lane == 0) reinterpret_cast<float*>(smem + SM::kOffRow)[r] = fminf(fmaxf(factor, 0x1p-126f), 0x1.fffffep127f);
         float sum = 0.f;
         __half* qf = reinterpret_cast<__half*>(smem + SM::kOffQ);
 #pragma unroll
@@ -873,7 +875,7 @@ cudaError_t launch_attention_kv4(const Kv4View& c, const Kv4Rows& q, void* o, fl
   a.lse = lse;
   a.q_heads = q_heads;
   a.group = q_heads / c.heads;
-  a.scale = scale * kLog2e;
+  a.scale = scale;
   a.runs = per_sm * dev.sm_count;
   a.wait_ns = exchange_wait_limit_ns();
   // Two places where a run is likely to hold several (sequence, head, block of rows)s (64 ragged sequences of 8 heads: 126 -> 121 us,
