@@ -249,7 +249,15 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
   const int per = (c.batch + 127) / 128, b0 = tid < 128 ? min(tid * per, c.batch) : c.batch, b1 = tid < 128 ? min(b0 + per, c.batch) : c.batch;
   bool bad = false;
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_places(seq_work<R, kKeys>(c, b, a.group, bad), c.heads, a.lead);
+  bool down = false;
+  for (int b = b0; b < b1; ++b) {
+    const SeqWork w = seq_work<R, kKeys>(c, b, a.group, bad);
+    mine += seq_places(w, c.heads, a.lead);
+    down |= w.s.down;
+  }
+  // Where offsets descend, sequences claim the same rows, up to batch times the work of the call: more places than a call has
+  // are taken off, the sum is negative, and no row is worked on.
+  if (down) mine = -(int64_t(1) << 55);
   if (bad && blockIdx.x == 0) kv4_bad(c);
   int64_t before = mine;
 #pragma unroll
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Runs runs = runs_of(W, a.runs);
-  if (W == 0 || int(blockIdx.x) >= runs.n) return;
+  if (W <= 0 || int(blockIdx.x) >= runs.n) return;
   const int64_t run0 = runs.first(blockIdx.x), run1 = runs.first(blockIdx.x + 1);
   if (tid < 128 && run0 >= before && run0 < before + mine) {
     int64_t p = before;
@@ -741,9 +749,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_attention_kv4_merge(AttnAr
   if (b >= 0) w = seq_work<R, kKeys>(c, b, a.group, bad);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (b < 0 || i < w.s.start || i >= w.s.start + w.s.n) return;
+  const int64_t W = a.prefix[c.batch], p0 = a.prefix[b];
+  if (W <= 0) return;
   const int h = hq / a.group, rr = int(i - w.s.start) * a.group + hq - h * a.group, rb = rr / R, r = rr - rb * R;
-  const Runs runs = runs_of(a.prefix[c.batch], a.runs);
-  const int64_t t0 = a.prefix[b] + (int64_t(h) * w.row_blocks + rb) * (w.tiles + a.lead);
+  const Runs runs = runs_of(W, a.runs);
+  const int64_t t0 = p0 + (int64_t(h) * w.row_blocks + rb) * (w.tiles + a.lead);
   const int c0 = runs.of(t0 + a.lead), c1 = runs.of(t0 + a.lead + w.tiles - 1);
   if (c0 == c1) return;  // one run held all of its keys and wrote the row
   const int late = t0 > runs.first(c0) ? 1 : 0;  // the part in run c0 is not that run's first

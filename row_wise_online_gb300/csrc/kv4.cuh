@@ -40,14 +40,17 @@ struct Kv4Block {
 // `bad`): nothing is read or written for them.
 struct Kv4Seq {
   int start, n, len;
+  bool down;  // the next offset is smaller
 };
 __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4View& c, int b, bool& bad) {
   Kv4Seq s;
   s.len = __ldg(c.lens + b);
+  s.down = false;
   if (c.cu) {
     const int lo = __ldg(c.cu + b), hi = __ldg(c.cu + b + 1);
     s.start = lo;
     s.n = hi - lo;
+    s.down = hi < lo;
     if (lo < 0 || hi < lo || hi > c.tokens) {
       bad = true;
       s.start = s.n = 0;
