@@ -373,7 +373,7 @@ __device__ __forceinline__ uint32_t quantised8(float2 (&x)[4], __half& sh, __hal
     lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
   }
-  if (lo < -65504.f || hi > 65504.f) {
+  if (!(lo >= -65504.f && hi <= 65504.f)) {  // (a group of NaN alone too: scales and zeros are finite, whatever comes in)
     lo = limited(lo);
     hi = limited(hi);
 #pragma unroll

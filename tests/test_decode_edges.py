@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import row_wise_online_gb300 as rwo
-from test_kv4 import BF, check_attention, pool
+from test_kv4 import BF, FP, check_attention, dev, pool
 
 pytestmark = pytest.mark.gpu
 
@@ -24,6 +24,40 @@ def test_scales_and_queries_far_from_one(q_sd, scale, d, group):
     lens = [900, 33, 2000]
     c, table = pool(lens, 2, 16, d, seed=d)
     check_attention(c, table, lens, [1, 3, 2], 2 * group, BF, seed=3, q_sd=q_sd, scale=scale)
+
+
+@pytest.mark.parametrize("runs", [False, True])
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("d,group", [(128, 4), (64, 2)])
+def test_tokens_that_are_not_numbers(d, group, dt, runs):
+    """A last token of NaN and infinities: the cache stays finite, the bytes of every other group and the rows of every
+    other token what they are without it."""
+    n, heads = 40, 2
+    gen = torch.Generator().manual_seed(d)
+    k, v = (torch.randn(n, heads, d, generator=gen).to(dt).cuda() for _ in range(2))
+    q = torch.randn(4, heads * group, d, generator=gen).to(dt).cuda()
+    table, lens = dev([[2, 0, 1]]), dev([n])
+    held, out = [], []
+    for bad in (False, True):
+        cache = rwo.kv4_cache_empty(3, heads, 16, d)
+        rwo.kv4_append(k[:n - 1], v[:n - 1], cache, table, lens - 1, cu_tokens=dev([0, n - 1]))
+        kk, vv = k.clone(), v.clone()
+        if bad:
+            kk[n - 1, 0, :] = float("nan")
+            vv[n - 1, 0, :32] = float("nan")
+            vv[n - 1, 0, 32:64] = float("inf")
+            vv[n - 1, 1, 3] = float("nan")
+            vv[n - 1, 1, 34] = -float("inf")
+        if runs:  # many tokens a sequence: the last ones are written again
+            rwo.kv4_append(kk[n - 9:], vv[n - 9:], cache, table, lens, cu_tokens=dev([0, 9]))
+        else:
+            rwo.kv4_append(kk[n - 1:], vv[n - 1:], cache, table, lens)
+        held.append([t[:n - 1] for t in rwo.kv4_gather(cache, table, lens, cu_tokens=dev([0, n]), num_tokens=n, dtype=dt)])
+        assert np.isfinite(cache.cpu().numpy().view(np.float16)[..., 8 * d:]).all()
+        out.append(rwo.attention_kv4(q, cache, table, lens, cu_tokens=dev([0, 4])))
+        assert rwo.get_status() == rwo.OK
+    assert all(torch.equal(a, b) for a, b in zip(*held))
+    assert torch.equal(out[0][:3], out[1][:3])
 
 
 def test_offsets_that_descend_are_not_worked_on():
