@@ -1,7 +1,7 @@
 // kernel_logits.cu -- penalties, biases and masks on logits, fused with the softmax that follows.
 //
 // For token j of row r, with c the times it was generated and "seen" whether it is in the prompt or was generated:
-//     l = x;  seen: l = l > 0 ? l / repetition (times the rounded reciprocal) : l repetition;
+//     l = x;  seen: l = l > 0 ? l / repetition : l repetition;
 //     c > 0: l -= frequency c + presence;  l += biases;  l *= scale;  mask bit clear: l = -inf
 // and y = l, softmax(l) or log softmax(l) with the row's online (m, d) state.
 //
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
       if (i < n_prompt) atomicOr(&words[k], kSeen);
       else atomicAdd(&words[k], 1u);
     });
-    const float rep = p.repetition ? __ldg(p.repetition + r) : 1.f, rep_inv = __frcp_rn(rep);
+    const float rep = p.repetition ? __ldg(p.repetition + r) : 1.f;
     const float freq = p.frequency ? __ldg(p.frequency + r) : 0.f, pres = p.presence ? __ldg(p.presence + r) : 0.f;
     __syncthreads();
 #pragma unroll 4
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logits(const __gr
       const int id = ids[i];
       const uint32_t w = words[i], c = w & kCount;
       float l = D::load1(x, id);
-      if ((w & kSeen) || c) l = __fmul_rn(l, l > 0.f ? rep_inv : rep);
+      if ((w & kSeen) || c) l = l > 0.f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
       if (c) l = __fsub_rn(l, __fadd_rn(__fmul_rn(freq, float(c)), pres));
       if (const int field = int((w & kField) >> 20)) {
         const int first = p.bias_count - field;

@@ -60,6 +60,23 @@ def test_tokens_that_are_not_numbers(d, group, dt, runs):
     assert torch.equal(out[0][:3], out[1][:3])
 
 
+@pytest.mark.parametrize("repetition", [1.3, 0.7, 1e-41, 3e38])
+def test_repetition_divides(repetition):
+    """A seen logit above zero is divided, one below multiplied: the fp32 quotient and product, to the last bit."""
+    M, N = 3, 4097
+    gen = torch.Generator().manual_seed(1)
+    x = 3 * torch.randn(M, N, generator=gen)
+    x[0, :9] = torch.tensor([1e-45, -1e-45, 1e-39, -1e-39, 0.0, 3e38, -3e38, 1e-3, 7.0])
+    rep = torch.full((M,), repetition)
+    tokens = torch.arange(N, dtype=torch.int32).repeat(M, 1)
+    y = rwo.logits_process_rows(x.cuda(), out="logits", tokens=tokens.cuda(), token_lens=dev([N] * M), repetition=rep.cuda())
+    assert rwo.get_status() == rwo.OK
+    r = rep.numpy()[:, None]
+    with np.errstate(over="ignore"):
+        want = np.where(x.numpy() > 0, x.numpy() / r, x.numpy() * r)
+    assert np.array_equal(y.cpu().numpy(), want)
+
+
 def test_offsets_that_descend_are_not_worked_on():
     """Offsets 0, T, 0, T, ...: half of the sequences claim every row.  Reported, and no row is written."""
     T, B, heads, d = 20000, 2000, 4, 64
