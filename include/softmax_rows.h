@@ -301,8 +301,10 @@ int kv4_append(const kv4_cache* cache, const kv4_rows* k, const kv4_rows* v, con
 
 /*
  * kv4_gather -- the values s * c + z of this call's tokens (whole sequences where n_b = seq_lens[b]),
- * rounded once to the element type: what attention_forward takes for a prompt whose prefix is in the cache.
- * k and v: [tokens][heads][head_dim], written.
+ * rounded once to the element type.  k and v: [tokens][heads][head_dim], written.
+ * For a prompt whose prefix is in the cache, attention_forward takes such keys and values as [heads][n][head_dim], one
+ * length for a call and a key/value head for each query head: read back with head strides of tokens * head_dim, then make
+ * a call for each sequence, its heads repeated q_heads / heads times, with causal = 1.
  */
 int kv4_gather(const kv4_cache* cache, const kv4_rows* k, const kv4_rows* v, int dtype, void* stream);
 

@@ -191,6 +191,7 @@ def kv4_gather(cache, page_table, seq_lens, cu_tokens=None, num_tokens: int | No
 
     Returns (k, v), [num_tokens, kv_heads, d] in ``dtype`` (default bf16) unless given; num_tokens defaults to
     the given k's rows, or to one a sequence.  Rows that belong to no sequence are left as they were.
+    attention_forward takes them a sequence at a time, [heads, n, d], heads repeated for their query heads.
     """
     import torch
 
