@@ -353,6 +353,7 @@ int64_t attention_kv4_workspace(int64_t batch, int64_t tokens, int64_t q_heads, 
  *   bias_ids, bias_values -- int32 and fp32 [M][bias_count], negative ids count as absent; at most 1024.
  *   mask        -- 32-bit words [M][ld_mask] (0: ceil(N / 32)), bit j % 32 of word j / 32 is set where j is
  *                  allowed; NULL: all.
+ * Every pointer is aligned to its elements (else SOFTMAX_ERR_MISALIGNED).
  * A token or bias id >= N is ignored, and softmax_get_status returns SOFTMAX_ERR_INVALID_ARG, as it does
  * for lengths outside 0 <= prompt <= all <= token_width (which are limited to that range).
  * Arithmetic is fp32; the results do not depend on the order in which the GPU counts.

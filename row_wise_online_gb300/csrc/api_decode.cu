@@ -166,6 +166,11 @@ int logits_process_rows(const logits_rows* a, int64_t M, int64_t N, int dtype, i
   if (a->token_width > 0 && a->tokens && !a->token_lens) return SOFTMAX_ERR_INVALID_ARG;
   if (a->bias_count > 0 && (!a->bias_ids || !a->bias_values)) return SOFTMAX_ERR_INVALID_ARG;
   if (!aligned(a->x, uintptr_t(s)) || !aligned(a->y, uintptr_t(s))) return SOFTMAX_ERR_MISALIGNED;
+  for (const void* p : {static_cast<const void*>(a->lse_out), static_cast<const void*>(a->tokens), static_cast<const void*>(a->prompt_lens),
+                        static_cast<const void*>(a->token_lens), static_cast<const void*>(a->repetition), static_cast<const void*>(a->frequency),
+                        static_cast<const void*>(a->presence), static_cast<const void*>(a->bias_ids), static_cast<const void*>(a->bias_values),
+                        static_cast<const void*>(a->mask), static_cast<const void*>(a->scale)})
+    if (!aligned(p, 4)) return SOFTMAX_ERR_MISALIGNED;
   const DeviceInfo* dev = nullptr;
   int st = current_device(&dev);
   if (st != SOFTMAX_OK) return st;
