@@ -254,7 +254,9 @@ int attention_forward(const void* q, const void* k, const void* v, void* o, floa
  * Values on the device cannot be checked before the launch.  A page, length, position or offset out
  * of its range is never followed: it is recorded (softmax_get_status returns
  * SOFTMAX_ERR_INVALID_ARG), a row of kv4_append or kv4_gather concerned is skipped, and the sequence's
- * rows of attention_kv4 are undefined.
+ * rows of attention_kv4 are undefined.  Where offsets descend, attention_kv4 writes no row at all.
+ * A sequence that brings more rows than it has tokens has rows at positions below 0: kv4_append and
+ * kv4_gather record and skip them; in attention_kv4 they see no key, and nothing is recorded.
  */
 typedef struct kv4_cache {
   void* data;                /* 16-byte aligned */
@@ -291,7 +293,8 @@ enum kv4_flags { KV4_FLAG_NEIGHBOURS = 1 /* rotate pairs (2 i, 2 i + 1) instead 
  * Quantisation of a group x of 32 (fp32 arithmetic, every operation rounded by itself, so a host can
  * reproduce the bytes): x limited to +-65504, z = fp16(min x), s = fp16((max x - min x) / 15),
  * c = (x - z) / s rounded to the nearest integer (ties to even) and limited to 0 .. 15, 0 where s = 0.
- * Non-finite inputs give unspecified values in their own group only.
+ * Non-finite inputs give unspecified values in their own group, and in the group of the element that
+ * they are rotated with; scales and zeros in the cache are finite whatever comes in.
  * Every token needs a place of its own: two tokens of one call that fall on one place of one page
  * leave it with bytes of either.  head_dim other than 64 and 128, fp32 and sizes beyond 2^31 rows
  * or positions return SOFTMAX_ERR_UNSUPPORTED.
@@ -311,8 +314,10 @@ int kv4_gather(const kv4_cache* cache, const kv4_rows* k, const kv4_rows* v, int
 /*
  * attention_kv4 -- O = softmax(scale Q K^T) V of this call's tokens over the cache, query head h with
  * key/value head h / (q_heads / heads).  Row i at position p sees the keys at positions 0 .. p, so the
- * call's own tokens must be in the cache (kv4_append) first.
- *   q         -- [tokens][q_heads][head_dim], bf16 or fp16; finite.
+ * call's own tokens must be in the cache (kv4_append) first.  Its bits depend on nothing else that the
+ * cache or q holds: not on later tokens, other rows, or bytes where no token lies.  (Scales and zeros of
+ * the sequence's tokens are finite, as kv4_append leaves them.)
+ *   q         -- [tokens][q_heads][head_dim], bf16 or fp16; finite, with |scale q.k| below 10^6.
  *   o         -- [tokens][q_heads][head_dim], contiguous, written.
  *   lse_out   -- fp32 [tokens][q_heads]: m + ln l of each row (natural log, of scale Q K^T), or NULL.
  *   q_heads   -- a multiple of heads.
@@ -321,8 +326,12 @@ int kv4_gather(const kv4_cache* cache, const kv4_rows* k, const kv4_rows* v, int
  *                no other call uses until this one is done (calls that may run at the same time, captured
  *                graphs among them, need one each).  Nothing in it is kept from call to call.
  * Built for a few tokens a sequence (decoding, drafts): any number is right, but a long prompt runs
- * faster through attention_forward on 16-bit keys and values.  Scores and row states are fp32; weights are
- * rounded to fp16 for the product with V.  A row that sees no key gets o = 0, LSE = -inf.
+ * faster through attention_forward on 16-bit keys and values.  Scores and row states are fp32.  For the
+ * product with V a weight is rounded to fp16, and so is its product with a scale of V: 2^-11 of each (in
+ * fp16 the second remainder goes on to a later token that the row sees).  The largest weight is held at
+ * 2^(9 - e) or more, 2^e the smallest power of two >= 1 not below the scales of V that the row has seen:
+ * weights down to 2^-(33 - e) of the largest count.  Scales of V below 2^-14 (values of some 10^-3 at most)
+ * lose bits of the products with small weights.  A row that sees no key gets o = 0, LSE = -inf.
  */
 int attention_kv4(const kv4_cache* cache, const kv4_rows* q, void* o, float* lse_out, int64_t q_heads, float scale, int dtype,
                   void* workspace, int64_t workspace_bytes, void* stream);

@@ -5,10 +5,12 @@
 //
 // What bounds it: the cache is read once (1.25 d bytes a token and head), every query head of a key/value head shares
 // the read, so HBM bandwidth is the floor; the work per byte (two products, 4-bit codes) has to stay below it.  Measured:
-// 8 query heads a key/value head, d = 128, one token each: 2 x 131072 keys 107 us (floor 99), 64 x 9000 keys on average
-// 121 (110): 0.91-0.92 of the copy rate.  d = 64 with 8 rows a head is bound by instruction issue (64 sequences: 72 us, floor 55),
-// and so are 16 rows and more (16 sequences of 8191 keys and 4 drafted tokens, 32 rows: d = 64 60 us, floor 12; d = 128 88, floor 25):
-// for a score the scales, the exponent and the conversion cost more slots than the two products.
+// one token each, d = 128: 2 x 262144 keys with 8 query heads a key/value head 108 us (floor 99), 64 x 9000 keys on average
+// with 4 121 (110): 0.90-0.92 of the copy rate.  With more work a byte latency bounds it: d = 64 with 8 rows a head 73 us (64
+// sequences, floor 55); 16 sequences of 8191 keys and 4 drafted tokens, 32 rows: d = 64 60 us, floor 12, d = 128 89, floor 25.
+// There (ncu, 8 of the 16, d = 64) instructions issue in 44% of the cycles and the matrix pipe is 29% busy: 12 consumer warps an
+// SM, each with one chain of product, scales, exponent, conversion and product, and 120 to 148 bytes of registers spilled
+// by tiles of 16 rows.
 //
 // * The products take codes, not values.  A code at bit 0 or 4 of a half word is the fp16 subnormal c 2^-24 or c 2^-20
 //   (exact), so A operands are made with one AND each, and the powers of two go into the other operand or the
@@ -23,8 +25,8 @@
 //   cancels; l, for the LSE, sums the weights before rounding, in fp32.
 // * A weight is p = 2^(score + mb), fp16 for the product: mb puts the running maximum at 2^(9 - e) and moves only when a
 //   score exceeds it by 2^6, or a scale of V exceeds 2^e (e = 0 at first, so V up to 15 in magnitude), so that p s stays
-//   below 2^15.  One vote per 32 or 64 keys replaces a maximum over lanes.  fp16's rounding is 2^-11 of a weight (bf16 would
-//   be 2^-8); weights down to 2^-33 of the largest still count.
+//   below 2^15.  One vote per 32 or 64 keys replaces a maximum over lanes; then each row moves by its own keys.  fp16's
+//   rounding is 2^-11 of a weight (bf16 would be 2^-8); weights down to 2^-(33 - e) of the largest still count.
 // * A CTA is 4 consumer warps and a producer warp, which keeps a ring of stages (cp.async.bulk of one to four blocks per
 //   consumer warp) ahead of them.  The tiles of all sequences and heads form one list, cut into equal runs, one per
 //   resident CTA: long and short sequences mix without imbalance (an item's own start and end count as two tiles).  A
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, Smem<DH, NT, KB>::kCtas) k_attention
         if (__any_sync(kFull, move || ptop > most)) {  // a new maximum, or larger scales: rescale what is summed so far
           // Each row moves by what it sees itself, so that its bits are the same whatever later tokens, other rows and slots that
           // hold no token hold.  (A row that does not see the last of these keys sees none after them: es need not be its own.)
-          // Rows that share their moves make fewer: 16 rows a head 188 us against 191, 4 drafted tokens d = 128 88 against 90.
+          // Rows that share their moves make fewer (4 drafted tokens a sequence, d = 128: 88 us against 89).
           int er[NT][2], e = es;
 #pragma unroll
           for (int i = 0; i < NT; ++i) er[i][0] = er[i][1] = es;

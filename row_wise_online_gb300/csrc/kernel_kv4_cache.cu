@@ -10,8 +10,9 @@
 // A row (one head of one token) is d / 4 lanes of 4 elements; a group is 8 lanes, its minimum and maximum three
 // shuffles.  Few tokens are taken row by row, where latency bounds (128 rows: 4.7 us in, 2.2 back); longer runs a block of 16
 // tokens at a time, so that the cache is touched in whole blocks.  Reading back is bound by bytes: 154480 tokens of 8 heads of
-// 128 take 131 us (floor 123).  Writing is bound by issue and bytes alike (58% and 47% busy): 15714 tokens of 8 heads of 128
-// with 32 rotated query heads take 85 us (the bytes alone 52).
+// 128 take 131 us (floor 123).  Writing is bound by latency: 15714 tokens of 8 heads of 128 with 32 rotated query heads take
+// 85 us (the bytes alone 52); half as many (ncu) keep issue 53% and DRAM 39% busy with 41% of the warps resident, which
+// wait for rows from memory more than for anything else.
 #include "kv4.cuh"
 
 namespace rwo {

@@ -18,9 +18,10 @@
 // a thread.  Streaming treats listed tokens as masked; their values join the state from the list, and their outputs are
 // written over the streamed ones at the end.  So a streamed element costs a mask bit and nothing else: 256 rows of 131072
 // bf16 logits with 8192 tokens of history, 64 biases and a mask take 57 us (11 more when each vector is looked up in the
-// map, in both passes).  The lists are 17 of these and the mask 10; the bytes alone would be 22.  Latency bounds it: with
-// two CTAs of 512 threads on an SM, one's work on its lists is covered only by the other's streaming.  (Fetching the part
-// into L2 while the lists are looked through: 2 more; the streaming then waits for the same bytes.)
+// map, in both passes).  The lists are 17 of these and the mask 10; the bytes alone would be 22.  Latency bounds it:
+// 256 rows are one wave, in which every CTA works on its lists at the same time and streams at the same time, and a batch of
+// vectors is loaded when the last one has been worked.  (Fetching the part into L2 while the lists are looked through: 2
+// more; the streaming then waits for the same bytes.)
 // The scale is folded into the exponent.  Biases of one token add up in the order of the list.
 // Where the listed tokens of a part may be more than shared memory holds, the part is taken in chunks.
 #include <atomic>
