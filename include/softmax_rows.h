@@ -393,6 +393,172 @@ enum logits_out { LOGITS_OUT_LOGITS = 0, LOGITS_OUT_SOFTMAX = 1, LOGITS_OUT_LOG_
 int logits_process_rows(const logits_rows* a, int64_t M, int64_t N, int dtype, int out, void* stream);
 
 /*
+ * The training step around the matrix products: the loss of the logits with its gradient, the
+ * root-mean-square norm of rows and its backward pass, embedding lookup and its gradient, the norm of all
+ * gradients and clipping.  (The pages give the loss, "从原始Softmax到在线Softmax", section "softmax实际代码实现",
+ * and stop at the forward pass; the gradients are the derivatives of the formulas stated here.)
+ *
+ * Rows lie at pitches (ld..., in elements, >= N, 0: N).  Every pointer is aligned to its elements (else
+ * SOFTMAX_ERR_MISALIGNED); any length and pitch is taken, and runs faster where rows start on 16-byte
+ * boundaries.  Sums are held in fp32, added up in an order that the sizes alone fix: the same call gives the same
+ * bits.  Each workspace is device memory, 256-byte aligned, that no other call uses until this one is done
+ * (calls that may run at the same time, captured graphs among them, need one each); nothing in it is kept from
+ * call to call.  A count of rows, tokens or tensors of 0 is a no-op unless an output is left to be written.
+ */
+
+/*
+ * cross_entropy_rows_grad -- the loss of cross_entropy_rows and its gradient, x read once where a row fits on
+ * chip.  For each row with label t, p = softmax(x), LSE = m + ln d, and e = label_smoothing, z = z_loss:
+ *     loss = (1 - e) (LSE - x_t) + e mean_j (LSE - x_j) + z LSE^2
+ *     grad_j = w (p_j (1 + 2 z LSE) - (1 - e) [j = t] - e / N),     w = grad_scale * upstream
+ * that is, grad = d(sum_r grad_scale * upstream_r * loss_r) / dx.
+ *   x          -- [M][N] at pitch ldx.
+ *   labels     -- int64 [M].  A negative label marks a row to ignore: loss = 0 and grad = 0, whatever x holds.  A
+ *                 label >= N gives loss = NaN and a grad of NaN, and softmax_get_status returns
+ *                 SOFTMAX_ERR_INVALID_ARG.
+ *   upstream   -- fp32 [M], the gradient of what is minimised by each row's loss, or NULL for 1.
+ *   grad_scale -- finite; 1 / rows for a mean, times a loss scale.
+ *   label_smoothing -- in [0, 1).    z_loss -- finite, >= 0.
+ *   grad       -- [M][N] at pitch ldg, dtype elements; may be x (with ldg == ldx), other overlaps are undefined.
+ *   loss       -- fp32 [M].   lse_out -- fp32 [M] or NULL (every row's, ignored ones too).
+ * Masked entries (-inf) have p = 0; a masked label gives loss = +inf, and so does smoothing over masked entries; their
+ * gradients stay finite.  A row whose entries are all -inf gives NaN unless it is ignored.
+ */
+int cross_entropy_rows_grad(const void* x, int64_t ldx, const int64_t* labels, const float* upstream, float grad_scale,
+                            float label_smoothing, float z_loss, void* grad, int64_t ldg, float* loss, float* lse_out,
+                            int64_t M, int64_t N, int dtype, void* stream);
+
+/*
+ * rms_norm_rows -- M rows of N: h = x + residual (rounded to the element type, which is what the norm is taken of),
+ *     rstd = 1 / sqrt(mean_j h_j^2 + eps),     y_j = h_j rstd (weight_j + offset)
+ *   x, residual -- residual may be NULL (h = x).
+ *   sum_out     -- h; required with a residual, NULL without one.  May be x or residual (with its pitch).
+ *   weight      -- [N], dtype elements or fp32 (weight_f32 = 1), or NULL for 1 - offset.
+ *   eps         -- finite, >= 0.   offset -- finite (1 where weights are kept as their difference from 1).
+ *   y           -- out = RMS_NORM_OUT_SAME: dtype elements.  May be x, or residual, where sum_out is not.
+ *                  out = RMS_NORM_OUT_E4M3: 8-bit floats (e4m3, largest 448), with fp32 scales: the value is
+ *                  code * scale, scale = max(max |y| / 448, 2^-126) over a group, code = y * (1 / scale) rounded to
+ *                  the nearest (ties to even).
+ *   scales      -- e4m3 only: [M][groups], groups = 1 for group = 0 (a scale for each row), else ceil(N / group).
+ *   group       -- 0 or 128 (the last group of a row may be shorter).
+ *   rstd_out    -- fp32 [M] or NULL; the backward pass reads it.
+ */
+typedef struct rms_norm_args {
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ld_residual;
+  void* sum_out;
+  int64_t ld_sum;
+  const void* weight;
+  int64_t weight_f32;
+  void* y;
+  int64_t ldy;
+  float* scales;
+  int64_t group;
+  float* rstd_out;
+  float eps;
+  float offset;
+} rms_norm_args;
+
+enum rms_norm_out { RMS_NORM_OUT_SAME = 0, RMS_NORM_OUT_E4M3 = 1 };
+
+int rms_norm_rows(const rms_norm_args* a, int64_t M, int64_t N, int dtype, int out, void* stream);
+
+/*
+ * rms_norm_rows_backward -- with xhat = h rstd and g = dy (weight + offset):
+ *     dx_j = rstd (g_j - xhat_j mean_i(g_i xhat_i)) + sum_grad_j      (of x and of residual alike)
+ *     dweight_j = sum_r dy_rj xhat_rj
+ *   dy, h, sum_grad -- [M][N]: the gradient of y; the sum that the norm was taken of; the gradient that reaches
+ *                 that sum by its other uses, or NULL.
+ *   rstd       -- fp32 [M], from the forward pass.
+ *   weight, weight_f32, offset -- as in the forward pass.
+ *   dx         -- [M][N]; may be dy, h or sum_grad (with its pitch).
+ *   dweight    -- fp32 [N], or NULL.  accumulate = 1 adds to what it holds, 0 overwrites it.
+ *   workspace  -- at least rms_norm_backward_workspace(M, N, dtype) bytes (with dweight; else unused).
+ */
+typedef struct rms_norm_grad_args {
+  const void* dy;
+  int64_t ld_dy;
+  const void* h;
+  int64_t ldh;
+  const void* sum_grad;
+  int64_t ld_sum_grad;
+  const float* rstd;
+  const void* weight;
+  int64_t weight_f32;
+  void* dx;
+  int64_t ld_dx;
+  float* dweight;
+  int64_t accumulate;
+  float offset;
+} rms_norm_grad_args;
+
+int rms_norm_rows_backward(const rms_norm_grad_args* a, int64_t M, int64_t N, int dtype, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace on the current device; -1 for sizes that the call refuses. */
+int64_t rms_norm_backward_workspace(int64_t M, int64_t N, int dtype);
+
+/*
+ * embedding_rows -- y_t = scale * table[tokens_t]: T rows of D elements out of a table of V rows.
+ *   tokens -- int32 (token_bytes = 4) or int64 (8), [T].  A negative token is padding: its row is 0.  A token >= V
+ *             gives a row of NaN, is not followed, and softmax_get_status returns SOFTMAX_ERR_INVALID_ARG.
+ *   scale  -- finite; the product is rounded once.
+ */
+int embedding_rows(const void* table, int64_t ld_table, const void* tokens, int token_bytes, void* y, int64_t ldy,
+                   int64_t T, int64_t V, int64_t D, float scale, int dtype, void* stream);
+
+/*
+ * embedding_rows_backward -- grad_v = scale * sum over the t with tokens_t = v of dy_t, [V][D] dense: rows that no
+ * token names are 0.  accumulate = 1: added to what grad holds (in fp32, then rounded), and rows that no token
+ * names are neither read nor written.  The tokens are sorted on the device; a row's sum runs over its tokens in
+ * their order, in parts where there are many.
+ *   dy         -- [T][D], dtype elements.   grad -- [V][D], grad_dtype elements: fp32 or dtype's.
+ *   tokens     -- as in embedding_rows: padding gives no gradient, nor does a token >= V (which is recorded).
+ *   workspace  -- at least embedding_backward_workspace(T, V, D) bytes.
+ * T up to 2^24, V up to 2^31 - 2 (else SOFTMAX_ERR_UNSUPPORTED).
+ */
+int embedding_rows_backward(const void* dy, int64_t ld_dy, const void* tokens, int token_bytes, void* grad,
+                            int64_t ld_grad, int64_t T, int64_t V, int64_t D, float scale, int accumulate, int dtype,
+                            int grad_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace; -1 for sizes that the call refuses. */
+int64_t embedding_backward_workspace(int64_t T, int64_t V, int64_t D);
+
+/* One tensor of a list: n contiguous elements, and where their scaled values go (out may be grad where the types are
+   one; grad_norm does not look at it).  out_dtype: fp32 or dtype. */
+typedef struct grad_tensor {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t dtype;
+  int32_t out_dtype;
+} grad_tensor;
+
+/*
+ * grad_norm -- norm_out = |scale| sqrt(sum of the squares of all elements of count tensors), fp32.  Squares are taken in
+ * fp32, a few dozen at a time, and in fp64 where those run over fp32's range or fall below it: neither large nor small
+ * values are lost.  +inf or NaN where an element is not finite (or the norm is above fp32's range).
+ * clip_grad_norm -- the same, and
+ *     out = grad * scale * min(1, max_norm / norm)
+ * for each tensor, rounded once.  Where the norm is inf or NaN nothing is limited: out = grad * scale.  A tensor in
+ * place (out == grad) whose factor is 1 is neither read again nor written.
+ *   tensors   -- HOST array of count entries (at most 2^20, 2^42 elements in all), read before the call returns; tensors may
+ *                not overlap each other.
+ *   scale     -- finite: 1 / (loss scale), 1 / (accumulated steps).   max_norm -- finite, > 0.
+ *   norm_out  -- fp32 [1], device.
+ *   workspace -- at least grad_norm_workspace(count) bytes.
+ */
+int grad_norm(const grad_tensor* tensors, int64_t count, float scale, float* norm_out, void* workspace,
+              int64_t workspace_bytes, void* stream);
+int clip_grad_norm(const grad_tensor* tensors, int64_t count, float scale, float max_norm, float* norm_out, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace on the current device; -1 for a count that the calls refuse. */
+int64_t grad_norm_workspace(int64_t count);
+
+/*
  * softmax_row_state -- only the per-row state (m, d) and LSE: the first pass
  * of the online method ("5.2 CUDA Online Softmax 实现优化", §2.2, pass 1;
  * "Softmax 数值稳定性与 IO-Aware Attention" §四, the mergeable state).  Reads x
@@ -463,7 +629,7 @@ int softmax_rows_splitrow_noalloc(const void* x, void* y, float* m_out, float* d
  * recorded since the last call (SOFTMAX_ERR_TIMEOUT for a bounded wait that
  * ran out, which takes precedence; SOFTMAX_ERR_INVALID_ARG for a cross-entropy
  * label >= N, or a page, token, length or position that a call of the decoding
- * step found out of range).  SOFTMAX_ERR_CUDA if the synchronisation itself failed.
+ * or the training step found out of range).  SOFTMAX_ERR_CUDA if the synchronisation itself failed.
  */
 int softmax_get_status(void* stream);
 

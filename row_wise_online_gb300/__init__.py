@@ -21,7 +21,9 @@ __all__ = [
     "softmax_row_state", "merge_states", "softmax_rows_host", "get_status", "status_string",
     "last_variant", "debug_set_fault", "debug_set_wait_limit_ns", "capi", "library_path",
     "softmax_rows_splitrow_noalloc", "softmax_rows_causal", "kv4_cache_empty", "kv4_append", "kv4_gather",
-    "attention_kv4", "attention_kv4_workspace", "logits_process_rows",
+    "attention_kv4", "attention_kv4_workspace", "logits_process_rows", "cross_entropy_rows_grad", "rms_norm_rows",
+    "rms_norm_rows_e4m3", "rms_norm_rows_backward", "rms_norm_backward_workspace", "embedding_rows",
+    "embedding_rows_backward", "embedding_backward_workspace", "grad_norm", "clip_grad_norm", "grad_norm_workspace",
 ]
 
 F32, BF16, F16 = 0, 1, 2
@@ -43,6 +45,8 @@ EXPORTED = (
     "softmax_debug_set_fault", "softmax_debug_set_wait_limit_ns", "softmax_rows_splitrow_noalloc",
     "softmax_rows_causal", "log_softmax_rows", "cross_entropy_rows", "softmax_rows_strided", "attention_forward",
     "kv4_append", "kv4_gather", "attention_kv4", "attention_kv4_workspace", "logits_process_rows",
+    "cross_entropy_rows_grad", "rms_norm_rows", "rms_norm_rows_backward", "rms_norm_backward_workspace", "embedding_rows",
+    "embedding_rows_backward", "embedding_backward_workspace", "grad_norm", "clip_grad_norm", "grad_norm_workspace",
 )
 
 
@@ -95,6 +99,7 @@ def capi() -> ctypes.CDLL:
                      "log_softmax_rows", "cross_entropy_rows", "softmax_rows_strided", "attention_forward"):
             getattr(lib, name).restype = ci
         decode._declare(lib)
+        train._declare(lib)
         _lib = lib
     return _lib
 
@@ -380,6 +385,9 @@ def debug_set_wait_limit_ns(ns: int) -> int:
     return int(capi().softmax_debug_set_wait_limit_ns(int(ns)))
 
 
-from . import decode  # noqa: E402  (uses the helpers above)
+from . import decode, train  # noqa: E402  (use the helpers above)
 from .decode import (attention_kv4, attention_kv4_workspace, kv4_append, kv4_cache_empty, kv4_gather,  # noqa: E402
                      logits_process_rows)
+from .train import (clip_grad_norm, cross_entropy_rows_grad, embedding_backward_workspace, embedding_rows,  # noqa: E402
+                    embedding_rows_backward, grad_norm, grad_norm_workspace, rms_norm_backward_workspace, rms_norm_rows,
+                    rms_norm_rows_backward, rms_norm_rows_e4m3)
