@@ -1,105 +1,83 @@
-// kernel_loss_grad.cu -- the cross-entropy loss of a row of logits and its gradient.
-//
-// With the row's online state (m, d), S = sum_j (m - x_j), label t, e = label smoothing, z the weight of LSE^2 and
-// w = grad_scale * upstream:
-//     LSE  = m + ln d
-//     loss = (1 - e) (m - x_t) + e S / N + ln d + z LSE^2
-//     grad_j = w (1 + 2 z LSE) / d * e^(x_j - m) - w e / N - [j = t] w (1 - e)
-// so once (m, d, S) are known an element needs one exponential and one multiply-add.  S is taken relative to the
-// maximum, as d is: m - x_j loses nothing where |m| is large.
-#include "train.cuh"
-#include "train.h"
+// kernel_loss_grad.cu -- the cross-entropy loss and its gradient (loss_grad.cuh): short rows in registers, two passes
+// for rows that are too long for a cluster, and the choice.
+#include "loss_grad.cuh"
 
 namespace rwo {
 namespace {
 
-struct Args {
-  const unsigned char* x;
-  unsigned char* g;
-  const int64_t* labels;
-  const float* upstream;
-  float* loss;
-  float* lse;
-  int64_t M, N;
-  int64_t x_pitch, g_pitch;  // bytes
-  float grad_scale, smoothing, z;
-  unsigned* status;
-};
+// ---- short rows: W warps a row, the row in registers ------------------------------------------------------------------
 
-// Part of a row: (m, d) of softmax, s = sum of (m - x) and n, how many elements (s and n with smoothing only).
-struct Fold {
-  float m, d, s, n;
-};
-__device__ __forceinline__ Fold empty_fold() { return Fold{-INFINITY, 0.f, 0.f, 0.f}; }
+constexpr int kRegThreads = 256;
 
-// s of a part, relative to a maximum mx >= its own.  Entries of -inf make s +inf; a part of nothing stays 0.
-__device__ __forceinline__ float moved(const Fold& f, float mx) {
-  return f.n > 0.f ? __fmaf_rn(f.n, mx - safe_max(f.m), f.s) : 0.f;
-}
-
-__device__ __forceinline__ Fold merge(const Fold& a, const Fold& b) {
-  const State t = merge(State{a.m, a.d}, State{b.m, b.d});
-  const float ms = safe_max(t.m);
-  return Fold{t.m, t.d, __fadd_rn(moved(a, ms), moved(b, ms)), a.n + b.n};
-}
-
-template <bool SMOOTH>
-__device__ __forceinline__ Fold warp_fold(Fold f) {
+// VEC: 16-byte vectors, K a thread; else K single elements.
+template <class D, int K, int W, bool VEC, bool SMOOTH>
+__global__ void __launch_bounds__(kRegThreads) k_loss_grad_reg(LossArgs a) {
+  constexpr int E = VEC ? D::kVec : 1, GT = W * 32, G = kRegThreads / GT;
+  __shared__ Fold parts[2][kRegThreads / 32];
+  const int group = threadIdx.x / GT, t = threadIdx.x % GT, lane = threadIdx.x & 31, warp = t >> 5;
+  const int units = int(a.N / E);
+  int it = 0;
+  for (int64_t row = int64_t(blockIdx.x) * G + group; row < a.M; row += int64_t(gridDim.x) * G, it ^= 1) {
+    const unsigned char* xr = a.x + row * a.x_pitch;
+    unsigned char* gr = a.g + row * a.g_pitch;
+    const int64_t label = a.labels[row];
+    const float x_label = t == 0 && label >= 0 && label < a.N ? load1c<D>(xr, label) : 0.f;
+    Fold f;
+    uint4 q[VEC ? K : 1];
+    float v[VEC ? 1 : K];
+    if constexpr (VEC) {
+      uint32_t whole = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Fold t{__shfl_xor_sync(~0u, f.m, o), __shfl_xor_sync(~0u, f.d, o), 0.f, 0.f};
-    if constexpr (SMOOTH) {
-      t.s = __shfl_xor_sync(~0u, f.s, o);
-      t.n = __shfl_xor_sync(~0u, f.n, o);
-    }
-    f = merge(f, t);
-  }
-  return f;
-}
-
-// What the elements of a row need once its state is known.
-struct Slope {
-  float ms;     // the maximum (0 for an empty row)
-  float a;      // factor of e^(x - m)
-  float b;      // subtracted from every element
-  float c;      // and from the labelled one
-  int64_t label;
-  bool live;    // false: every element is 0
-};
-
-// One thread of a row passes write = true: it stores the loss and LSE and records a bad label.
-__device__ __forceinline__ Slope slope_of(const Args& a, int64_t row, const Fold& f, int64_t label, float x_label, bool write) {
-  Slope s;
-  const float lnd = logf(f.d), lse = f.m + lnd;  // an empty row: -inf; NaN among -inf: NaN
-  const bool bad = label >= a.N;
-  const float w = a.grad_scale * (a.upstream ? a.upstream[row] : 1.f);
-  s.ms = safe_max(f.m);
-  s.a = bad ? __int_as_float(0x7fc00000) : w * (1.f + 2.f * a.z * lse) / f.d;
-  s.b = w * (a.smoothing / float(a.N));
-  s.c = w * (1.f - a.smoothing);
-  s.label = label;
-  s.live = label >= 0;
-  if (write) {
-    float l = 0.f;
-    if (bad) {
-      l = __int_as_float(0x7fc00000);
-      atomicOr(a.status, kStatusBadLabel);
-    } else if (label >= 0) {
-      if (f.m == -INFINITY) {
-        l = __int_as_float(0x7fc00000);
-      } else {
-        l = __fmaf_rn(1.f - a.smoothing, f.m - x_label, lnd);
-        if (a.smoothing > 0.f) l = __fmaf_rn(a.smoothing, f.s / float(a.N), l);
-        if (a.z > 0.f) l = __fmaf_rn(a.z * lse, lse, l);
+      for (int k = 0; k < K; ++k) {
+        const int u = t + k * GT;
+        if (u < units) whole |= 1u << k;
+        q[k] = u < units ? ld_stream16(xr + u * 16) : make_uint4(D::kNegInfWord, D::kNegInfWord, D::kNegInfWord, D::kNegInfWord);
+      }
+      f = fold_vectors<D, K, SMOOTH>(q, whole);
+    } else {
+      f = empty_fold();
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int u = t + k * GT;
+        v[k] = u < units ? D::load1(xr, u) : -INFINITY;
+        f.m = fmaxf(f.m, v[k]);
+      }
+      const float ms = safe_max(f.m);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        f.d += exp_diff(v[k], ms);
+        if (SMOOTH && t + k * GT < units) {
+          f.s += ms - v[k];
+          f.n += 1.f;
+        }
       }
     }
-    a.loss[row] = l;
-    if (a.lse) a.lse[row] = lse;
+    f = fold_lanes<SMOOTH>(f, 32);
+    if constexpr (W > 1) {
+      Fold* mine = parts[it] + group * W;
+      if (lane == 0) mine[warp] = f;
+      named_barrier_sync(1 + group, GT);
+      f = fold_lanes<SMOOTH>(mine[lane & (W - 1)], W);
+    } else {
+      __syncwarp();  // x_label is read before the row is overwritten
+    }
+    const Slope s = slope_of(a, row, f, label, x_label, t == 0);
+    if constexpr (VEC) {
+      const int at = label >= 0 && label < a.N ? int(label) - t * E : -1 - t * E;
+      grad_vectors<D, K>(s, q, [&](int k) { return t + k * GT < units; }, [&](int k) { return at - k * GT * E; },
+                         [&](int k, const float2(&y)[E / 2]) { st_stream16(gr + (t + k * GT) * 16, D::pack2(y)); });
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int u = t + k * GT;
+        if (u >= units) continue;
+        float y = grad_of(s, v[k]);
+        if (s.live && u == label) y -= s.c;
+        D::store1(gr, u, y);
+      }
+    }
   }
-  return s;
 }
-
-__device__ __forceinline__ float grad_of(const Slope& s, float x) { return s.live ? __fmaf_rn(exp_diff(x, s.ms), s.a, -s.b) : 0.f; }
 
 // ---- two passes, rows of any length and alignment ------------------------------------------------------------------
 
@@ -107,7 +85,7 @@ constexpr int kThreads = 512;
 
 // A CTA a row: the fold, then the gradient from a second read.  VEC: 16-byte units, else single elements.
 template <class D, bool VEC, bool SMOOTH>
-__global__ void __launch_bounds__(kThreads) k_loss_grad_twopass(Args a) {
+__global__ void __launch_bounds__(kThreads) k_loss_grad_twopass(LossArgs a) {
   constexpr int E = VEC ? D::kVec : 1;
   __shared__ Fold parts[2][kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -150,10 +128,10 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad_twopass(Args a) {
         f.n += float(E);
       }
     }
-    f = warp_fold<SMOOTH>(f);
+    f = fold_lanes<SMOOTH>(f, 32);
     if (lane == 0) parts[it][warp] = f;
     __syncthreads();
-    f = warp_fold<SMOOTH>(lane < kThreads / 32 ? parts[it][lane] : empty_fold());
+    f = fold_lanes<SMOOTH>(parts[it][lane & (kThreads / 32 - 1)], kThreads / 32);
     const Slope s = slope_of(a, row, f, label, x_label, threadIdx.x == 0);
     for (int64_t u = threadIdx.x; u < units; u += kThreads) {
       float v[E];
@@ -162,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad_twopass(Args a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         v[e] = grad_of(s, v[e]);
-        if (s.live && u * E + e == s.label) v[e] -= s.c;
+        if (s.live && u * E + e == label) v[e] -= s.c;
       }
       if constexpr (VEC) st_stream16(gr + u * 16, D::pack(v));
       else D::store1(gr, u, v[0]);
@@ -170,13 +148,34 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad_twopass(Args a) {
   }
 }
 
-using Kernel = void (*)(Args);
+using Kernel = void (*)(LossArgs);
+
+struct RegConfig {
+  int warps, units;  // warps a row, units they hold
+  Kernel fn[2];      // [smoothing]
+};
+template <class D, int K, int W, bool VEC>
+constexpr RegConfig reg() {
+  return RegConfig{W, 32 * W * K, {k_loss_grad_reg<D, K, W, VEC, false>, k_loss_grad_reg<D, K, W, VEC, true>}};
+}
 
 template <class D>
-cudaError_t launch_type(const LossGrad& p, Args a, const DeviceInfo& dev) {
+cudaError_t launch_type(const LossGrad& p, const LossArgs& a, const DeviceInfo& dev) {
+  static const RegConfig vectors[] = {reg<D, 1, 1, true>(), reg<D, 2, 1, true>(), reg<D, 4, 1, true>(), reg<D, 4, 2, true>(), reg<D, 4, 4, true>(), reg<D, 4, 8, true>()};
+  static const RegConfig elements[] = {reg<D, 2, 1, false>(), reg<D, 8, 1, false>(), reg<D, 8, 4, false>()};
   const bool smooth = p.smoothing > 0.f;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.g) | uintptr_t(a.x_pitch) | uintptr_t(a.g_pitch) |
                      uintptr_t(p.N * D::kBytes)) & 15) == 0;
+  const int64_t units = vec ? p.N / D::kVec : p.N;
+  const RegConfig* tab = vec ? vectors : elements;
+  for (int i = 0; i < (vec ? 6 : 3); ++i) {
+    if (units > tab[i].units) continue;
+    const int64_t groups = kRegThreads / 32 / tab[i].warps, ctas = (p.M + groups - 1) / groups;
+    const int64_t slots = int64_t(dev.sm_count) * (dev.max_threads_per_sm / kRegThreads) * 4;
+    tab[i].fn[smooth]<<<unsigned(ctas < slots ? ctas : slots), kRegThreads, 0, p.stream>>>(a);
+    return cudaGetLastError();
+  }
+  if (loss_grad_cluster_fits(p)) return launch_loss_grad_cluster(p, a, dev);
   const Kernel k = vec ? (smooth ? k_loss_grad_twopass<D, true, true> : k_loss_grad_twopass<D, true, false>)
                        : (smooth ? k_loss_grad_twopass<D, false, true> : k_loss_grad_twopass<D, false, false>);
   const int64_t slots = int64_t(dev.sm_count) * (dev.max_threads_per_sm / kThreads);
@@ -187,7 +186,7 @@ cudaError_t launch_type(const LossGrad& p, Args a, const DeviceInfo& dev) {
 }  // namespace
 
 cudaError_t launch_loss_grad(const LossGrad& p, const DeviceInfo& dev) {
-  Args a;
+  LossArgs a;
   const int64_t s = elem_bytes(p.dtype);
   a.x = static_cast<const unsigned char*>(p.x);
   a.g = static_cast<unsigned char*>(p.grad);
@@ -202,6 +201,7 @@ cudaError_t launch_loss_grad(const LossGrad& p, const DeviceInfo& dev) {
   a.grad_scale = p.grad_scale;
   a.smoothing = p.smoothing;
   a.z = p.z;
+  a.smoothing_each = p.smoothing / float(p.N);
   a.status = dev.status;
   return p.dtype == SOFTMAX_F32 ? launch_type<F32>(p, a, dev) : p.dtype == SOFTMAX_BF16 ? launch_type<BF16>(p, a, dev) : launch_type<F16>(p, a, dev);
 }
