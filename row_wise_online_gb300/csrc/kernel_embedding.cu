@@ -3,19 +3,29 @@
 // Lookup: y_t = scale * table[token_t], a copy of rows.
 //
 // Gradient: grad_v = scale * sum of dy_t over the t with token_t = v.  The tokens are sorted with their positions
-// (k_sort_tokens: a stable radix sort by one thread-block cluster), so that the rows of a token are one run of the
-// sorted list.  The list is cut into chunks of kChunk tokens, whatever the runs: a CTA takes a chunk's columns and adds
-// up the runs in it (k_embedding_rows).  A run inside a chunk is written at once; one that goes on into the next chunk
-// leaves partial sums, which k_embedding_join adds up in their order.  So a frequent token is spread over the GPU as
-// others are, no atomics touch the sums, and their order is a function of the tokens alone.  Rows without a token
-// are zeroed by the same launch, from a bit map that the sort leaves.
+// (k_rank_tokens: few tokens, each counts those that come before it; k_sort_tokens: a stable radix sort by one thread-block
+// cluster), so that the rows of a token are one run of the sorted list.  The list is cut into chunks of some tokens, whatever
+// the runs: a CTA takes a chunk's columns and adds up the runs in it (k_embedding_rows).  A run inside a chunk is written at
+// once; one that goes on into the next chunk leaves partial sums, which k_embedding_join adds up in their order.  So a frequent
+// token is spread over the GPU as others are, no atomics touch the sums, and their order is a function of the tokens alone.
+// Rows without a token are zeroed by the same launch, from a bit map that the sort leaves.
+#include <initializer_list>
+
 #include "train.cuh"
 #include "train.h"
 
 namespace rwo {
 namespace {
 
-constexpr int kChunk = 32;
+constexpr int kMostChunk = 32;  // tokens of a chunk at most
+
+// Tokens of a chunk: 32, fewer where that would leave SMs without one (1500 tokens of 512 elements: 8).
+int chunk_of(int64_t T, int64_t D) {
+  int c = kMostChunk;
+  while (c > 8 && (T + c - 1) / c * ((D + 1023) / 1024) < 512) c /= 2;
+  return c;
+}
+
 constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCtas = 8;
 constexpr int kDigitBits = 10;
 
@@ -29,53 +39,80 @@ struct LookupArgs {
   const unsigned char* table;
   unsigned char* y;
   const void* tokens;
-  int64_t T, V;
+  int64_t T, V, D;
   int64_t table_pitch, y_pitch;  // bytes
-  uint32_t units;                // of a row
+  int64_t pieces;                // of a row
+  int units;                     // vectors of a row
   int token_bytes;
   float scale;
   unsigned* status;
 };
 
-constexpr int kLookupThreads = 256, kLookupPer = 4;
+constexpr int kLookupThreads = 256, kLookupPer = 8;
 
-// Units (16-byte vectors, or elements) of all rows in one line; a thread takes kLookupPer of them.
-template <class D, bool VEC>
-__global__ void __launch_bounds__(kLookupThreads) k_embedding(LookupArgs a) {
-  constexpr int E = VEC ? D::kVec : 1;
-  const int64_t base = int64_t(blockIdx.x) * (kLookupThreads * kLookupPer);
-  const int64_t t0 = base / a.units;
-  const uint32_t first = uint32_t(base - t0 * a.units);
-  float v[kLookupPer][E];
-  int64_t at[kLookupPer];
-#pragma unroll
-  for (int k = 0; k < kLookupPer; ++k) {
-    const uint64_t o = uint64_t(first) + threadIdx.x + k * kLookupThreads;
-    const uint64_t dt = o >> 32 ? o / a.units : uint32_t(o) / a.units;
-    const int64_t t = t0 + int64_t(dt);
-    const uint32_t u = uint32_t(o - dt * a.units);
-    at[k] = -1;
-    if (t >= a.T) continue;
-    const int64_t token = token_at(a.tokens, a.token_bytes, t);
-    at[k] = t * a.y_pitch + int64_t(u) * (E * D::kBytes);
-    if (token >= 0 && token < a.V) {
+// A warp moves pieces of rows: kLookupPer vectors a lane, all loaded before the first is stored, and the next piece's token is
+// under way meanwhile.
+template <class D, bool SHIFT>
+__global__ void __launch_bounds__(kLookupThreads, 4) k_embedding(LookupArgs a) {
+  constexpr int E = D::kVec;
+  const int lane = threadIdx.x & 31, n = int(a.D);
+  const int64_t warps = int64_t(gridDim.x) * (kLookupThreads / 32), items = a.T * a.pieces;
+  const Bytes table = bytes_of(a.table, a.V, a.table_pitch, a.D * D::kBytes);
+  int64_t item = int64_t(blockIdx.x) * (kLookupThreads / 32) + (threadIdx.x >> 5);
+  if (item >= items) return;
+  int64_t t = item / a.pieces;
+  int64_t next = token_at(a.tokens, a.token_bytes, t);
+  while (true) {
+    const int64_t token = next;
+    const int u0 = int(item - t * a.pieces) * (kLookupPer * 32) + lane;
+    unsigned char* to = a.y + t * a.y_pitch;
+    item += warps;
+    t = item / a.pieces;
+    if (item < items) next = token_at(a.tokens, a.token_bytes, t);
+    uint4 q[kLookupPer];
+    const bool real = token >= 0 && token < a.V;
+    if (real) {
       const unsigned char* row = a.table + token * a.table_pitch;
-      if constexpr (VEC) D::unpack(ld_stream16(row + int64_t(u) * 16), v[k]);
-      else v[k][0] = D::load1(row, u);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] *= a.scale;
+      for (int k = 0; k < kLookupPer; ++k) {
+        const int u = u0 + k * 32;
+        if constexpr (SHIFT) q[k] = load_vector<D>(row, u, n, table);
+        else if (u < a.units) q[k] = ld_stream16(row + int64_t(u) * 16);
+      }
+      if (a.scale != 1.f) {
+        const float2 s = make_float2(a.scale, a.scale);
+#pragma unroll
+        for (int k = 0; k < kLookupPer; ++k) {
+          float2 v[E / 2];
+          D::unpack2(q[k], v);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) v[e] = __fmul2_rn(v[e], s);
+          q[k] = D::pack2(v);
+        }
+      }
     } else {
-      if (token >= 0 && u == 0) atomicOr(a.status, kStatusBadIndex);
+      if (token >= 0 && u0 == 0) atomicOr(a.status, kStatusBadIndex);
+      float2 v[E / 2];
+      const float f = token < 0 ? 0.f : __int_as_float(0x7fc00000);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] = token < 0 ? 0.f : __int_as_float(0x7fc00000);
+      for (int e = 0; e < E / 2; ++e) v[e] = make_float2(f, f);
+#pragma unroll
+      for (int k = 0; k < kLookupPer; ++k) q[k] = D::pack2(v);
     }
+#pragma unroll
+    for (int k = 0; k < kLookupPer; ++k) {
+      const int u = u0 + k * 32;
+      if constexpr (SHIFT) store_vector<D>(to, u, n, q[k]);
+      else if (u < a.units) st_stream16(to + int64_t(u) * 16, q[k]);
+    }
+    if (item >= items) return;
   }
-#pragma unroll
-  for (int k = 0; k < kLookupPer; ++k)
-    if (at[k] >= 0) {
-      if constexpr (VEC) st_stream16(a.y + at[k], D::pack(v[k]));
-      else D::store1(a.y + at[k], 0, v[k][0]);
-    }
+}
+
+bool on16(std::initializer_list<uintptr_t> v) {
+  uintptr_t all = 0;
+  for (const uintptr_t x : v) all |= x;
+  return (all & 15) == 0;
 }
 
 template <class D>
@@ -86,28 +123,22 @@ cudaError_t launch_lookup(const Embedding& p, const DeviceInfo& dev) {
   a.tokens = p.tokens;
   a.T = p.T;
   a.V = p.V;
+  a.D = p.D;
   a.table_pitch = p.table_pitch * D::kBytes;
   a.y_pitch = p.y_pitch * D::kBytes;
   a.token_bytes = p.token_bytes;
   a.scale = p.scale;
   a.status = dev.status;
-  const bool vec = ((reinterpret_cast<uintptr_t>(a.table) | reinterpret_cast<uintptr_t>(a.y) | uintptr_t(a.table_pitch) | uintptr_t(a.y_pitch) |
-                     uintptr_t(p.D * D::kBytes)) & 15) == 0;
-  a.units = uint32_t(vec ? p.D / D::kVec : p.D);
-  const int64_t per = kLookupThreads * kLookupPer;
-  // the grid's limit of 2^31 - 1 CTAs: more rows than that take further launches
-  const int64_t rows = (int64_t(1) << 30) * per / a.units;
-  for (int64_t t = 0; t < p.T; t += rows) {
-    LookupArgs b = a;
-    b.T = p.T - t < rows ? p.T - t : rows;
-    b.tokens = static_cast<const unsigned char*>(p.tokens) + t * p.token_bytes;
-    b.y = a.y + t * a.y_pitch;
-    const unsigned grid = unsigned((b.T * a.units + per - 1) / per);
-    if (vec) k_embedding<D, true><<<grid, kLookupThreads, 0, p.stream>>>(b);
-    else k_embedding<D, false><<<grid, kLookupThreads, 0, p.stream>>>(b);
-    if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  const bool vec = on16({reinterpret_cast<uintptr_t>(a.table), reinterpret_cast<uintptr_t>(a.y), uintptr_t(a.table_pitch), uintptr_t(a.y_pitch),
+                         uintptr_t(p.D * D::kBytes)});
+  a.units = int((p.D + D::kVec - 1) / D::kVec);
+  a.pieces = (a.units + kLookupPer * 32 - 1) / (kLookupPer * 32);
+  const int64_t per = kLookupThreads / 32, most = int64_t(dev.sm_count) * 4;
+  const int64_t ctas = p.T > most * per ? most : (p.T * a.pieces + per - 1) / per;
+  const unsigned grid = unsigned(ctas < most ? ctas : most);
+  if (vec) k_embedding<D, false><<<grid, kLookupThreads, 0, p.stream>>>(a);
+  else k_embedding<D, true><<<grid, kLookupThreads, 0, p.stream>>>(a);
+  return cudaGetLastError();
 }
 
 // ---- gradient: the sort ---------------------------------------------------------------------------------------------
@@ -126,7 +157,8 @@ struct GradArgs {
   int64_t dy_pitch, g_pitch;  // bytes
   int64_t part_pitch;         // floats
   int64_t chunks;
-  uint32_t units;             // of a row
+  int chunk;                  // tokens of one
+  int units;                  // vectors of a row of dy
   int slices;                 // CTAs of a chunk
   int64_t fill_rows;          // rows of a zeroing CTA
   int token_bytes, passes, digit_bits;
@@ -135,9 +167,53 @@ struct GradArgs {
   unsigned* status;
 };
 
+// The token's key: its row, or V where it names none; such keys end up last.
+__device__ __forceinline__ uint32_t key_of(const GradArgs& a, int64_t i) {
+  const int64_t t = token_at(a.tokens, a.token_bytes, i);
+  if (t >= a.V) atomicOr(a.status, kStatusBadIndex);
+  return t >= 0 && t < a.V ? uint32_t(t) : uint32_t(a.V);
+}
+
+// Few tokens: a warp a token counts the keys before its own (smaller, or equal and earlier), which is the token's place.  Every
+// CTA also makes its part of the bit map.  1500 tokens take 4 us, the radix sort's two passes 13.
+constexpr int kRankTokens = 4096, kRankWords = 8192;
+
+__global__ void __launch_bounds__(kSortThreads) k_rank_tokens(GradArgs a) {
+  __shared__ uint32_t keys[kRankTokens];
+  __shared__ uint32_t bits[kRankWords];
+  griddep_launch();
+  const int n = int(a.T), tid = threadIdx.x, lane = tid & 31;
+  const int64_t words = (a.V + 31) / 32, mine = (words + gridDim.x - 1) / gridDim.x;
+  const int64_t w0 = blockIdx.x * mine < words ? blockIdx.x * mine : words, w1 = w0 + mine < words ? w0 + mine : words;
+  for (int i = tid; i < n; i += kSortThreads) keys[i] = key_of(a, i);
+  for (int w = tid; w < int(w1 - w0); w += kSortThreads) bits[w] = 0;
+  __syncthreads();
+  if (!a.accumulate) {
+    for (int i = tid; i < n; i += kSortThreads) {
+      const int64_t w = int64_t(keys[i] / 32) - w0;
+      if (keys[i] < a.V && w >= 0 && w < w1 - w0) atomicOr(bits + w, 1u << keys[i] % 32);
+    }
+    __syncthreads();
+    for (int w = tid; w < int(w1 - w0); w += kSortThreads) a.bits[w0 + w] = bits[w];
+  }
+  for (int i = int(blockIdx.x) * kSortWarps + (tid >> 5); i < n; i += int(gridDim.x) * kSortWarps) {
+    const uint32_t key = keys[i];
+    int before = 0;
+    for (int j = lane; j < n; j += 32) before += keys[j] < key || (keys[j] == key && j < i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(~0u, before, o);
+    if (lane == 0) {
+      a.keys[0][before] = key;
+      a.pos[0][before] = uint32_t(i);
+    }
+  }
+}
+
 // Least significant digit first, digits of digit_bits.  A warp owns a run of the list and a column of counts; ranks
-// within 32 tokens come from a vote (lanes of the same digit), so equal tokens keep their order.  Tokens outside the
-// table get the key V and end up last.
+// within 32 tokens come from a vote (lanes of the same digit), so equal tokens keep their order.  A run is loaded kRun tokens a
+// lane at a time, and stays in registers between counting and moving where that is all of it.
+constexpr int kRun = 8;
+
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) k_sort_tokens(GradArgs a) {
   extern __shared__ uint32_t shared[];
   const int bins = 1 << a.digit_bits, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -145,11 +221,13 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
   uint32_t* base = total + bins;                        // [bins]
   uint32_t* counts = base + bins;                       // [bins][33]: a warp's counts, then where they start
   __shared__ uint32_t sums[kSortWarps];
+  griddep_launch();
   const uint32_t cta = cluster_ctarank();
   const int64_t per = ((a.T + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
-  const int64_t i0 = (int64_t(cta) * kSortWarps + warp) * per;
+  const int64_t i0 = (int64_t(cta) * kSortWarps + warp) * per < a.T ? (int64_t(cta) * kSortWarps + warp) * per : a.T;
   const int64_t i1 = i0 + per < a.T ? i0 + per : a.T;
   const uint32_t below = (1u << lane) - 1;
+  const bool whole = per <= kRun * 32;
 
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.digit_bits;
@@ -157,25 +235,37 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     const uint32_t* from_pos = a.pos[(pass + 1) & 1];
     uint32_t* to_keys = a.keys[pass & 1];
     uint32_t* to_pos = a.pos[pass & 1];
-    auto key_at = [&](int64_t i) -> uint32_t {
-      if (pass) return __ldcg(from_keys + i);
-      const int64_t t = token_at(a.tokens, a.token_bytes, i);
-      return t >= 0 && t < a.V ? uint32_t(t) : uint32_t(a.V);
+    uint32_t key[kRun], pos[kRun];
+    const auto load = [&](int64_t i, bool positions) {
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        const int64_t at = i + k * 32 + lane;
+        key[k] = pos[k] = 0;
+        if (at >= i1) continue;
+        key[k] = pass ? __ldcg(from_keys + at) : key_of(a, at);
+        if (positions) pos[k] = pass ? __ldcg(from_pos + at) : uint32_t(at);
+      }
     };
+    if (whole) load(i0, true);
     for (int b = tid; b < bins * 33; b += kSortThreads) counts[b] = 0;
     __syncthreads();
-    for (int64_t i = i0; i < i1; i += 32) {
-      const bool on = i + lane < i1;
-      const uint32_t d = on ? key_at(i + lane) >> shift & (bins - 1) : 0xffffffffu;
-      if (!pass && on && token_at(a.tokens, a.token_bytes, i + lane) >= a.V) atomicOr(a.status, kStatusBadIndex);
-      const uint32_t same = __match_any_sync(~0u, d);
-      if (on && !(same & below)) counts[d * 33 + warp] += __popc(same);
-      __syncwarp();
+    for (int64_t i = i0; i < i1; i += kRun * 32) {
+      if (!whole) load(i, false);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        if (i + k * 32 >= i1) break;
+        const bool on = i + k * 32 + lane < i1;
+        const uint32_t d = on ? key[k] >> shift & (bins - 1) : 0xffffffffu;
+        const uint32_t same = __match_any_sync(~0u, d);
+        if (on && !(same & below)) counts[d * 33 + warp] += __popc(same);
+        __syncwarp();
+      }
     }
     __syncthreads();
     // bin b's counts to starts within this CTA's part of the bin
     if (tid < bins) {
       uint32_t run = 0;
+#pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t c = counts[tid * 33 + w];
         counts[tid * 33 + w] = run;
@@ -185,13 +275,17 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     }
     cluster_sync();
     uint32_t all = 0, before = 0;
-    if (tid < bins)
+    if (tid < bins) {
+      uint32_t n[kSortCtas];
+#pragma unroll
+      for (uint32_t c = 0; c < kSortCtas; ++c)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n[c]) : "r"(map_to_rank(smem_addr(total + tid), c)) : "memory");
+#pragma unroll
       for (uint32_t c = 0; c < kSortCtas; ++c) {
-        uint32_t n;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n) : "r"(map_to_rank(smem_addr(total + tid), c)) : "memory");
-        all += n;
-        before += c < cta ? n : 0;
+        all += n[c];
+        before += c < cta ? n[c] : 0;
       }
+    }
     // exclusive sum over the bins
     uint32_t incl = all;
 #pragma unroll
@@ -206,18 +300,23 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(~0u, w, o);
     if (tid < bins) base[tid] = w + incl - all + before;
     __syncthreads();
-    for (int64_t i = i0; i < i1; i += 32) {
-      const bool on = i + lane < i1;
-      const uint32_t key = on ? key_at(i + lane) : 0, d = on ? key >> shift & (bins - 1) : 0xffffffffu;
-      const uint32_t same = __match_any_sync(~0u, d);
-      if (on) {
-        const uint32_t to = base[d] + counts[d * 33 + warp] + __popc(same & below);
-        to_keys[to] = key;
-        to_pos[to] = pass ? __ldcg(from_pos + i + lane) : uint32_t(i + lane);
+    for (int64_t i = i0; i < i1; i += kRun * 32) {
+      if (!whole) load(i, true);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        if (i + k * 32 >= i1) break;
+        const bool on = i + k * 32 + lane < i1;
+        const uint32_t d = on ? key[k] >> shift & (bins - 1) : 0xffffffffu;
+        const uint32_t same = __match_any_sync(~0u, d);
+        if (on) {
+          const uint32_t to = base[d] + counts[d * 33 + warp] + __popc(same & below);
+          to_keys[to] = key[k];
+          to_pos[to] = pos[k];
+        }
+        __syncwarp();
+        if (on && !(same & below)) counts[d * 33 + warp] += __popc(same);
+        __syncwarp();
       }
-      __syncwarp();
-      if (on && !(same & below)) counts[d * 33 + warp] += __popc(same);
-      __syncwarp();
     }
     cluster_sync();
   }
@@ -233,40 +332,55 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 
 // ---- gradient: the sums ---------------------------------------------------------------------------------------------
 
-// E sums to elements u * E .. of row v of the gradient.
-template <class G, bool VEC, int E>
-__device__ __forceinline__ void write_grad(const GradArgs& a, uint32_t v, int64_t u, const float (&sum)[E]) {
-  unsigned char* at = a.g + int64_t(v) * a.g_pitch + u * (E * G::kBytes);
-  float y[E];
+// A vector's sums, times scale, into vector u of a row of the gradient (or added to it), of the gradient's type.
+template <class G, bool SHIFT>
+__device__ __forceinline__ void write_vector(const GradArgs& a, unsigned char* row, int u, const float (&sum)[G::kVec], const Bytes& m) {
+  const int n = int(a.D);
+  float y[G::kVec];
+  if (a.accumulate) {
+    uint4 old = make_uint4(0, 0, 0, 0);
+    if constexpr (SHIFT) old = load_vector<G>(row, u, n, m);
+    else if (u * G::kVec < n) old = ld16(row + int64_t(u) * 16);
+    G::unpack(old, y);
 #pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = sum[e] * a.scale;
-  if constexpr (VEC) {
-    constexpr int n = E / G::kVec;
-#pragma unroll
-    for (int k = 0; k < n; ++k) {
-      float part[G::kVec];
-      if (a.accumulate) {
-        float old[G::kVec];
-        G::unpack(ld16(at + k * 16), old);
-#pragma unroll
-        for (int e = 0; e < G::kVec; ++e) part[e] = __fmaf_rn(sum[k * G::kVec + e], a.scale, old[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < G::kVec; ++e) part[e] = y[k * G::kVec + e];
-      }
-      st_stream16(at + k * 16, G::pack(part));
-    }
+    for (int e = 0; e < G::kVec; ++e) y[e] = __fmaf_rn(sum[e], a.scale, y[e]);
   } else {
-    if (a.accumulate) y[0] = __fmaf_rn(sum[0], a.scale, G::load1(at, 0));
-    G::store1(at, 0, y[0]);
+#pragma unroll
+    for (int e = 0; e < G::kVec; ++e) y[e] = sum[e] * a.scale;
+  }
+  if constexpr (SHIFT) store_vector<G>(row, u, n, G::pack(y));
+  else if (u * G::kVec < n) st_stream16(row + int64_t(u) * 16, G::pack(y));
+}
+
+// E sums a lane, of elements u * E .. of row v; all lanes of a warp, with consecutive u.
+template <class G, bool SHIFT, int E>
+__device__ __forceinline__ void write_grad(const GradArgs& a, uint32_t v, int u, const float (&sum)[E], const Bytes& m) {
+  unsigned char* row = a.g + int64_t(v) * a.g_pitch;
+  if constexpr (E == G::kVec) {
+    write_vector<G, SHIFT>(a, row, u, sum, m);
+  } else {
+    // sixteen bits into 32: a lane's elements are two vectors.  Each half of the warp's elements is dealt out, a vector a lane.
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float part[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float lo = __shfl_sync(~0u, sum[e], half * 16 + lane / 2), hi = __shfl_sync(~0u, sum[e + 4], half * 16 + lane / 2);
+        part[e] = lane & 1 ? hi : lo;
+      }
+      write_vector<G, SHIFT>(a, row, (u - lane) * 2 + half * 32 + lane, part, m);
+    }
   }
 }
 
 constexpr int kRowThreads = 128, kAhead = 8;
 
-template <class D, class G, bool VEC>
+template <class D, class G, bool SHIFT>
 __global__ void __launch_bounds__(kRowThreads) k_embedding_rows(GradArgs a) {
-  constexpr int E = VEC ? D::kVec : 1;
+  constexpr int E = D::kVec;
+  griddep_wait();
+  griddep_launch();
   const int64_t chunk_ctas = a.chunks * a.slices;
   if (blockIdx.x >= chunk_ctas) {
     // rows without a token
@@ -281,49 +395,47 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding_rows(GradArgs a) {
     }
     return;
   }
-  __shared__ uint32_t keys[kChunk + 2], pos[kChunk];
-  const int64_t chunk = blockIdx.x / a.slices, first = chunk * kChunk;
-  const int64_t u = (blockIdx.x - chunk * a.slices) * int64_t(kRowThreads) + threadIdx.x;
-  if (threadIdx.x < kChunk + 2) {
+  __shared__ uint32_t keys[kMostChunk + 2], pos[kMostChunk];
+  const int64_t chunk = blockIdx.x / a.slices, first = chunk * a.chunk;
+  const int u = int(blockIdx.x - chunk * a.slices) * kRowThreads + int(threadIdx.x);
+  if (threadIdx.x < a.chunk + 2) {
     const int64_t i = first + int(threadIdx.x) - 1;
     keys[threadIdx.x] = i >= 0 && i < a.T ? a.sorted_keys[i] : 0xffffffffu;
-    if (threadIdx.x >= 1 && threadIdx.x <= kChunk && i < a.T) pos[threadIdx.x - 1] = a.sorted_pos[i];
+    if (threadIdx.x >= 1 && threadIdx.x <= a.chunk && i < a.T) pos[threadIdx.x - 1] = a.sorted_pos[i];
   }
   __syncthreads();
-  if (u >= a.units) return;
-  const unsigned char* column = a.dy + u * (E * D::kBytes);
+  if ((u & ~31) >= a.units) return;  // warps stay whole
+  const int n = int(a.D);
+  const Bytes dm = bytes_of(a.dy, a.T, a.dy_pitch, a.D * D::kBytes), gm = bytes_of(a.g, a.V, a.g_pitch, a.D * G::kBytes);
   float sum[E] = {};
   bool head = keys[0] == keys[1];  // the run came from the chunk before
-  for (int i = 0; i < kChunk && keys[i + 1] < a.V; i += kAhead) {
+  for (int i = 0; i < a.chunk && keys[i + 1] < a.V; i += kAhead) {
     uint4 q[kAhead];
-    float s[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (keys[i + j + 1] < a.V) {
-        const unsigned char* at = column + int64_t(pos[i + j]) * a.dy_pitch;
-        if constexpr (VEC) q[j] = ld_stream16(at);
-        else s[j] = D::load1(at, 0);
-      }
+    for (int j = 0; j < kAhead; ++j) {
+      if (keys[i + j + 1] >= a.V) continue;
+      const unsigned char* row = a.dy + int64_t(pos[i + j]) * a.dy_pitch;
+      if constexpr (SHIFT) q[j] = load_vector<D>(row, u, n, dm);
+      else q[j] = u < a.units ? ld_stream16(row + int64_t(u) * 16) : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const uint32_t key = keys[i + j + 1], next = keys[i + j + 2];
       if (key >= a.V) break;
-      if constexpr (VEC) {
-        float f[E];
-        D::unpack(q[j], f);
+      float f[E];
+      D::unpack(q[j], f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum[e] += f[e];
-      } else {
-        sum[0] += s[j];
-      }
-      const bool last = i + j + 1 == kChunk;
+      for (int e = 0; e < E; ++e) sum[e] += f[e];
+      const bool last = i + j + 1 == a.chunk;
       if (next == key && !last) continue;
       if (head || (last && next == key)) {
-        float* part = a.parts + (chunk * 2 + (head ? 0 : 1)) * a.part_pitch + u * E;
+        float* part = a.parts + (chunk * 2 + (head ? 0 : 1)) * a.part_pitch + int64_t(u) * E;
+        if (u < a.units) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) part[e] = sum[e];
+          for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(part + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+        }
       } else {
-        write_grad<G, VEC, E>(a, key, u, sum);
+        write_grad<G, SHIFT, E>(a, key, u, sum, gm);
       }
       head = false;
 #pragma unroll
@@ -332,43 +444,80 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding_rows(GradArgs a) {
   }
 }
 
-// Runs that go over the end of the chunk they begin in: a CTA takes 32 columns of one, eight warps every eighth partial sum.
-constexpr int kJoinWarps = 8;
+// Runs that go over the end of the chunk they begin in: a warp looks at one chunk for its run, and adds up the partial sums where they
+// are few; those of longer runs the CTA's warps take together, every eighth each.
+constexpr int kJoinWarps = 8, kJoinAlone = 16, kJoinColumns = 128;  // columns of a warp at a time, four a lane
+
+template <class G>
+__device__ __forceinline__ void write_four(const GradArgs& a, uint32_t key, int64_t c, const float4& sum) {
+  unsigned char* row = a.g + int64_t(key) * a.g_pitch;
+  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + e < a.D) G::store1(row, c + e, a.accumulate ? __fmaf_rn(v[e], a.scale, load1c<G>(row, c + e)) : v[e] * a.scale);
+}
+__device__ __forceinline__ void add(float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
 
 template <class G>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_embedding_join(GradArgs a) {
-  const int64_t chunk = blockIdx.x, end = (chunk + 1) * kChunk;
-  if (end >= a.T) return;
-  const uint32_t key = a.sorted_keys[end];
-  if (key >= a.V || a.sorted_keys[end - 1] != key) return;
-  if (chunk > 0 && a.sorted_keys[chunk * kChunk] == key && a.sorted_keys[chunk * kChunk - 1] == key) return;  // began earlier
-  // the last chunk that the run reaches: its first token is the run's
-  int64_t lo = chunk + 1, step = 1;
-  while (lo + step < a.chunks && a.sorted_keys[(lo + step) * kChunk] == key) {
-    lo += step;
-    step *= 2;
-  }
-  int64_t hi = lo + step < a.chunks ? lo + step : a.chunks;  // lo is the run's, hi is not
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (a.sorted_keys[mid * kChunk] == key) lo = mid;
-    else hi = mid;
-  }
-  const int64_t n = lo - chunk + 1;  // parts: the chunk's second, then the first of each that follows
-  __shared__ float sums[kJoinWarps][32];
+  __shared__ float4 sums[kJoinWarps][32];
+  __shared__ int64_t lengths[kJoinWarps];
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t c0 = int64_t(blockIdx.y) * 32; c0 < a.D; c0 += int64_t(gridDim.y) * 32) {
-    const int64_t c = c0 + lane;
-    float sum = 0.f;
-    if (c < a.D)
-      for (int64_t k = warp; k < n; k += kJoinWarps) sum += a.parts[((chunk + k) * 2 + (k == 0)) * a.part_pitch + c];
-    __syncthreads();
-    sums[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && c < a.D) {
-      float one[1] = {0.f};
-      for (int w = 0; w < kJoinWarps; ++w) one[0] += sums[w][lane];
-      write_grad<G, false, 1>(a, key, c, one);
+  const uint32_t* keys = a.sorted_keys;
+  const int64_t C = a.chunk, chunk0 = int64_t(blockIdx.x) * kJoinWarps, chunk = chunk0 + warp, end = (chunk + 1) * C;
+  uint32_t key = 0;
+  int64_t n = 0;  // parts of the run that begins in this warp's chunk: the chunk's second, then the first of each that follows
+  if (end < a.T) {
+    key = keys[end];
+    const bool begins = key < a.V && keys[end - 1] == key && !(chunk > 0 && keys[chunk * C] == key && keys[chunk * C - 1] == key);
+    if (begins) {
+      // the last chunk that the run reaches: its first token is the run's
+      int64_t lo = chunk + 1, step = 1;
+      while (lo + step < a.chunks && keys[(lo + step) * C] == key) {
+        lo += step;
+        step *= 2;
+      }
+      int64_t hi = lo + step < a.chunks ? lo + step : a.chunks;  // lo is the run's, hi is not
+      while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) / 2;
+        if (keys[mid * C] == key) lo = mid;
+        else hi = mid;
+      }
+      n = lo - chunk + 1;
+    }
+  }
+  const int64_t c0 = int64_t(blockIdx.y) * kJoinColumns + lane * 4, step = int64_t(gridDim.y) * kJoinColumns;
+  const auto part = [&](int64_t first, int64_t k, int64_t c) {
+    return *reinterpret_cast<const float4*>(a.parts + ((first + k) * 2 + (k == 0)) * a.part_pitch + c);
+  };
+  if (n > 0 && n <= kJoinAlone)
+    for (int64_t c = c0; c < a.D; c += step) {
+      float4 sum = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+      for (int64_t k = 0; k < n; ++k) add(sum, part(chunk, k, c));
+      write_four<G>(a, key, c, sum);
+    }
+  if (lane == 0) lengths[warp] = n > kJoinAlone ? n : 0;
+  __syncthreads();
+  for (int w = 0; w < kJoinWarps; ++w) {
+    n = lengths[w];
+    if (n == 0) continue;
+    key = keys[(chunk0 + w + 1) * C];
+    for (int64_t c = c0; c - lane * 4 < a.D; c += step) {
+      float4 sum = make_float4(0, 0, 0, 0);
+      if (c < a.D) {
+#pragma unroll 8
+        for (int64_t k = warp; k < n; k += kJoinWarps) add(sum, part(chunk0 + w, k, c));
+      }
+      __syncthreads();
+      sums[warp][lane] = sum;
+      __syncthreads();
+      if (warp == 0 && c < a.D) {
+#pragma unroll
+        for (int i = 1; i < kJoinWarps; ++i) add(sum, sums[i][lane]);
+        write_four<G>(a, key, c, sum);
+      }
     }
   }
 }
@@ -379,13 +528,15 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 struct Scratch {
   size_t list, bits, parts, bytes;
   int64_t part_pitch, chunks;
+  int chunk;
 };
 Scratch scratch_of(int64_t T, int64_t V, int64_t D) {
   Scratch s;
   s.list = up256(size_t(T) * 4);
   s.bits = up256(size_t((V + 31) / 32) * 4);
   s.part_pitch = (D + 7) / 8 * 8;
-  s.chunks = (T + kChunk - 1) / kChunk;
+  s.chunk = chunk_of(T, D);
+  s.chunks = (T + s.chunk - 1) / s.chunk;
   s.parts = up256(size_t(s.chunks) * 2 * size_t(s.part_pitch) * 4);
   s.bytes = 4 * s.list + s.bits + s.parts + 256;
   return s;
@@ -412,6 +563,7 @@ cudaError_t launch_grad(const EmbeddingGrad& p, const DeviceInfo& dev) {
   a.g_pitch = p.g_pitch * G::kBytes;
   a.part_pitch = s.part_pitch;
   a.chunks = s.chunks;
+  a.chunk = s.chunk;
   a.token_bytes = p.token_bytes;
   int bits = 1;
   while (p.V >> bits) ++bits;  // keys 0 .. V
@@ -422,30 +574,33 @@ cudaError_t launch_grad(const EmbeddingGrad& p, const DeviceInfo& dev) {
   a.scale = p.scale;
   a.accumulate = p.accumulate;
   a.status = dev.status;
-  const bool grad16 = ((reinterpret_cast<uintptr_t>(a.g) | uintptr_t(a.g_pitch) | uintptr_t(p.D * G::kBytes)) & 15) == 0;
-  const bool vec = grad16 && ((reinterpret_cast<uintptr_t>(a.dy) | uintptr_t(a.dy_pitch) | uintptr_t(p.D * D::kBytes)) & 15) == 0;
-  a.fill_vec = grad16;
-  a.units = uint32_t(vec ? p.D / D::kVec : p.D);
-  a.slices = int((a.units + kRowThreads - 1) / kRowThreads);
+  a.fill_vec = on16({reinterpret_cast<uintptr_t>(a.g), uintptr_t(a.g_pitch), uintptr_t(p.D * G::kBytes)});
+  const bool vec = a.fill_vec && on16({reinterpret_cast<uintptr_t>(a.dy), uintptr_t(a.dy_pitch), uintptr_t(p.D * D::kBytes)});
+  a.units = int((p.D + D::kVec - 1) / D::kVec);
+  a.slices = (a.units + kRowThreads - 1) / kRowThreads;
   a.fill_rows = (65536 + p.D * G::kBytes - 1) / (p.D * G::kBytes);
   const int64_t fill = p.accumulate ? 0 : (p.V + a.fill_rows - 1) / a.fill_rows;
   cudaError_t e;
-  const size_t shared = (size_t(1) << a.digit_bits) * 35 * 4;
-  if ((e = cudaFuncSetAttribute(k_sort_tokens, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared))) != cudaSuccess) return e;
-  k_sort_tokens<<<kSortCtas, kSortThreads, shared, p.stream>>>(a);
+  if (p.T <= kRankTokens && (p.V + 31) / 32 <= int64_t(kRankWords) * dev.sm_count) {
+    a.sorted_keys = a.keys[0];
+    a.sorted_pos = a.pos[0];
+    k_rank_tokens<<<unsigned(dev.sm_count), kSortThreads, 0, p.stream>>>(a);
+  } else {
+    const size_t shared = (size_t(1) << a.digit_bits) * 35 * 4;
+    if ((e = cudaFuncSetAttribute(k_sort_tokens, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared))) != cudaSuccess) return e;
+    k_sort_tokens<<<kSortCtas, kSortThreads, shared, p.stream>>>(a);
+  }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t ctas = a.chunks * a.slices + fill;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  if (ctas > 0) {
-    if (vec) k_embedding_rows<D, G, true><<<unsigned(ctas), kRowThreads, 0, p.stream>>>(a);
-    else k_embedding_rows<D, G, false><<<unsigned(ctas), kRowThreads, 0, p.stream>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
+  if (ctas > 0 && (e = launch_after(vec ? k_embedding_rows<D, G, false> : k_embedding_rows<D, G, true>, dim3(unsigned(ctas)), kRowThreads, p.stream, a)) != cudaSuccess)
+    return e;
   if (a.chunks > 1) {
-    const int64_t columns = (p.D + 31) / 32;
-    k_embedding_join<G><<<dim3(unsigned(a.chunks), unsigned(columns < 1024 ? columns : 1024)), kJoinWarps * 32, 0, p.stream>>>(a);
+    const int64_t columns = (p.D + kJoinColumns - 1) / kJoinColumns;
+    return launch_after(k_embedding_join<G>, dim3(unsigned((a.chunks + kJoinWarps - 1) / kJoinWarps), unsigned(columns < 32 ? columns : 32)), kJoinWarps * 32,
+                        p.stream, a);
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace

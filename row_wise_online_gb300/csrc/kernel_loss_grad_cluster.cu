@@ -89,40 +89,7 @@ __device__ __forceinline__ void copy_edges(const Part& p, uint32_t slot, int lan
 }
 
 // 16 bytes of shared memory from byte delta (a multiple of 2, below 16) of an aligned address on.
-__device__ __forceinline__ uint4 lds16_shifted(uint32_t at, int delta) {
-  const uint4 a = lds16(at), b = lds16(at + 16);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  const int words = delta >> 2;
-  if (words & 2) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (words & 1) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  const uint32_t bits = (delta & 3) * 8;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Elements [from, to) of a vector, the others -inf.
-template <class D>
-__device__ __forceinline__ uint4 keep(uint4 q, int from, int to) {
-  uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  constexpr int n = 4 / D::kBytes;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (n == 1) {
-      if (i < from || i >= to) w[i] = D::kNegInfWord;
-    } else {
-      if (2 * i < from || 2 * i >= to) w[i] = (w[i] & 0xffff0000u) | (D::kNegInfWord & 0xffffu);
-      if (2 * i + 1 < from || 2 * i + 1 >= to) w[i] = (w[i] & 0xffffu) | (D::kNegInfWord & 0xffff0000u);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+__device__ __forceinline__ uint4 lds16_shifted(uint32_t at, int delta) { return shifted(lds16(at), lds16(at + 16), delta); }
 
 // s and n of elements [from, to) of a vector.
 template <class D>
@@ -187,7 +154,7 @@ __global__ void __launch_bounds__(T, 8192 / (T * K)) k_loss_grad_cluster(Args a)
       if (j < p.j1) {
         q[k] = SHIFT ? lds16_shifted(slot + i * 16, p.delta) : lds16(slot + i * 16);
         if (j >= p.w0 && j < p.w1) whole |= 1u << k;
-        else q[k] = keep<D>(q[k], max(0, p.lead - j * E), min(E, int(a.p.N) + p.lead - j * E));
+        else q[k] = keep<D>(q[k], max(0, p.lead - j * E), min(E, int(a.p.N) + p.lead - j * E), D::kNegInfWord);
       }
     }
     const auto refill = [&] {  // every thread has read the slot

@@ -28,7 +28,7 @@ struct NormArgs {
   int64_t x_pitch, r_pitch, h_pitch, y_pitch;  // bytes
   int64_t groups;                              // scales of a row
   float eps, offset;
-  bool w_f32;
+  bool w_f32, w_vec;  // w_vec: on a 16-byte boundary
 };
 
 struct GradArgs {
@@ -45,7 +45,7 @@ struct GradArgs {
   int64_t rows_per_part;
   int parts_n;
   float offset;
-  bool w_f32, accumulate;
+  bool w_f32, w_vec, accumulate;
 };
 
 template <class D, class A>
@@ -188,18 +188,20 @@ __global__ void __launch_bounds__(kThreads) k_rms_weight_grad(GradArgs a) {
 
 // ---- rows in registers ------------------------------------------------------------------------------------------------
 //
-// W warps own a row.  VEC: thread t of the group has the 16-byte vectors t, t + 32 W, ...; else its warp has runs of 128
-// elements (run w, w + W, ...), a lane every 32nd of one.  Either way the 128 elements that share a scale in 8 bits lie in
-// one warp.
+// W warps own a row: thread t of the group has the vectors t, t + 32 W, ...  SHIFT: rows that start anywhere, of any length
+// (load_vector, store_vector); else they are on 16-byte boundaries.  The 128 elements that share a scale in 8 bits lie in one
+// warp.
 
-template <class D, int W, bool VEC>
-struct Place {
-  static constexpr int E = VEC ? D::kVec : 1;
-  // Unit k of a thread: a vector, or an element.
-  __device__ static __forceinline__ int unit(int t, int k) {
-    return VEC ? t + k * (W * 32) : ((t >> 5) + (k >> 2) * W) * kGroup + (k & 3) * 32 + (t & 31);
-  }
-};
+template <class D, bool SHIFT>
+__device__ __forceinline__ uint4 take(const unsigned char* row, int u, int units, int n, const Bytes& m) {
+  if constexpr (SHIFT) return load_vector<D>(row, u, n, m);
+  else return u < units ? ld_stream16(row + int64_t(u) * 16) : make_uint4(0, 0, 0, 0);
+}
+template <class D, bool SHIFT>
+__device__ __forceinline__ void put(unsigned char* row, int u, int units, int n, const uint4& q) {
+  if constexpr (SHIFT) store_vector<D>(row, u, n, q);
+  else if (u < units) st_stream16(row + int64_t(u) * 16, q);
+}
 
 // The sum of v over the W warps of a group, the same in all threads.  slots: W floats of the group, another set for the next call.
 template <int W>
@@ -229,114 +231,91 @@ __device__ __forceinline__ float group_max(float v, float* slots, int group, int
   return v;
 }
 
-// The factors weight + offset of unit u.
-template <class D, bool VEC, class A>
-__device__ __forceinline__ void weights(const A& a, int u, float (&w)[VEC ? D::kVec : 1]) {
-  constexpr int E = VEC ? D::kVec : 1;
+// The factors weight + offset of vector u, 0 behind the row's end.
+template <class D, bool SHIFT, class A>
+__device__ __forceinline__ void weights(const A& a, int u, float (&w)[D::kVec]) {
+  constexpr int E = D::kVec;
+  const int left = SHIFT ? int(a.N) - u * E : E;
   if (!a.w) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) w[e] = 1.f;
+    for (int e = 0; e < E; ++e) w[e] = e < left ? 1.f : 0.f;
     return;
   }
-  if constexpr (VEC) {
-    if (a.w_f32 && D::kBytes == 2) {
-      const float4* p = static_cast<const float4*>(a.w) + 2 * u;
-      const float4 lo = __ldg(p), hi = __ldg(p + 1);
-      w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
-      w[E - 4] = hi.x, w[E - 3] = hi.y, w[E - 2] = hi.z, w[E - 1] = hi.w;
-    } else {
-      D::unpack(__ldg(static_cast<const uint4*>(a.w) + u), w);
-    }
+  if (SHIFT && (left < E || !a.w_vec)) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] = e < left ? weight1<D>(a, int64_t(u) * E + e) : 0.f;
+    return;
+  }
+  if (a.w_f32 && D::kBytes == 2) {
+    const float4* p = static_cast<const float4*>(a.w) + 2 * u;
+    const float4 lo = __ldg(p), hi = __ldg(p + 1);
+    w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
+    w[E - 4] = hi.x, w[E - 3] = hi.y, w[E - 2] = hi.z, w[E - 1] = hi.w;
   } else {
-    w[0] = a.w_f32 ? __ldg(static_cast<const float*>(a.w) + u) : D::load1(a.w, u);
+    D::unpack(__ldg(static_cast<const uint4*>(a.w) + u), w);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) w[e] += a.offset;
 }
 
-// What a thread holds of a unit: packed elements, or one in 32 bits.
-template <class D, bool VEC>
-struct Held {
-  static constexpr int E = VEC ? D::kVec : 1;
-  uint4 q;
-  __device__ __forceinline__ void load(const unsigned char* row, int u) { q = ld_stream16(row + int64_t(u) * 16); }
-  __device__ __forceinline__ void clear() { q = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&v)[E]) const { D::unpack(q, v); }
-  __device__ __forceinline__ void set(const float (&v)[E]) { q = D::pack(v); }
-  __device__ __forceinline__ void store(unsigned char* row, int u) const { st_stream16(row + int64_t(u) * 16, q); }
-};
-template <class D>
-struct Held<D, false> {
-  float q;
-  __device__ __forceinline__ void load(const unsigned char* row, int u) { q = D::load1(row, u); }
-  __device__ __forceinline__ void clear() { q = 0.f; }
-  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = q; }
-  __device__ __forceinline__ void set(const float (&v)[1]) { q = rounded<D>(v[0]); }
-  __device__ __forceinline__ void store(unsigned char* row, int u) const { D::store1(row, u, q); }
-};
-
-// E codes of unit u.
-template <int E>
-__device__ __forceinline__ void store_codes(unsigned char* row, int u, const float (&v)[E], float inv) {
-  if constexpr (E == 8) {
-    uint2 c;
-    c.x = uint32_t(pack_e4m3x2(v[0] * inv, v[1] * inv)) | uint32_t(pack_e4m3x2(v[2] * inv, v[3] * inv)) << 16;
-    c.y = uint32_t(pack_e4m3x2(v[4] * inv, v[5] * inv)) | uint32_t(pack_e4m3x2(v[6] * inv, v[7] * inv)) << 16;
-    *reinterpret_cast<uint2*>(row + int64_t(u) * 8) = c;
-  } else if constexpr (E == 4) {
-    *reinterpret_cast<uint32_t*>(row + int64_t(u) * 4) =
-        uint32_t(pack_e4m3x2(v[0] * inv, v[1] * inv)) | uint32_t(pack_e4m3x2(v[2] * inv, v[3] * inv)) << 16;
+// The codes of vector u, left elements of it.
+template <int E, bool SHIFT>
+__device__ __forceinline__ void store_codes(unsigned char* row, int u, int left, const float (&v)[E], float inv) {
+  uint16_t c[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) c[e] = pack_e4m3x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+  unsigned char* p = row + int64_t(u) * E;
+  if (SHIFT && (left < E || (reinterpret_cast<uintptr_t>(p) & (E - 1)))) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e < left) p[e] = (unsigned char)(c[e / 2] >> (e & 1) * 8);
+  } else if constexpr (E == 8) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(c[0] | uint32_t(c[1]) << 16, c[2] | uint32_t(c[3]) << 16);
   } else {
-    row[u] = (unsigned char)(pack_e4m3x2(v[0] * inv, 0.f) & 0xff);
+    *reinterpret_cast<uint32_t*>(p) = c[0] | uint32_t(c[1]) << 16;
   }
 }
 
 __host__ __device__ constexpr int reg_threads(int warps) { return warps * 32 > 256 ? warps * 32 : 256; }
 
-template <class D, int K, int W, bool VEC, bool E4M3>
-__global__ void __launch_bounds__(reg_threads(W)) k_rms_norm(NormArgs a) {
-  using P = Place<D, W, VEC>;
-  constexpr int E = P::E, GT = W * 32, G = reg_threads(W) / GT;
+// CTAs of 256 threads an SM: in 8 bits three (16384 x 8192 bf16 with a residual 156 us; two, which the compiler takes by
+// itself, 182; four 176), else four (16384 x 8192 bf16 84 us, three 93, six 91).
+template <class D, int K, int W, bool SHIFT, bool E4M3>
+__global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 ? 3 : 4) * 256 / reg_threads(W)) k_rms_norm(NormArgs a) {
+  constexpr int E = D::kVec, GT = W * 32, G = reg_threads(W) / GT;
   __shared__ float sums[2][reg_threads(W) / 32], tops[2][reg_threads(W) / 32];
   const int group = threadIdx.x / GT, t = threadIdx.x % GT, lane = t & 31;
-  const int units = int(a.N / E);
+  const int n = int(a.N), units = (n + E - 1) / E;
+  const int64_t bytes = a.N * D::kBytes;
+  const Bytes xm = bytes_of(a.x, a.M, a.x_pitch, bytes), rm = bytes_of(a.r, a.M, a.r_pitch, bytes);
   int it = 0;
   for (int64_t row = int64_t(blockIdx.x) * G + group; row < a.M; row += int64_t(gridDim.x) * G, it ^= 1) {
     const unsigned char* xr = a.x + row * a.x_pitch;
-    Held<D, VEC> h[K];
+    uint4 h[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int u = P::unit(t, k);
-      if (u < units) h[k].load(xr, u);
-      else h[k].clear();
-    }
+    for (int k = 0; k < K; ++k) h[k] = take<D, SHIFT>(xr, t + k * GT, units, n, xm);
     if (a.r) {
       const unsigned char* rr = a.r + row * a.r_pitch;
       unsigned char* to = a.h + row * a.h_pitch;
-      Held<D, VEC> r[K];
+      uint4 r[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) r[k] = take<D, SHIFT>(rr, t + k * GT, units, n, rm);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int u = P::unit(t, k);
-        if (u < units) r[k].load(rr, u);
-        else r[k].clear();
-      }
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int u = P::unit(t, k);
         float v[E], w[E];
-        h[k].get(v);
-        r[k].get(w);
+        D::unpack(h[k], v);
+        D::unpack(r[k], w);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] += w[e];
-        h[k].set(v);
-        if (u < units) h[k].store(to, u);
+        h[k] = D::pack(v);
+        put<D, SHIFT>(to, t + k * GT, units, n, h[k]);
       }
     }
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float v[E];
-      h[k].get(v);
+      D::unpack(h[k], v);
 #pragma unroll
       for (int e = 0; e < E; ++e) sum = __fmaf_rn(v[e], v[e], sum);
     }
@@ -344,33 +323,31 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_norm(NormArgs a) {
     const float rstd = 1.f / sqrtf(sum / float(a.N) + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     unsigned char* yr = a.y + row * a.y_pitch;
+    const auto value = [&](int k, float(&v)[E]) {  // y in 32 bits, 0 behind the row's end
+      const int u = t + k * GT;
+      float w[E];
+      D::unpack(h[k], v);
+      weights<D, SHIFT>(a, min(u, units - 1), w);  // h is 0 behind the end
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = v[e] * rstd * w[e];
+    };
     if constexpr (!E4M3) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int u = P::unit(t, k);
-        if (u >= units) continue;
-        float v[E], w[E];
-        h[k].get(v);
-        weights<D, VEC>(a, u, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = v[e] * rstd * w[e];
-        h[k].set(v);
-        h[k].store(yr, u);
+        float v[E];
+        value(k, v);
+        put<D, SHIFT>(yr, t + k * GT, units, n, D::pack(v));
       }
     } else {
-      const auto value = [&](int k, float(&v)[E]) {  // y in 32 bits, 0 behind the row's end
-        const int u = P::unit(t, k);
-        float w[E];
-        h[k].get(v);
-        if (u < units) weights<D, VEC>(a, u, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = u < units ? v[e] * rstd * w[e] : 0.f;
-      };
       const auto top_of = [&](const float(&v)[E]) {
         float m = fabsf(v[0]);
 #pragma unroll
         for (int e = 1; e < E; ++e) m = fmaxf(m, fabsf(v[e]));
         return m;
+      };
+      const auto store = [&](int k, const float(&v)[E], float inv) {
+        const int u = t + k * GT;
+        if (u < units) store_codes<E, SHIFT>(yr, u, n - u * E, v, inv);
       };
       if (a.groups == 1 && a.N > kGroup) {
         float y[K][E], top = 0.f;
@@ -383,28 +360,20 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_norm(NormArgs a) {
         const float scale = fmaxf(top / kE4m3Max, kScaleMin), inv = 1.f / scale;
         if (t == 0) a.scales[row] = scale;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          const int u = P::unit(t, k);
-          if (u < units) store_codes<E>(yr, u, y[k], inv);
-        }
+        for (int k = 0; k < K; ++k) store(k, y[k], inv);
       } else {
-        constexpr int step = VEC ? 1 : 4, lanes = VEC ? kGroup / E : 32;  // units of a group in a lane; lanes of a group
+        constexpr int lanes = kGroup / E;  // of a group
 #pragma unroll
-        for (int k = 0; k < K; k += step) {
-          float y[step][E], top = 0.f;
-#pragma unroll
-          for (int j = 0; j < step; ++j) {
-            value(k + j, y[j]);
-            top = fmaxf(top, top_of(y[j]));
-          }
+        for (int k = 0; k < K; ++k) {
+          float y[E];
+          value(k, y);
+          float top = top_of(y);
 #pragma unroll
           for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
           const float scale = fmaxf(top / kE4m3Max, kScaleMin), inv = 1.f / scale;
-          const int u = P::unit(t, k);
-          if (u < units && (lane & (lanes - 1)) == 0) a.scales[row * a.groups + u * E / kGroup] = scale;
-#pragma unroll
-          for (int j = 0; j < step; ++j)
-            if (P::unit(t, k + j) < units) store_codes<E>(yr, P::unit(t, k + j), y[j], inv);
+          const int u = t + k * GT;
+          if (u < units && (lane & (lanes - 1)) == 0) a.scales[row * a.groups + u / lanes] = scale;
+          store(k, y, inv);
         }
       }
     }
@@ -412,145 +381,272 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_norm(NormArgs a) {
 }
 
 // Backward: every CTA walks its rows with the columns' sums of dw in registers, and leaves them as one part.
-template <class D, int K, int W, bool VEC>
+template <class D, int K, int W, bool SHIFT>
 __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
-  using P = Place<D, W, VEC>;
-  constexpr int E = P::E, GT = W * 32, G = reg_threads(W) / GT;
+  constexpr int E = D::kVec, GT = W * 32, G = reg_threads(W) / GT;
   __shared__ float sums[2][reg_threads(W) / 32];
   __shared__ float columns[G > 1 ? K * E * GT : 1];
   const int group = threadIdx.x / GT, t = threadIdx.x % GT;
-  const int units = int(a.N / E);
-  const int64_t step = int64_t(gridDim.x) * G;
+  const int n = int(a.N), units = (n + E - 1) / E;
+  const int64_t step = int64_t(gridDim.x) * G, bytes = a.N * D::kBytes;
+  const Bytes dm = bytes_of(a.dy, a.M, a.dy_pitch, bytes), hm = bytes_of(a.h, a.M, a.h_pitch, bytes), gm = bytes_of(a.sg, a.M, a.sg_pitch, bytes);
   float dw[K][E] = {};
-  Held<D, VEC> dy[K], h[K], sg[K];
-  float rstd = 0.f;
-  const auto fetch = [&](int64_t row) {
+  int it = 0;
+  for (int64_t row = int64_t(blockIdx.x) * G + group; row < a.M; row += step, it ^= 1) {
+    uint4 dy[K], h[K], sg[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = P::unit(t, k);
-      if (u < units) {
-        dy[k].load(a.dy + row * a.dy_pitch, u);
-        h[k].load(a.h + row * a.h_pitch, u);
-        if (a.sg) sg[k].load(a.sg + row * a.sg_pitch, u);
-      }
+      const int u = t + k * GT;
+      dy[k] = take<D, SHIFT>(a.dy + row * a.dy_pitch, u, units, n, dm);
+      h[k] = take<D, SHIFT>(a.h + row * a.h_pitch, u, units, n, hm);
+      sg[k] = a.sg ? take<D, SHIFT>(a.sg + row * a.sg_pitch, u, units, n, gm) : make_uint4(0, 0, 0, 0);
     }
-    rstd = a.rstd[row];
-  };
-#pragma unroll
-  for (int k = 0; k < K; ++k) dy[k].clear(), h[k].clear(), sg[k].clear();
-  int64_t row = int64_t(blockIdx.x) * G + group;
-  if (row < a.M) fetch(row);
-  int it = 0;
-  for (; row < a.M; row += step, it ^= 1) {
+    const float rstd = a.rstd[row];
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = P::unit(t, k);
+      const int u = t + k * GT;
       if (u >= units) continue;
       float d[E], x[E], w[E];
-      dy[k].get(d);
-      h[k].get(x);
-      weights<D, VEC>(a, u, w);
+      D::unpack(dy[k], d);
+      D::unpack(h[k], x);
+      weights<D, SHIFT>(a, u, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float p = d[e] * (x[e] * rstd);
+        const float p = d[e] * x[e];
         sum = __fmaf_rn(p, w[e], sum);
-        dw[k][e] += p;
+        dw[k][e] = __fmaf_rn(p, rstd, dw[k][e]);
       }
     }
-    const float mean = group_sum<W>(sum, sums[it] + group * W, group, t) / float(a.N);
+    sum = group_sum<W>(sum, sums[it] + group * W, group, t);  // and every load of the row is done
+    const float slope = -(rstd * rstd * rstd) * (sum / float(a.N));
     unsigned char* to = a.dx + row * a.dx_pitch;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = P::unit(t, k);
-      if (u >= units) continue;
-      float d[E], x[E], w[E], s[E];
-      dy[k].get(d);
-      h[k].get(x);
-      sg[k].get(s);
-      weights<D, VEC>(a, u, w);
+      const int u = t + k * GT;
+      float d[E], x[E], w[E] = {}, s[E];
+      D::unpack(dy[k], d);
+      D::unpack(h[k], x);
+      D::unpack(sg[k], s);
+      if (u < units) weights<D, SHIFT>(a, u, w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float v = rstd * __fmaf_rn(-(x[e] * rstd), mean, d[e] * w[e]);
-        d[e] = a.sg ? v + s[e] : v;
-      }
-      Held<D, VEC> out;
-      out.set(d);
-      out.store(to, u);
+      for (int e = 0; e < E; ++e) d[e] = __fmaf_rn(rstd, d[e] * w[e], __fmaf_rn(slope, x[e], s[e]));
+      put<D, SHIFT>(to, u, units, n, D::pack(d));
     }
-    if (row + step < a.M) fetch(row + step);
   }
+  griddep_launch();
   if (!a.dw) return;
   float* part = a.parts + blockIdx.x * a.N;
-  if constexpr (G == 1) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int u = P::unit(t, k);
-      if (u >= units) continue;
-#pragma unroll
-      for (int e = 0; e < E; ++e) part[u * E + e] = dw[k][e];
-    }
-  } else {
-    // the groups' sums one after the other
-    for (int g = 0; g < G; ++g) {
-      if (group == g) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            float* c = columns + (k * E + e) * GT + t;
-            *c = g ? *c + dw[k][e] : dw[k][e];
-          }
-      }
-      __syncthreads();
-    }
-    if (group == 0) {
+  for (int g = 0; g < G; ++g) {  // the groups' sums one after the other
+    if (group == g) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int u = P::unit(t, k);
-        if (u >= units) continue;
+        const int u = t + k * GT;
 #pragma unroll
-        for (int e = 0; e < E; ++e) part[u * E + e] = columns[(k * E + e) * GT + t];
+        for (int e = 0; e < E; ++e) {
+          float* c = columns + (G > 1 ? (k * E + e) * GT + t : 0);
+          const float v = g ? *c + dw[k][e] : dw[k][e];
+          if (g < G - 1) *c = v;
+          else if (u * E + e < n) part[u * E + e] = v;
+        }
       }
     }
+    __syncthreads();
   }
 }
 
-// dw = the parts added up: 32 columns a CTA, eight warps every eighth part.
-__global__ void __launch_bounds__(kThreads) k_rms_weight_join(GradArgs a) {
-  __shared__ float sums[kThreads / 32][32];
+// The same with the rows on their way in shared memory: a slot has the G rows of dy, h and sum_grad that the CTA's groups take
+// next, copied by cp.async.bulk, and is read twice.  The copies of up to kMostSlots turns are under way while one is worked on,
+// whatever the registers leave of the SM's warps: 16384 x 4096 bf16 takes 88 us, with the rows in registers 103 (at the best
+// number of CTAs an SM).  Arithmetic in pairs of fp32: with single operations, 104 us.
+constexpr int kMostSlots = 4;
+
+struct RingArgs {
+  GradArgs g;
+  int slots;  // at least 2
+  uint32_t row_bytes, slot_bytes;
+  unsigned* status;
+  uint64_t wait_ns;
+};
+
+template <class D, int K, int W>
+__global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_grad_ring(RingArgs r) {
+  constexpr int E = D::kVec, GT = W * 32, G = reg_threads(W) / GT;
+  extern __shared__ __align__(128) unsigned char shared[];
+  __shared__ uint64_t full[kMostSlots];
+  __shared__ float sums[2][reg_threads(W) / 32];
+  const GradArgs& a = r.g;
+  const int tid = threadIdx.x, group = tid / GT, t = tid % GT;
+  const int units = int(a.N / E);
+  const int64_t turns = (a.M + G - 1) / G, mine = turns > blockIdx.x ? (turns - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+  const uint64_t policy = policy_evict_first();
+  bool timed_out = false;
+
+  const auto fetch = [&](int64_t i) {  // turn i of this CTA, by warp 0
+    const int s = int(i % r.slots), arrays = a.sg ? 3 : 2;
+    const int64_t row0 = (blockIdx.x + i * gridDim.x) * G;
+    const int rows = int(a.M - row0 < G ? a.M - row0 : G);
+    const uint32_t bar = smem_addr(&full[s]), slot = smem_addr(shared) + s * r.slot_bytes;
+    if (tid == 0) mbar_arrive_expect_tx(bar, uint32_t(rows * arrays) * r.row_bytes);
+    __syncwarp();
+    if (tid < rows * arrays) {
+      const int which = tid / rows, row = tid % rows;
+      const unsigned char* from = which == 0   ? a.dy + (row0 + row) * a.dy_pitch
+                                  : which == 1 ? a.h + (row0 + row) * a.h_pitch
+                                               : a.sg + (row0 + row) * a.sg_pitch;
+      bulk_g2s(slot + uint32_t(which * G + row) * r.row_bytes, from, r.row_bytes, bar, policy);
+    }
+  };
+  if (tid == 0) {
+    for (int s = 0; s < r.slots; ++s) mbar_init(smem_addr(&full[s]), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (tid < 32)
+    for (int64_t i = 0; i < r.slots && i < mine; ++i) fetch(i);
+  float2 w[K][E / 2], dw[K][E / 2];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float f[E] = {};
+    if (t + k * GT < units) weights<D, false>(a, t + k * GT, f);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) w[k][e] = make_float2(f[2 * e], f[2 * e + 1]), dw[k][e] = make_float2(0.f, 0.f);
+  }
+  int64_t row = int64_t(blockIdx.x) * G + group;
+  const int64_t step = int64_t(gridDim.x) * G;
+  float next_rstd = row < a.M ? a.rstd[row] : 0.f;
+  int s = 0;
+  uint32_t parity = 0;
+  for (int64_t i = 0; i < mine; ++i, row += step) {
+    const float rstd = next_rstd;
+    if (row + step < a.M) next_rstd = a.rstd[row + step];
+    const uint32_t dys = smem_addr(shared) + s * r.slot_bytes + group * r.row_bytes, hs = dys + G * r.row_bytes, sgs = hs + G * r.row_bytes;
+    const bool on = row < a.M;
+    if (!mbar_wait(smem_addr(&full[s]), parity, r.wait_ns)) timed_out = true;
+    const float2 rstd2 = make_float2(rstd, rstd);
+    float2 sum2 = make_float2(0.f, 0.f);  // of g h
+    if (on) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int u = t + k * GT;
+        if (u >= units) continue;
+        float2 d[E / 2], x[E / 2];
+        D::unpack2(lds16(dys + u * 16), d);
+        D::unpack2(lds16(hs + u * 16), x);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const float2 p = __fmul2_rn(d[e], x[e]);
+          sum2 = __ffma2_rn(p, w[k][e], sum2);
+          dw[k][e] = __ffma2_rn(p, rstd2, dw[k][e]);
+        }
+      }
+    }
+    float sum = sum2.x + sum2.y;
+    // the barrier here also says that every thread is done with the turn before: its slot is refilled
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    float* const slots = sums[i & 1] + group * W;
+    if ((t & 31) == 0) slots[t >> 5] = sum;
+    __syncthreads();
+    if (tid < 32 && i > 0 && i - 1 + r.slots < mine) fetch(i - 1 + r.slots);
+    if constexpr (W > 1) {
+      sum = slots[t & (W - 1)];
+#pragma unroll
+      for (int o = W >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    }
+    if (on) {
+      const float slope = -(rstd * rstd * rstd) * (sum / float(a.N));  // dx = rstd g + slope h + sum_grad
+      const float2 slope2 = make_float2(slope, slope);
+      unsigned char* to = a.dx + row * a.dx_pitch;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int u = t + k * GT;
+        if (u >= units) continue;
+        float2 d[E / 2], x[E / 2], g[E / 2] = {};
+        D::unpack2(lds16(dys + u * 16), d);
+        D::unpack2(lds16(hs + u * 16), x);
+        if (a.sg) D::unpack2(lds16(sgs + u * 16), g);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) d[e] = __ffma2_rn(__fmul2_rn(d[e], w[k][e]), rstd2, __ffma2_rn(x[e], slope2, g[e]));
+        st_stream16(to + int64_t(u) * 16, D::pack2(d));
+      }
+    }
+    if (++s == r.slots) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+  if (timed_out) atomicOr(r.status, kStatusTimeout);
+  griddep_launch();
+  if (!a.dw) return;
+  float* part = a.parts + blockIdx.x * a.N;
+  // the groups' sums one after the other, where the slots were
+  __syncthreads();
+  float* columns = reinterpret_cast<float*>(shared);
+  for (int g = 0; g < G; ++g) {
+    if (group == g) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int u = t + k * GT;
+        if (u >= units) continue;
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          float4 v = make_float4(dw[k][e / 2].x, dw[k][e / 2].y, dw[k][e / 2 + 1].x, dw[k][e / 2 + 1].y);
+          float4* c = reinterpret_cast<float4*>(columns + u * E + e);
+          if (g) v.x += c->x, v.y += c->y, v.z += c->z, v.w += c->w;
+          *(g == G - 1 ? reinterpret_cast<float4*>(part + u * E + e) : c) = v;
+        }
+      }
+    }
+    if constexpr (G > 1) __syncthreads();
+  }
+}
+
+// dw = the parts added up: 32 columns a CTA, its warps every 32nd part.
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads) k_rms_weight_join(GradArgs a) {
+  __shared__ float sums[kJoinThreads / 32][33];
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t i = int64_t(blockIdx.x) * 32 + lane;
   float sum = 0.f;
   if (i < a.N) {
-#pragma unroll 8
-    for (int k = warp; k < a.parts_n; k += kThreads / 32) sum += a.parts[k * a.N + i];
+#pragma unroll 16
+    for (int k = warp; k < a.parts_n; k += kJoinThreads / 32) sum += a.parts[k * a.N + i];
   }
   sums[warp][lane] = sum;
   __syncthreads();
-  if (warp == 0 && i < a.N) {
-    float all = 0.f;
+  // warp w: column w's sums over the warps
+  sum = sums[lane][warp];
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) all += sums[w][lane];
-    a.dw[i] = a.accumulate ? a.dw[i] + all : all;
-  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  const int64_t c = int64_t(blockIdx.x) * 32 + warp;
+  if (lane == 0 && c < a.N) a.dw[c] = a.accumulate ? a.dw[c] + sum : sum;
 }
 
 struct NormConfig {
   int warps, units;            // warps a row, units they hold
   void (*fn[2])(NormArgs);     // [e4m3]
 };
-template <class D, int K, int W, bool VEC>
+template <class D, int K, int W, bool SHIFT>
 constexpr NormConfig norm_cfg() {
-  return NormConfig{W, 32 * W * K, {k_rms_norm<D, K, W, VEC, false>, k_rms_norm<D, K, W, VEC, true>}};
+  return NormConfig{W, 32 * W * K, {k_rms_norm<D, K, W, SHIFT, false>, k_rms_norm<D, K, W, SHIFT, true>}};
 }
 struct GradConfig {
   int warps, units;
   void (*fn)(GradArgs);
 };
-template <class D, int K, int W, bool VEC>
+template <class D, int K, int W, bool SHIFT>
 constexpr GradConfig grad_cfg() {
-  return GradConfig{W, 32 * W * K, k_rms_grad<D, K, W, VEC>};
+  return GradConfig{W, 32 * W * K, k_rms_grad<D, K, W, SHIFT>};
+}
+struct RingConfig {
+  int warps, units;
+  void (*fn)(RingArgs);
+};
+template <class D, int K, int W>
+constexpr RingConfig ring_cfg() {
+  return RingConfig{W, 32 * W * K, k_rms_grad_ring<D, K, W>};
 }
 
 // The first configuration that holds a row.
@@ -579,16 +675,17 @@ uintptr_t bits(const T* p) {
 template <class D>
 cudaError_t launch_norm_type(const RmsNorm& p, const NormArgs& a, const DeviceInfo& dev) {
   // at most 64 elements a thread
-  static const NormConfig vectors[] = {norm_cfg<D, 1, 1, true>(), norm_cfg<D, 2, 1, true>(), norm_cfg<D, 4, 1, true>(), norm_cfg<D, 4, 2, true>(),
-                                       norm_cfg<D, 4, 4, true>(), norm_cfg<D, 4, 8, true>(), norm_cfg<D, 4, 16, true>(), norm_cfg<D, 8, 16, true>()};
-  static const NormConfig elements[] = {norm_cfg<D, 4, 1, false>(), norm_cfg<D, 16, 1, false>(), norm_cfg<D, 16, 4, false>(), norm_cfg<D, 32, 4, false>(),
-                                        norm_cfg<D, 32, 8, false>(), norm_cfg<D, 32, 16, false>()};
+  static const NormConfig aligned[] = {norm_cfg<D, 1, 1, false>(), norm_cfg<D, 2, 1, false>(), norm_cfg<D, 4, 1, false>(), norm_cfg<D, 4, 2, false>(),
+                                       norm_cfg<D, 4, 4, false>(), norm_cfg<D, 4, 8, false>(), norm_cfg<D, 4, 16, false>(), norm_cfg<D, 8, 16, false>()};
+  static const NormConfig anywhere[] = {norm_cfg<D, 1, 1, true>(), norm_cfg<D, 4, 1, true>(), norm_cfg<D, 4, 4, true>(), norm_cfg<D, 4, 8, true>(),
+                                        norm_cfg<D, 4, 16, true>(), norm_cfg<D, 8, 16, true>()};
   const bool e4m3 = p.out == RMS_NORM_OUT_E4M3;
   // codes of a vector are 8 or 4 bytes: half or a quarter of what the element types need
   const uintptr_t code = e4m3 ? 16 / D::kVec : 1;
   const bool vec = on16({bits(a.x), bits(a.r), bits(a.h), bits(a.y) * code, bits(static_cast<const char*>(a.w)), uintptr_t(a.x_pitch),
                          a.r ? uintptr_t(a.r_pitch | a.h_pitch) : 0, uintptr_t(a.y_pitch) * code, uintptr_t(p.N * D::kBytes)});
-  const NormConfig* c = vec ? pick(vectors, p.N / D::kVec) : pick(elements, p.N);
+  const int64_t units = (p.N + D::kVec - 1) / D::kVec;
+  const NormConfig* c = vec ? pick(aligned, units) : pick(anywhere, units);
   if (c) {
     const int threads = reg_threads(c->warps), groups = threads / 32 / c->warps;
     const int64_t ctas = (p.M + groups - 1) / groups, most = int64_t(dev.sm_count) * (dev.max_threads_per_sm / threads) * 4;
@@ -607,16 +704,42 @@ template <class D>
 cudaError_t launch_grad_type(const RmsNormGrad& p, GradArgs a, const DeviceInfo& dev) {
   // at most 32 elements a thread, whose sums of dw stay in registers
   constexpr int F = D::kBytes / 2;  // fp32 vectors have half the elements
-  static const GradConfig vectors[] = {grad_cfg<D, F, 1, true>(), grad_cfg<D, 2 * F, 1, true>(), grad_cfg<D, 4 * F, 1, true>(), grad_cfg<D, 4 * F, 2, true>(),
-                                       grad_cfg<D, 2 * F, 8, true>(), grad_cfg<D, 4 * F, 8, true>(), grad_cfg<D, 4 * F, 16, true>()};
-  static const GradConfig elements[] = {grad_cfg<D, 4, 1, false>(), grad_cfg<D, 16, 1, false>(), grad_cfg<D, 16, 4, false>(), grad_cfg<D, 16, 8, false>(),
-                                        grad_cfg<D, 32, 8, false>(), grad_cfg<D, 32, 16, false>()};
+  static const RingConfig rings[] = {ring_cfg<D, F, 1>(), ring_cfg<D, 2 * F, 1>(), ring_cfg<D, 4 * F, 1>(), ring_cfg<D, 4 * F, 2>(),
+                                     ring_cfg<D, 2 * F, 8>(), ring_cfg<D, 4 * F, 8>(), ring_cfg<D, 4 * F, 16>()};
+  static const GradConfig aligned[] = {grad_cfg<D, 4 * F, 16, false>()};  // two slots of such rows may not fit an SM
+  static const GradConfig anywhere[] = {grad_cfg<D, F, 1, true>(), grad_cfg<D, 2 * F, 2, true>(), grad_cfg<D, 2 * F, 8, true>(), grad_cfg<D, 4 * F, 8, true>(),
+                                        grad_cfg<D, 4 * F, 16, true>()};
   const bool vec = on16({bits(a.dy), bits(a.h), bits(a.sg), bits(a.dx), bits(static_cast<const char*>(a.w)), uintptr_t(a.dy_pitch), uintptr_t(a.h_pitch),
                          a.sg ? uintptr_t(a.sg_pitch) : 0, uintptr_t(a.dx_pitch), uintptr_t(p.N * D::kBytes)});
-  const GradConfig* c = vec ? pick(vectors, p.N / D::kVec) : pick(elements, p.N);
+  const int64_t units = (p.N + D::kVec - 1) / D::kVec;
+  const RingConfig* ring = vec ? pick(rings, units) : nullptr;
+  RingArgs r;
+  int ring_ctas = 0, shared = 0;  // of an SM
+  if (ring) {
+    const int threads = reg_threads(ring->warps), groups = threads / 32 / ring->warps, arrays = a.sg ? 3 : 2;
+    r.row_bytes = uint32_t(p.N * D::kBytes);
+    r.slot_bytes = r.row_bytes * uint32_t(groups * arrays);
+    const auto slots = [&](int ctas) { return (dev.max_smem_per_sm / ctas - 2048) / int(r.slot_bytes); };
+    for (ring_ctas = 512 / threads; ring_ctas > 1 && slots(ring_ctas) < 2;) --ring_ctas;
+    r.slots = slots(ring_ctas) < kMostSlots ? slots(ring_ctas) : kMostSlots;
+    shared = r.slots * int(r.slot_bytes);
+    if (r.slots < 2) ring = nullptr;
+  }
+  const GradConfig* c = ring ? nullptr : vec ? pick(aligned, units) : pick(anywhere, units);
   const unsigned joins = unsigned((p.N + 31) / 32);
   if (p.M == 0) {
     a.parts_n = 0;
+  } else if (ring) {
+    const int threads = reg_threads(ring->warps), groups = threads / 32 / ring->warps;
+    const int64_t turns = (p.M + groups - 1) / groups, most = int64_t(dev.sm_count) * ring_ctas;
+    a.parts_n = int(turns < most ? turns : most);
+    r.g = a;
+    r.status = dev.status;
+    r.wait_ns = local_wait_limit_ns();
+    cudaError_t e = cudaFuncSetAttribute((const void*)ring->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+    if (e != cudaSuccess) return e;
+    ring->fn<<<unsigned(a.parts_n), threads, size_t(shared), p.stream>>>(r);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   } else if (c) {
     const int threads = reg_threads(c->warps), groups = threads / 32 / c->warps;
     const int64_t ctas = (p.M + groups - 1) / groups;
@@ -631,10 +754,9 @@ cudaError_t launch_grad_type(const RmsNormGrad& p, GradArgs a, const DeviceInfo&
     if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
   }
   if (a.dw) {
-    k_rms_weight_join<<<joins, kThreads, 0, p.stream>>>(a);
-    if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (const cudaError_t e = launch_after(k_rms_weight_join, joins, kJoinThreads, p.stream, a); e != cudaSuccess) return e;
   }
-  if (p.M > 0 && !c) k_rms_grad_loop<D><<<row_grid(p.M, dev), kThreads, 0, p.stream>>>(a);
+  if (p.M > 0 && !c && !ring) k_rms_grad_loop<D><<<row_grid(p.M, dev), kThreads, 0, p.stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -660,6 +782,7 @@ cudaError_t launch_rms_norm(const RmsNorm& p, const DeviceInfo& dev) {
   a.eps = p.a.eps;
   a.offset = p.a.offset;
   a.w_f32 = p.a.weight_f32 != 0;
+  a.w_vec = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
   return p.dtype == SOFTMAX_F32 ? launch_norm_type<F32>(p, a, dev) : p.dtype == SOFTMAX_BF16 ? launch_norm_type<BF16>(p, a, dev) : launch_norm_type<F16>(p, a, dev);
 }
 
@@ -689,6 +812,7 @@ cudaError_t launch_rms_norm_grad(const RmsNormGrad& p, const DeviceInfo& dev) {
   a.rows_per_part = 0;
   a.offset = p.a.offset;
   a.w_f32 = p.a.weight_f32 != 0;
+  a.w_vec = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
   a.accumulate = p.a.accumulate != 0;
   return p.dtype == SOFTMAX_F32 ? launch_grad_type<F32>(p, a, dev) : p.dtype == SOFTMAX_BF16 ? launch_grad_type<BF16>(p, a, dev) : launch_grad_type<F16>(p, a, dev);
 }

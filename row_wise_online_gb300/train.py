@@ -14,10 +14,11 @@ from __future__ import annotations
 import array
 import ctypes
 import functools
+import struct
 
 import row_wise_online_gb300 as _rwo
 
-from .decode import _on, _tensor
+from .decode import _raw_stream, _switched
 
 _vp, _i64, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float
 
@@ -38,12 +39,16 @@ class _Grad(ctypes.Structure):
     _fields_ = [("grad", _vp), ("out", _vp), ("n", _i64), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
+# The same structures packed in one go: filling a ctypes.Structure field by field takes 2 us of a call's 9.
+_NORM, _NORM_GRAD = struct.Struct("=13q2f"), struct.Struct("=13qf4x")
+
+
 def _declare(lib) -> None:
     """Argument types of the calls of this module."""
     ci = ctypes.c_int
     lib.cross_entropy_rows_grad.argtypes = [_vp, _i64, _vp, _vp, _f32, _f32, _f32, _vp, _i64, _vp, _vp, _i64, _i64, ci, _vp]
-    lib.rms_norm_rows.argtypes = [ctypes.POINTER(_Norm), _i64, _i64, ci, ci, _vp]
-    lib.rms_norm_rows_backward.argtypes = [ctypes.POINTER(_NormGrad), _i64, _i64, ci, _vp, _i64, _vp]
+    lib.rms_norm_rows.argtypes = [_vp, _i64, _i64, ci, ci, _vp]
+    lib.rms_norm_rows_backward.argtypes = [_vp, _i64, _i64, ci, _vp, _i64, _vp]
     lib.rms_norm_backward_workspace.argtypes = [_i64, _i64, ci]
     lib.embedding_rows.argtypes = [_vp, _i64, _vp, ci, _vp, _i64, _i64, _i64, _i64, _f32, ci, _vp]
     lib.embedding_rows_backward.argtypes = [_vp, _i64, _vp, ci, _vp, _i64, _i64, _i64, _i64, _f32, ci, ci, ci, _vp, _i64, _vp]
@@ -58,25 +63,78 @@ def _declare(lib) -> None:
         getattr(lib, name).restype = _i64
 
 
-def _sizes(t, name):
-    """(M, N) and the device of a matrix of rows along the last dimension."""
+@functools.lru_cache(maxsize=None)
+def _codes():
+    import torch
+
+    return {torch.float32: _rwo.F32, torch.bfloat16: _rwo.BF16, torch.float16: _rwo.F16}
+
+
+def _code(t) -> int:
+    c = _codes().get(t.dtype)
+    return _rwo._dtype_code(t) if c is None else c  # raises
+
+
+@functools.lru_cache(maxsize=None)
+def _current():
+    """The current device, and a device's current stream as a pointer: torch's own short ways where it has them."""
+    import torch
+
+    return getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _stream_of(index, stream):
+    """The stream's pointer where device ``index`` is current and the stream is its current one, else None: the call then
+    makes itself again with both switched to."""
+    if stream is not None:
+        return None
+    device, raw = _current()
+    return raw(index) if device() == index else None
+
+
+def _lead(t, name):
+    """Shape, length N of the last dimension, rows M and device of a matrix of rows along it."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() == 0:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name} must have at least one dimension")
-    N = int(t.shape[-1])
-    return (t.numel() // N if N else 0), N, t.get_device()
+    N = shape[-1]
+    return shape, N, (t.numel() // N if N else 0), t.get_device()
+
+
+def _pitch(t, name, shape):
+    """Row pitch of a matrix."""
+    if t.is_contiguous():
+        return shape[-1]
+    if len(shape) != 2 or (t.stride(1) != 1 and shape[1] > 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
+        raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows (stride(1) == 1, stride(0) >= N)")
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _matrix(t, name, shape, dtype, index):
     """Pointer and row pitch of a matrix of a shape and dtype on CUDA device ``index``."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[-1]
-    if t.dim() != 2 or (t.stride(1) != 1 and shape[1] > 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
-        raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows (stride(1) == 1, stride(0) >= N)")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    return t.data_ptr(), _pitch(t, name, shape)
+
+
+def _vector(t, name, dtype, shape, index):
+    """Pointer of a contiguous tensor of a dtype and shape on CUDA device ``index`` (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
+    return t.data_ptr()
+
+
+def _like(t, dtype=None):
+    """A new contiguous tensor of t's shape."""
+    import torch
+
+    if dtype is None and t.is_contiguous():
+        return torch.empty_like(t)  # 1 us less than spelling it out
+    return torch.empty(t.shape, dtype=dtype or t.dtype, device=t.device)
 
 
 def _weight(w, N, dtype, index):
@@ -84,9 +142,9 @@ def _weight(w, N, dtype, index):
     import torch
 
     if w is None:
-        return None, 0
+        return 0, 0
     f32 = w.dtype is torch.float32
-    return _tensor(w, "weight", torch.float32 if f32 else dtype, (N,), index), int(f32)
+    return _vector(w, "weight", torch.float32 if f32 else dtype, (N,), index), int(f32)
 
 
 def _scratch(workspace, need, device, index, what):
@@ -127,53 +185,69 @@ def cross_entropy_rows_grad(x, labels, grad=None, loss=None, lse_out=None, upstr
     """
     import torch
 
-    M, N, index = _sizes(x, "x")
-    dt, lead = _rwo._dtype_code(x), x.shape[:-1]
-    xp, ldx = _matrix(x, "x", x.shape, x.dtype, index)
-    lp = _tensor(labels, "labels", torch.int64, lead, index)
-    up = _tensor(upstream, "upstream", torch.float32, lead, index)
-    with _on(index, stream) as s:
-        if grad is None:
-            grad = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if loss is None:
-            loss = torch.empty(lead, dtype=torch.float32, device=x.device)
-        gp, ldg = _matrix(grad, "grad", x.shape, x.dtype, index)
-        st = _rwo.capi().cross_entropy_rows_grad(xp, ldx, lp, up, grad_scale, label_smoothing, z_loss, gp, ldg,
-                                                 _tensor(loss, "loss", torch.float32, lead, index),
-                                                 _tensor(lse_out, "lse_out", torch.float32, lead, index), M, N, dt, s)
-    _rwo._check(st, "cross_entropy_rows_grad")
+    shape, N, M, index = _lead(x, "x")
+    s = _stream_of(index, stream)
+    if s is None:
+        with _switched(index, stream):
+            return cross_entropy_rows_grad(x, labels, grad, loss, lse_out, upstream, grad_scale, label_smoothing, z_loss)
+    dt, lead, f32 = _code(x), shape[:-1], torch.float32
+    xp, ldx = x.data_ptr(), _pitch(x, "x", shape)
+    lp, up = _vector(labels, "labels", torch.int64, lead, index), _vector(upstream, "upstream", f32, lead, index)
+    if grad is None:
+        grad = _like(x)
+        gp, ldg = grad.data_ptr(), N
+    else:
+        gp, ldg = _matrix(grad, "grad", shape, x.dtype, index)
+    if loss is None:
+        loss = torch.empty(lead, dtype=f32, device=x.device)
+        op = loss.data_ptr()
+    else:
+        op = _vector(loss, "loss", f32, lead, index)
+    st = _rwo.capi().cross_entropy_rows_grad(xp, ldx, lp, up, grad_scale, label_smoothing, z_loss, gp, ldg, op,
+                                             _vector(lse_out, "lse_out", f32, lead, index), M, N, dt, s)
+    if st:
+        _rwo._check(st, "cross_entropy_rows_grad")
     return loss, grad
 
 
 def _norm(x, weight, residual, sum_out, y, scales, group, rstd_out, eps, offset, out, stream):
     import torch
 
-    M, N, index = _sizes(x, "x")
-    dt, lead = _rwo._dtype_code(x), x.shape[:-1]
-    a = _Norm(group=group, eps=eps, offset=offset)
-    a.x, a.ldx = _matrix(x, "x", x.shape, x.dtype, index)
-    a.weight, a.weight_f32 = _weight(weight, N, x.dtype, index)
-    a.rstd_out = _tensor(rstd_out, "rstd_out", torch.float32, lead, index)
-    if residual is None and sum_out is not None:
+    shape, N, M, index = _lead(x, "x")
+    s = _stream_of(index, stream)
+    if s is None:
+        with _switched(index, stream):
+            return _norm(x, weight, residual, sum_out, y, scales, group, rstd_out, eps, offset, out, None)
+    dt, lead, f32 = _code(x), shape[:-1], torch.float32
+    xp, ldx = x.data_ptr(), _pitch(x, "x", shape)
+    wp, wf = _weight(weight, N, x.dtype, index)
+    rp = ldr = hp = ldh = sp = 0
+    if residual is not None:
+        rp, ldr = _matrix(residual, "residual", shape, x.dtype, index)
+        if sum_out is None:
+            sum_out = _like(x)
+            hp, ldh = sum_out.data_ptr(), N
+        else:
+            hp, ldh = _matrix(sum_out, "sum_out", shape, x.dtype, index)
+    elif sum_out is not None:
         raise ValueError("sum_out without residual")
-    if out and group not in (0, 128):
-        raise ValueError("group must be 0 (a scale for each row) or 128")
-    with _on(index, stream) as s:
-        if residual is not None:
-            a.residual, a.ld_residual = _matrix(residual, "residual", x.shape, x.dtype, index)
-            if sum_out is None:
-                sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            a.sum_out, a.ld_sum = _matrix(sum_out, "sum_out", x.shape, x.dtype, index)
-        if y is None:
-            y = torch.empty(x.shape, dtype=torch.float8_e4m3fn if out else x.dtype, device=x.device)
-        a.y, a.ldy = _matrix(y, "y", x.shape, torch.float8_e4m3fn if out else x.dtype, index)
-        if out:
-            shape = (*lead, -(-N // group) if group else 1)
-            if scales is None:
-                scales = torch.empty(shape, dtype=torch.float32, device=x.device)
-            a.scales = _tensor(scales, "scales", torch.float32, shape, index)
-        st = _rwo.capi().rms_norm_rows(a, M, N, dt, out, s)
-    _rwo._check(st, "rms_norm_rows")
+    held = torch.float8_e4m3fn if out else None
+    if y is None:
+        y = _like(x, held)
+        yp, ldy = y.data_ptr(), N
+    else:
+        yp, ldy = _matrix(y, "y", shape, held or x.dtype, index)
+    if out:
+        if group not in (0, 128):
+            raise ValueError("group must be 0 (a scale for each row) or 128")
+        parts = (*lead, -(-N // group) if group else 1)
+        if scales is None:
+            scales = torch.empty(parts, dtype=f32, device=x.device)
+        sp = _vector(scales, "scales", f32, parts, index)
+    st = _rwo.capi().rms_norm_rows(_NORM.pack(xp, ldx, rp, ldr, hp, ldh, wp, wf, yp, ldy, sp, group,
+                                              _vector(rstd_out, "rstd_out", f32, lead, index), eps, offset), M, N, dt, out, s)
+    if st:
+        _rwo._check(st, "rms_norm_rows")
     return y, scales, sum_out
 
 
@@ -213,30 +287,35 @@ def rms_norm_rows_backward(dy, h, rstd, weight=None, offset: float = 0.0, sum_gr
     """
     import torch
 
-    M, N, index = _sizes(h, "h")
-    dt = _rwo._dtype_code(h)
-    a = _NormGrad(offset=offset, accumulate=int(accumulate))
-    a.h, a.ldh = _matrix(h, "h", h.shape, h.dtype, index)
-    a.dy, a.ld_dy = _matrix(dy, "dy", h.shape, h.dtype, index)
-    if sum_grad is not None:
-        a.sum_grad, a.ld_sum_grad = _matrix(sum_grad, "sum_grad", h.shape, h.dtype, index)
-    a.rstd = _tensor(rstd, "rstd", torch.float32, h.shape[:-1], index)
-    a.weight, a.weight_f32 = _weight(weight, N, h.dtype, index)
-    if dweight is None and accumulate:
-        raise ValueError("accumulate needs a dweight to add to")
-    with _on(index, stream) as s:
-        if dx is None:
-            dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-        a.dx, a.ld_dx = _matrix(dx, "dx", h.shape, h.dtype, index)
-        if dweight is None and weight is not None:
-            dweight = torch.empty(N, dtype=torch.float32, device=h.device)
-        a.dweight = _tensor(dweight, "dweight", torch.float32, (N,), index)
-        wp, wn = None, 0
-        if dweight is not None:
-            workspace = _scratch(workspace, _bytes_of("rms_norm_backward_workspace", index, M, N, dt), h.device, index, "rms_norm_rows_backward")
-            wp, wn = workspace.data_ptr(), workspace.numel()
-        st = _rwo.capi().rms_norm_rows_backward(a, M, N, dt, wp, wn, s)
-    _rwo._check(st, "rms_norm_rows_backward")
+    shape, N, M, index = _lead(h, "h")
+    s = _stream_of(index, stream)
+    if s is None:
+        with _switched(index, stream):
+            return rms_norm_rows_backward(dy, h, rstd, weight, offset, sum_grad, dx, dweight, accumulate, workspace)
+    dt, f32 = _code(h), torch.float32
+    hp, ldh = h.data_ptr(), _pitch(h, "h", shape)
+    dp, ldd = _matrix(dy, "dy", shape, h.dtype, index)
+    gp, ldg = (0, 0) if sum_grad is None else _matrix(sum_grad, "sum_grad", shape, h.dtype, index)
+    wp, wf = _weight(weight, N, h.dtype, index)
+    if dx is None:
+        dx = _like(h)
+        xp, ldx = dx.data_ptr(), N
+    else:
+        xp, ldx = _matrix(dx, "dx", shape, h.dtype, index)
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dweight to add to")
+        if weight is not None:
+            dweight = torch.empty(N, dtype=f32, device=h.device)
+    sp, sn = 0, 0
+    if dweight is not None:
+        workspace = _scratch(workspace, _bytes_of("rms_norm_backward_workspace", index, M, N, dt), h.device, index, "rms_norm_rows_backward")
+        sp, sn = workspace.data_ptr(), workspace.numel()
+    st = _rwo.capi().rms_norm_rows_backward(
+        _NORM_GRAD.pack(dp, ldd, hp, ldh, gp, ldg, _vector(rstd, "rstd", f32, shape[:-1], index), wp, wf, xp, ldx,
+                        _vector(dweight, "dweight", f32, (N,), index), 1 if accumulate else 0, offset), M, N, dt, sp, sn, s)
+    if st:
+        _rwo._check(st, "rms_norm_rows_backward")
     return dx, dweight
 
 
@@ -244,28 +323,36 @@ def _tokens(tokens, lead, index):
     """Pointer and element size of int32 or int64 tokens of a shape."""
     import torch
 
-    if tokens.dtype is not torch.int64 and tokens.dtype is not torch.int32:
-        raise ValueError("tokens must be int32 or int64")
-    return _tensor(tokens, "tokens", tokens.dtype, lead, index), 8 if tokens.dtype is torch.int64 else 4
+    if tokens.dtype is torch.int64:
+        return _vector(tokens, "tokens", torch.int64, lead, index), 8
+    if tokens.dtype is torch.int32:
+        return _vector(tokens, "tokens", torch.int32, lead, index), 4
+    raise ValueError("tokens must be int32 or int64")
 
 
 def embedding_rows(table, tokens, y=None, scale: float = 1.0, stream=None):
     """y[...] = scale * table[tokens[...]] for a table [V, D] and int32 or int64 tokens; a negative token gives zeros."""
     import torch
 
-    if not table.is_cuda or table.dim() != 2:
+    shape, D, V, index = _lead(table, "table")
+    if len(shape) != 2:
         raise ValueError("table must be a 2-D CUDA tensor [V, D]")
-    V, D = table.shape
-    dt, index = _rwo._dtype_code(table), table.get_device()
-    tp, ldt = _matrix(table, "table", table.shape, table.dtype, index)
+    s = _stream_of(index, stream)
+    if s is None:
+        with _switched(index, stream):
+            return embedding_rows(table, tokens, y, scale)
+    dt = _code(table)
+    tp, ldt = table.data_ptr(), _pitch(table, "table", shape)
     kp, kb = _tokens(tokens, tokens.shape, index)
-    shape = (*tokens.shape, D)
-    with _on(index, stream) as s:
-        if y is None:
-            y = torch.empty(shape, dtype=table.dtype, device=table.device)
-        yp, ldy = _matrix(y, "y", shape, table.dtype, index)
-        st = _rwo.capi().embedding_rows(tp, ldt, kp, kb, yp, ldy, tokens.numel(), V, D, scale, dt, s)
-    _rwo._check(st, "embedding_rows")
+    out = (*tokens.shape, D)
+    if y is None:
+        y = torch.empty(out, dtype=table.dtype, device=table.device)
+        yp, ldy = y.data_ptr(), D
+    else:
+        yp, ldy = _matrix(y, "y", out, table.dtype, index)
+    st = _rwo.capi().embedding_rows(tp, ldt, kp, kb, yp, ldy, tokens.numel(), shape[0], D, scale, dt, s)
+    if st:
+        _rwo._check(st, "embedding_rows")
     return y
 
 
@@ -282,23 +369,30 @@ def embedding_rows_backward(dy, tokens, num_rows: int | None = None, grad=None, 
     """
     import torch
 
-    T, D, index = _sizes(dy, "dy")
-    dt, lead = _rwo._dtype_code(dy), dy.shape[:-1]
-    dp, ldd = _matrix(dy, "dy", dy.shape, dy.dtype, index)
-    kp, kb = _tokens(tokens, lead, index)
-    if grad is None and (num_rows is None or accumulate):
-        raise ValueError("accumulate needs a grad to add to" if accumulate else "num_rows is needed to allocate grad")
-    V = int(grad.shape[0]) if grad is not None else int(num_rows)
-    if num_rows is not None and num_rows != V:
-        raise ValueError(f"grad has {V} rows, num_rows is {num_rows}")
-    with _on(index, stream) as s:
-        if grad is None:
-            grad = torch.empty((V, D), dtype=dtype or torch.float32, device=dy.device)
+    shape, D, T, index = _lead(dy, "dy")
+    s = _stream_of(index, stream)
+    if s is None:
+        with _switched(index, stream):
+            return embedding_rows_backward(dy, tokens, num_rows, grad, scale, accumulate, dtype, workspace)
+    dt = _code(dy)
+    dp, ldd = dy.data_ptr(), _pitch(dy, "dy", shape)
+    kp, kb = _tokens(tokens, shape[:-1], index)
+    if grad is None:
+        if accumulate or num_rows is None:
+            raise ValueError("accumulate needs a grad to add to" if accumulate else "num_rows is needed to allocate grad")
+        V = int(num_rows)
+        grad = torch.empty((V, D), dtype=dtype or torch.float32, device=dy.device)
+        gp, ldg = grad.data_ptr(), D
+    else:
+        V = grad.shape[0] if grad.dim() else 0
+        if num_rows is not None and num_rows != V:
+            raise ValueError(f"grad has {V} rows, num_rows is {num_rows}")
         gp, ldg = _matrix(grad, "grad", (V, D), dtype or grad.dtype, index)
-        workspace = _scratch(workspace, _bytes_of("embedding_backward_workspace", index, T, V, D), dy.device, index, "embedding_rows_backward")
-        st = _rwo.capi().embedding_rows_backward(dp, ldd, kp, kb, gp, ldg, T, V, D, scale, int(accumulate), dt, _rwo._dtype_code(grad),
-                                                 workspace.data_ptr(), workspace.numel(), s)
-    _rwo._check(st, "embedding_rows_backward")
+    workspace = _scratch(workspace, _bytes_of("embedding_backward_workspace", index, T, V, D), dy.device, index, "embedding_rows_backward")
+    st = _rwo.capi().embedding_rows_backward(dp, ldd, kp, kb, gp, ldg, T, V, D, scale, 1 if accumulate else 0, dt, _code(grad),
+                                             workspace.data_ptr(), workspace.numel(), s)
+    if st:
+        _rwo._check(st, "embedding_rows_backward")
     return grad
 
 
@@ -307,54 +401,71 @@ def grad_norm_workspace(count: int, device=None):
     return _workspace("grad_norm_workspace", device, count)
 
 
-@functools.lru_cache(maxsize=None)
-def _codes():
-    import torch
-
-    return {torch.float32: _rwo.F32, torch.bfloat16: _rwo.BF16, torch.float16: _rwo.F16}
+def _type_words(ts, error):
+    """Type codes of tensors, as one number where all are of one type."""
+    codes = _codes()
+    kinds = {t.dtype for t in ts}
+    if not kinds <= codes.keys():
+        raise ValueError(error)
+    return codes[kinds.pop()] if len(kinds) == 1 else [codes[t.dtype] for t in ts]
 
 
 def _grads(tensors, out):
     """The list as the C call takes it (four 64-bit words a tensor: grad, out, n, types), and its device."""
     import torch
 
-    if not tensors:
+    n, kind = len(tensors), torch.Tensor
+    if not n:
         return array.array("q"), torch.cuda.current_device()
-    index, codes, words = tensors[0].get_device(), _codes(), []
-    for t in tensors:
-        code = codes.get(t.dtype)
-        if code is None or t.get_device() != index or index < 0 or not t.is_contiguous():
-            raise ValueError("gradients must be contiguous float32, bfloat16 or float16 tensors on one CUDA device")
-        p = t.data_ptr()
-        words += (p, p, t.numel(), code | code << 32)
+    index = tensors[0].get_device()
+    error = "gradients must be contiguous float32, bfloat16 or float16 tensors on one CUDA device"
+    # map() over the tensors' own methods: 0.25 us a tensor, where a loop with the same checks takes 0.45
+    if index < 0 or set(map(kind.get_device, tensors)) != {index} or not all(map(kind.is_contiguous, tensors)):
+        raise ValueError(error)
+    words = array.array("q", bytes(32 * n))
+    words[0::4] = words[1::4] = array.array("q", map(kind.data_ptr, tensors))
+    words[2::4] = array.array("q", map(kind.numel, tensors))
+    types = outs = _type_words(tensors, error)
     if out is not None:
-        if len(out) != len(tensors):
-            raise ValueError(f"out must have as many tensors as there are gradients ({len(tensors)})")
-        for i, (t, o) in enumerate(zip(tensors, out)):
-            if o.shape != t.shape or (o.dtype is not t.dtype and o.dtype is not torch.float32) or o.get_device() != index or not o.is_contiguous():
-                raise ValueError("out must be contiguous tensors of the gradients' shapes, in their dtype or float32, on their device")
-            words[4 * i + 1] = o.data_ptr()
-            words[4 * i + 3] = codes[t.dtype] | codes[o.dtype] << 32
-    return array.array("q", words), index
+        error = "out must be contiguous tensors of the gradients' shapes, in their dtype or float32, on their device"
+        if len(out) != n:
+            raise ValueError(f"out must have as many tensors as there are gradients ({n})")
+        if set(map(kind.get_device, out)) != {index} or not all(map(kind.is_contiguous, out)) or any(o.shape != t.shape for t, o in zip(tensors, out)):
+            raise ValueError(error)
+        words[1::4] = array.array("q", map(kind.data_ptr, out))
+        outs = _type_words(out, error)
+        if any(o.dtype is not t.dtype and o.dtype is not torch.float32 for t, o in zip(tensors, out)):
+            raise ValueError(error)
+    if isinstance(types, int) and isinstance(outs, int):
+        words[3::4] = array.array("q", [types | outs << 32]) * n
+    else:
+        types, outs = ([v] * n if isinstance(v, int) else v for v in (types, outs))
+        words[3::4] = array.array("q", [a | b << 32 for a, b in zip(types, outs)])
+    return words, index
 
 
 def _grad_norm(tensors, out, max_norm, scale, norm_out, workspace, stream):
     import torch
 
-    tensors = list(tensors)
+    tensors = tensors if isinstance(tensors, (list, tuple)) else list(tensors)
     words, index = _grads(tensors, out)
+    s = _stream_of(index, stream)
+    if s is None:
+        with _switched(index, stream):
+            return _grad_norm(tensors, out, max_norm, scale, norm_out, workspace, None)
     n = len(tensors)
-    with _on(index, stream) as s:
-        if norm_out is None:
-            norm_out = torch.empty((), dtype=torch.float32, device=f"cuda:{index}")
-        np = _tensor(norm_out, "norm_out", torch.float32, norm_out.shape if norm_out.numel() == 1 else (), index)
-        workspace = _scratch(workspace, _bytes_of("grad_norm_workspace", index, n), norm_out.device, index, "grad_norm")
-        wp, wn, lp = workspace.data_ptr(), workspace.numel(), words.buffer_info()[0] if n else None
-        if max_norm is None:
-            st = _rwo.capi().grad_norm(lp, n, scale, np, wp, wn, s)
-        else:
-            st = _rwo.capi().clip_grad_norm(lp, n, scale, max_norm, np, wp, wn, s)
-    _rwo._check(st, "grad_norm" if max_norm is None else "clip_grad_norm")
+    device = tensors[0].device if n else torch.device("cuda", index)
+    if norm_out is None:
+        norm_out = torch.empty((), dtype=torch.float32, device=device)
+    np = _vector(norm_out, "norm_out", torch.float32, norm_out.shape if norm_out.numel() == 1 else (), index)
+    workspace = _scratch(workspace, _bytes_of("grad_norm_workspace", index, n), device, index, "grad_norm")
+    wp, wn, lp = workspace.data_ptr(), workspace.numel(), words.buffer_info()[0] if n else None
+    if max_norm is None:
+        st = _rwo.capi().grad_norm(lp, n, scale, np, wp, wn, s)
+    else:
+        st = _rwo.capi().clip_grad_norm(lp, n, scale, max_norm, np, wp, wn, s)
+    if st:
+        _rwo._check(st, "grad_norm" if max_norm is None else "clip_grad_norm")
     return norm_out
 
 
