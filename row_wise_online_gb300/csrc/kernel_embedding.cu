@@ -72,12 +72,13 @@ __global__ void __launch_bounds__(kLookupThreads, 4) k_embedding(LookupArgs a) {
     uint4 q[kLookupPer];
     const bool real = token >= 0 && token < a.V;
     if (real) {
-      const unsigned char* row = a.table + token * a.table_pitch;
+      const RowAt r = row_at<D>(a.table + token * a.table_pitch, n, table);
+      if constexpr (SHIFT) {
+        load_vectors<D>(r, u0, q);
+      } else {
 #pragma unroll
-      for (int k = 0; k < kLookupPer; ++k) {
-        const int u = u0 + k * 32;
-        if constexpr (SHIFT) q[k] = load_vector<D>(row, u, n, table);
-        else if (u < a.units) q[k] = ld_stream16(row + int64_t(u) * 16);
+        for (int k = 0; k < kLookupPer; ++k)
+          if (u0 + k * 32 < a.units) q[k] = ld_stream16(r.row + int64_t(u0 + k * 32) * 16);
       }
       if (a.scale != 1.f) {
         const float2 s = make_float2(a.scale, a.scale);
@@ -99,11 +100,12 @@ __global__ void __launch_bounds__(kLookupThreads, 4) k_embedding(LookupArgs a) {
 #pragma unroll
       for (int k = 0; k < kLookupPer; ++k) q[k] = D::pack2(v);
     }
+    if constexpr (SHIFT) {
+      store_vectors<D>(to, u0, n, q);
+    } else {
 #pragma unroll
-    for (int k = 0; k < kLookupPer; ++k) {
-      const int u = u0 + k * 32;
-      if constexpr (SHIFT) store_vector<D>(to, u, n, q[k]);
-      else if (u < a.units) st_stream16(to + int64_t(u) * 16, q[k]);
+      for (int k = 0; k < kLookupPer; ++k)
+        if (u0 + k * 32 < a.units) st_stream16(to + int64_t(u0 + k * 32) * 16, q[k]);
     }
     if (item >= items) return;
   }
@@ -338,18 +340,19 @@ __device__ __forceinline__ void write_vector(const GradArgs& a, unsigned char* r
   const int n = int(a.D);
   float y[G::kVec];
   if (a.accumulate) {
-    uint4 old = make_uint4(0, 0, 0, 0);
-    if constexpr (SHIFT) old = load_vector<G>(row, u, n, m);
-    else if (u * G::kVec < n) old = ld16(row + int64_t(u) * 16);
-    G::unpack(old, y);
+    uint4 old[1] = {};
+    if constexpr (SHIFT) load_vectors<G>(row_at<G>(row, n, m), u, old);
+    else if (u * G::kVec < n) old[0] = ld16(row + int64_t(u) * 16);
+    G::unpack(old[0], y);
 #pragma unroll
     for (int e = 0; e < G::kVec; ++e) y[e] = __fmaf_rn(sum[e], a.scale, y[e]);
   } else {
 #pragma unroll
     for (int e = 0; e < G::kVec; ++e) y[e] = sum[e] * a.scale;
   }
-  if constexpr (SHIFT) store_vector<G>(row, u, n, G::pack(y));
-  else if (u * G::kVec < n) st_stream16(row + int64_t(u) * 16, G::pack(y));
+  const uint4 q[1] = {G::pack(y)};
+  if constexpr (SHIFT) store_vectors<G>(row, u, n, q);
+  else if (u * G::kVec < n) st_stream16(row + int64_t(u) * 16, q[0]);
 }
 
 // E sums a lane, of elements u * E .. of row v; all lanes of a warp, with consecutive u.
@@ -410,20 +413,20 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding_rows(GradArgs a) {
   float sum[E] = {};
   bool head = keys[0] == keys[1];  // the run came from the chunk before
   for (int i = 0; i < a.chunk && keys[i + 1] < a.V; i += kAhead) {
-    uint4 q[kAhead];
+    uint4 q[kAhead][1];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (keys[i + j + 1] >= a.V) continue;
       const unsigned char* row = a.dy + int64_t(pos[i + j]) * a.dy_pitch;
-      if constexpr (SHIFT) q[j] = load_vector<D>(row, u, n, dm);
-      else q[j] = u < a.units ? ld_stream16(row + int64_t(u) * 16) : make_uint4(0, 0, 0, 0);
+      if constexpr (SHIFT) load_vectors<D>(row_at<D>(row, n, dm), u, q[j]);
+      else q[j][0] = u < a.units ? ld_stream16(row + int64_t(u) * 16) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const uint32_t key = keys[i + j + 1], next = keys[i + j + 2];
       if (key >= a.V) break;
       float f[E];
-      D::unpack(q[j], f);
+      D::unpack(q[j][0], f);
 #pragma unroll
       for (int e = 0; e < E; ++e) sum[e] += f[e];
       const bool last = i + j + 1 == a.chunk;

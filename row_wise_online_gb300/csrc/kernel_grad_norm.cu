@@ -14,7 +14,7 @@ namespace rwo {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kChunkVecs = 4;  // 16-byte vectors of a thread in a chunk
+constexpr int kChunkVecs = 8;  // 16-byte vectors of a thread in a chunk
 constexpr int kSmall = 64, kLarge = 512;
 
 template <int K>
@@ -32,6 +32,7 @@ struct Params {
   float* norm;
   int parts_n, part0;
   float scale, max_norm;
+  bool in_place;  // every tensor of the table
 };
 
 __host__ __device__ constexpr int chunk_elems(int type) { return kThreads * kChunkVecs * (type == 0 ? 4 : 8); }
@@ -54,28 +55,42 @@ __host__ __device__ inline int64_t lead_of(const void* g, int64_t n, int bytes) 
   return lead < n ? lead : n;
 }
 
-// Elements of a chunk: whole 16-byte vectors from the tensor's first aligned element on; the first chunk also has the
-// elements before it, the last one the rest.
-struct Span {
-  int64_t begin;   // first element of the first vector
-  int vecs;        // whole vectors
-  int64_t loose0;  // single elements [loose0, loose1) and [begin + vecs * E, tail1)
-  int64_t loose1;
-  int64_t tail1;
+// A chunk: whole 16-byte vectors from the tensor's first aligned element on; the first chunk also has the elements before
+// it, the last one the rest.
+struct Chunk {
+  const unsigned char* g;
+  unsigned char* out;
+  int64_t begin;  // first element of the first vector
+  int64_t tail;   // the rest ends here (0: none)
+  int vecs;       // whole vectors
+  int lead;       // single elements from the tensor's first on
+  int type, out_type;
 };
-template <class D>
-__device__ __forceinline__ Span span_of(const unsigned char* g, int64_t n, uint32_t index, bool last) {
-  constexpr int E = D::kVec;
-  const int64_t lead = lead_of(g, n, D::kBytes);
-  Span s;
-  s.begin = lead + int64_t(index) * (kThreads * kChunkVecs * E);
-  int64_t v = (n - s.begin) / E;
-  if (v < 0) v = 0;
+template <int K>
+__device__ __forceinline__ Chunk chunk_of(const Table<K>& t, uint32_t c) {
+  const int i = tensor_of(t, c);
+  const uint32_t index = c - t.first[i];
+  Chunk s;
+  s.g = t.g[i];
+  s.out = t.out[i];
+  s.type = t.type[i];
+  s.out_type = t.out_type[i];
+  const int bytes = s.type == SOFTMAX_F32 ? 4 : 2, per = 16 / bytes;
+  const int64_t n = t.n[i], lead = lead_of(s.g, n, bytes);
+  s.begin = lead + int64_t(index) * (kThreads * kChunkVecs * per);
+  const int64_t v = n > s.begin ? (n - s.begin) / per : 0;
   s.vecs = int(v < kThreads * kChunkVecs ? v : kThreads * kChunkVecs);
-  s.loose0 = 0;
-  s.loose1 = index == 0 ? lead : 0;
-  s.tail1 = last ? n : 0;
+  s.lead = index == 0 ? int(lead) : 0;
+  s.tail = c + 1 == t.first[i + 1] ? n : 0;
   return s;
+}
+
+// This thread's vectors of a chunk, 0 where it has none.
+__device__ __forceinline__ void load(const Chunk& s, uint4 (&q)[kChunkVecs]) {
+  const unsigned char* p = s.g + s.begin * (s.type == SOFTMAX_F32 ? 4 : 2) + threadIdx.x * 16;
+#pragma unroll
+  for (int k = 0; k < kChunkVecs; ++k)
+    q[k] = int(threadIdx.x) + k * kThreads < s.vecs ? ld_stream16(p + k * (kThreads * 16)) : make_uint4(0, 0, 0, 0);
 }
 
 __device__ __forceinline__ double block_sum(double v, double* slots) {
@@ -90,21 +105,15 @@ __device__ __forceinline__ double block_sum(double v, double* slots) {
   return __shfl_sync(~0u, v, 0);
 }
 
-// This thread's part of a chunk's sum of squares.  A thread adds up at most some 40 squares in fp32.  Where their sum may
+// This thread's part of a chunk's sum of squares.  A thread adds up at most 66 squares in fp32.  Where their sum may
 // have run over, or may have lost squares below fp32's range to it, they are taken again in fp64.
 template <class D>
-__device__ __forceinline__ double squares(const unsigned char* g, const Span& s) {
+__device__ __forceinline__ double squares(const Chunk& s, const uint4 (&q)[kChunkVecs]) {
   constexpr int E = D::kVec;
-  uint4 q[kChunkVecs];
-#pragma unroll
-  for (int k = 0; k < kChunkVecs; ++k) {
-    const int i = threadIdx.x + k * kThreads;
-    q[k] = i < s.vecs ? ld_stream16(g + (s.begin + int64_t(i) * E) * D::kBytes) : make_uint4(0, 0, 0, 0);
-  }
   float loose[2] = {0.f, 0.f};
-  if (s.loose0 + threadIdx.x < s.loose1) loose[0] = D::load1(g, s.loose0 + threadIdx.x);
+  if (int(threadIdx.x) < s.lead) loose[0] = D::load1(s.g, threadIdx.x);
   const int64_t rest = s.begin + int64_t(s.vecs) * E + threadIdx.x;
-  if (rest < s.tail1) loose[1] = D::load1(g, rest);
+  if (rest < s.tail) loose[1] = D::load1(s.g, rest);
   float2 a = make_float2(loose[0] * loose[0], loose[1] * loose[1]);
   uint32_t any = __float_as_uint(loose[0]) | __float_as_uint(loose[1]);
 #pragma unroll
@@ -132,19 +141,44 @@ __device__ __forceinline__ double squares(const unsigned char* g, const Span& s)
   }
 }
 
-template <int K>
-__global__ void __launch_bounds__(kThreads) k_squares(const __grid_constant__ Table<K> t, Params p) {
-  __shared__ double slots[kWarps];
-  double sum = 0.0;
+// Chunks first, first + step, ... of a table: the next one's vectors are under way while one is worked on.
+template <int K, class Work>
+__device__ __forceinline__ void each_chunk(const Table<K>& t, bool backwards, Work&& work) {
   const uint32_t chunks = t.first[t.count];
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    const bool last = c + 1 == t.first[i + 1];
-    const uint32_t index = c - t.first[i];
-    if (t.type[i] == SOFTMAX_F32) sum += squares<F32>(t.g[i], span_of<F32>(t.g[i], t.n[i], index, last));
-    else if (t.type[i] == SOFTMAX_BF16) sum += squares<BF16>(t.g[i], span_of<BF16>(t.g[i], t.n[i], index, last));
-    else sum += squares<F16>(t.g[i], span_of<F16>(t.g[i], t.n[i], index, last));
+  const auto nth = [&](uint32_t i) { return chunk_of(t, backwards ? chunks - 1 - i : i); };
+  uint32_t i = blockIdx.x;
+  if (i >= chunks) return;
+  Chunk s = nth(i);
+  uint4 q[kChunkVecs];
+  load(s, q);
+  while (true) {
+    i += gridDim.x;
+    Chunk next;
+    uint4 p[kChunkVecs];
+    if (i < chunks) {
+      next = nth(i);
+      load(next, p);
+    }
+    work(s, q);
+    if (i >= chunks) return;
+    s = next;
+#pragma unroll
+    for (int k = 0; k < kChunkVecs; ++k) q[k] = p[k];
   }
+}
+
+// CTAs of an SM.  Two with eight vectors a thread under way and eight worked on: the norm of 2^30 bf16 elements takes 345 us; four with four
+// and four 402, six 671.
+constexpr int kCtas = 2;
+
+template <int K>
+__global__ void __launch_bounds__(kThreads, kCtas) k_squares(const __grid_constant__ Table<K> t, Params p) {
+  __shared__ double slots[kWarps];
+  griddep_launch();
+  double sum = 0.0;
+  each_chunk(t, false, [&](const Chunk& s, const uint4(&q)[kChunkVecs]) {
+    sum += s.type == SOFTMAX_F32 ? squares<F32>(s, q) : s.type == SOFTMAX_BF16 ? squares<BF16>(s, q) : squares<F16>(s, q);
+  });
   sum = block_sum(sum, slots);
   if (threadIdx.x == 0) p.parts[p.part0 + blockIdx.x] = sum;
 }
@@ -158,75 +192,80 @@ __device__ __forceinline__ double norm_of(const Params& p, double* slots) {
 
 __global__ void __launch_bounds__(kThreads) k_norm(Params p) {
   __shared__ double slots[kWarps];
+  griddep_wait();
   const double norm = norm_of(p, slots);
   if (threadIdx.x == 0) *p.norm = float(norm);
 }
 
+// Eight fp32 values a lane, 32 bytes at p: two lanes write 32 bytes of one together, then of the other, so that every store fills
+// whole sectors (2^30 elements, bf16 into fp32: 1082 us against 1322).  All lanes of a warp.
+__device__ __forceinline__ void pair_store(unsigned char* p, const float2 (&f)[4]) {
+  const bool odd = threadIdx.x & 1;
+  float2 a = odd ? f[0] : f[2], b = odd ? f[1] : f[3];  // what the other lane stores
+  a = make_float2(__shfl_xor_sync(~0u, a.x, 1), __shfl_xor_sync(~0u, a.y, 1));
+  b = make_float2(__shfl_xor_sync(~0u, b.x, 1), __shfl_xor_sync(~0u, b.y, 1));
+  // the even lane's 32 bytes, its own first half and the odd lane's copy of the second; then the odd lane's
+  const float2 lo[2] = {odd ? a : f[0], odd ? b : f[1]}, hi[2] = {odd ? f[2] : a, odd ? f[3] : b};
+  unsigned char* even = p - (odd ? 32 : 0) + (odd ? 16 : 0);
+  st_stream16(even, F32::pack2(lo));
+  st_stream16(even + 32, F32::pack2(hi));
+}
+
 // O: the output's type.
 template <class D, class O>
-__device__ __forceinline__ void scaled(const unsigned char* g, unsigned char* out, const Span& s, float k) {
+__device__ __forceinline__ void scaled(const Chunk& s, const uint4 (&q)[kChunkVecs], float k) {
   constexpr int E = D::kVec;
-  if (s.loose0 + threadIdx.x < s.loose1) O::store1(out, s.loose0 + threadIdx.x, k * D::load1(g, s.loose0 + threadIdx.x));
+  if (int(threadIdx.x) < s.lead) O::store1(s.out, threadIdx.x, k * D::load1(s.g, threadIdx.x));
   const int64_t rest = s.begin + int64_t(s.vecs) * E + threadIdx.x;
-  if (rest < s.tail1) O::store1(out, rest, k * D::load1(g, rest));
-  const bool wide = (reinterpret_cast<uintptr_t>(out + s.begin * O::kBytes) & 15) == 0;
-  uint4 q[kChunkVecs];
+  if (rest < s.tail) O::store1(s.out, rest, k * D::load1(s.g, rest));
+  unsigned char* out = s.out + s.begin * O::kBytes + threadIdx.x * (E * O::kBytes);
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+  const float2 k2 = make_float2(k, k);
+  const bool paired = s.vecs == kThreads * kChunkVecs;
 #pragma unroll
   for (int j = 0; j < kChunkVecs; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    if (i < s.vecs) q[j] = ld_stream16(g + (s.begin + int64_t(i) * E) * D::kBytes);
-  }
+    if (int(threadIdx.x) + j * kThreads >= s.vecs) continue;
+    float2 f[E / 2];
+    D::unpack2(q[j], f);
 #pragma unroll
-  for (int j = 0; j < kChunkVecs; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    if (i >= s.vecs) continue;
-    float f[E];
-    D::unpack(q[j], f);
-    unsigned char* at = out + (s.begin + int64_t(i) * E) * O::kBytes;
+    for (int e = 0; e < E / 2; ++e) f[e] = __fmul2_rn(f[e], k2);
+    unsigned char* at = out + j * (kThreads * E * O::kBytes);
     if (wide) {
-#pragma unroll
-      for (int b = 0; b < E / O::kVec; ++b) {
-        float y[O::kVec];
-#pragma unroll
-        for (int e = 0; e < O::kVec; ++e) y[e] = k * f[b * O::kVec + e];
-        st_stream16(at + b * 16, O::pack(y));
-      }
+      if constexpr (E == O::kVec) st_stream16(at, O::pack2(f));
+      else if (paired) pair_store(at, f);
+      else st_stream16(at, O::pack2({f[0], f[1]})), st_stream16(at + 16, O::pack2({f[2], f[3]}));
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) O::store1(at, e, k * f[e]);
+      for (int e = 0; e < E; ++e) O::store1(at, e, e & 1 ? f[e / 2].y : f[e / 2].x);
     }
   }
 }
 
 template <int K>
-__global__ void __launch_bounds__(kThreads) k_scale(const __grid_constant__ Table<K> t, Params p) {
+__global__ void __launch_bounds__(kThreads, kCtas) k_scale(const __grid_constant__ Table<K> t, Params p) {
   __shared__ double slots[kWarps];
+  griddep_wait();
   const double norm = norm_of(p, slots);
   if (p.part0 == 0 && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = float(norm);
   const bool limited = norm > double(p.max_norm) && float(norm) <= 3.4028234663852886e38f;
   const float k = limited ? float(double(p.scale) * (double(p.max_norm) / norm)) : p.scale;
-  const uint32_t chunks = t.first[t.count];
-  for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
-    const uint32_t c = chunks - 1 - b;  // last chunks first: they are the likeliest to be in L2 still
-    const int i = tensor_of(t, c);
-    if (k == 1.f && t.out[i] == t.g[i]) continue;
-    const bool last = c + 1 == t.first[i + 1];
-    const uint32_t index = c - t.first[i];
-    if (t.type[i] == SOFTMAX_F32) {
-      scaled<F32, F32>(t.g[i], t.out[i], span_of<F32>(t.g[i], t.n[i], index, last), k);
-    } else if (t.type[i] == SOFTMAX_BF16) {
-      const Span s = span_of<BF16>(t.g[i], t.n[i], index, last);
-      if (t.out_type[i] == SOFTMAX_F32) scaled<BF16, F32>(t.g[i], t.out[i], s, k);
-      else scaled<BF16, BF16>(t.g[i], t.out[i], s, k);
+  if (k == 1.f && p.in_place) return;
+  // last chunks first: they are the likeliest to be in L2 still
+  each_chunk(t, true, [&](const Chunk& s, const uint4(&q)[kChunkVecs]) {
+    if (k == 1.f && s.out == s.g) return;
+    if (s.type == SOFTMAX_F32) {
+      scaled<F32, F32>(s, q, k);
+    } else if (s.type == SOFTMAX_BF16) {
+      if (s.out_type == SOFTMAX_F32) scaled<BF16, F32>(s, q, k);
+      else scaled<BF16, BF16>(s, q, k);
     } else {
-      const Span s = span_of<F16>(t.g[i], t.n[i], index, last);
-      if (t.out_type[i] == SOFTMAX_F32) scaled<F16, F32>(t.g[i], t.out[i], s, k);
-      else scaled<F16, F16>(t.g[i], t.out[i], s, k);
+      if (s.out_type == SOFTMAX_F32) scaled<F16, F32>(s, q, k);
+      else scaled<F16, F16>(s, q, k);
     }
-  }
+  });
 }
 
-int64_t grid_most(const DeviceInfo& dev) { return int64_t(dev.sm_count) * (dev.max_threads_per_sm / kThreads); }
+int64_t grid_most(const DeviceInfo& dev) { return int64_t(dev.sm_count) * kCtas; }
 
 // Tensors from `from` on that fit a table; returns the first one after them.
 template <int K>
@@ -258,6 +297,7 @@ cudaError_t run(const GradNorm& p, const DeviceInfo& dev) {
   a.part0 = 0;
   a.scale = p.scale;
   a.max_norm = p.max_norm;
+  a.in_place = false;
   Table<K> t;
   cudaError_t e;
   for (int64_t from = 0; from < p.count;) {
@@ -271,16 +311,16 @@ cudaError_t run(const GradNorm& p, const DeviceInfo& dev) {
     a.parts_n += int(grid);
   }
   if (p.max_norm == 0.f || a.parts_n == 0) {
-    k_norm<<<1, kThreads, 0, p.stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(k_norm, dim3(1), kThreads, p.stream, a);
   }
   a.part0 = 0;
   for (int64_t from = 0; from < p.count;) {
     from = fill(t, p, from);
     if (t.count == 0) continue;
     const int64_t chunks = t.first[t.count], most = grid_most(dev);
-    k_scale<K><<<unsigned(chunks < most ? chunks : most), kThreads, 0, p.stream>>>(t, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    a.in_place = true;
+    for (int i = 0; i < t.count; ++i) a.in_place = a.in_place && t.out[i] == t.g[i];
+    if ((e = launch_after(k_scale<K>, dim3(unsigned(chunks < most ? chunks : most)), kThreads, p.stream, t, a)) != cudaSuccess) return e;
     a.part0 = 1;  // the norm is written
   }
   return cudaSuccess;

@@ -54,6 +54,8 @@ __device__ __forceinline__ float weight1(const A& a, int64_t i) {
   return (a.w_f32 ? __ldg(static_cast<const float*>(a.w) + i) : D::load1(a.w, i)) + a.offset;
 }
 
+__device__ __forceinline__ float scale_of(float top) { return fmaxf(top * (1.f / kE4m3Max), kScaleMin); }
+
 // Two values -> two e4m3 codes (lo in the low byte), to the nearest, limited to +-448.
 __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_loop(NormArgs a) {
       float top = 0.f;
       for (int64_t i = threadIdx.x; i < a.N; i += kThreads) top = fmaxf(top, fabsf(load1c<D>(hr, i) * rstd * weight1<D>(a, i)));
       top = block_max<kThreads / 32>(top, slots);
-      const float scale = fmaxf(top / kE4m3Max, kScaleMin), inv = 1.f / scale;
+      const float scale = scale_of(top), inv = __fdividef(1.f, scale);
       if (threadIdx.x == 0) a.scales[row] = scale;
       for (int64_t i = threadIdx.x; i < a.N; i += kThreads)
         yr[i] = (unsigned char)(pack_e4m3x2(load1c<D>(hr, i) * rstd * weight1<D>(a, i) * inv, 0.f) & 0xff);
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_loop(NormArgs a) {
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        const float scale = fmaxf(top / kE4m3Max, kScaleMin), inv = 1.f / scale;
+        const float scale = scale_of(top), inv = __fdividef(1.f, scale);
         if (lane == 0) a.scales[row * a.groups + g] = scale;
 #pragma unroll
         for (int k = 0; k < kGroup / 32; ++k) {
@@ -188,19 +190,37 @@ __global__ void __launch_bounds__(kThreads) k_rms_weight_grad(GradArgs a) {
 
 // ---- rows in registers ------------------------------------------------------------------------------------------------
 //
-// W warps own a row: thread t of the group has the vectors t, t + 32 W, ...  SHIFT: rows that start anywhere, of any length
-// (load_vector, store_vector); else they are on 16-byte boundaries.  The 128 elements that share a scale in 8 bits lie in one
-// warp.
+// W warps own a row, K vectors a thread: those of a warp 32 W apart, or, with SHIFT, one run of 32 K (rows that start anywhere, of any
+// length: load_vectors, store_vectors); without, rows are on 16-byte boundaries.  The 128 elements that share a scale in 8 bits
+// lie in one warp.
 
-template <class D, bool SHIFT>
-__device__ __forceinline__ uint4 take(const unsigned char* row, int u, int units, int n, const Bytes& m) {
-  if constexpr (SHIFT) return load_vector<D>(row, u, n, m);
-  else return u < units ? ld_stream16(row + int64_t(u) * 16) : make_uint4(0, 0, 0, 0);
+template <int K, int W, bool SHIFT>
+__device__ __forceinline__ int unit_of(int t, int k) {
+  return SHIFT ? (t >> 5) * (32 * K) + k * 32 + (t & 31) : t + k * (32 * W);
 }
-template <class D, bool SHIFT>
-__device__ __forceinline__ void put(unsigned char* row, int u, int units, int n, const uint4& q) {
-  if constexpr (SHIFT) store_vector<D>(row, u, n, q);
-  else if (u < units) st_stream16(row + int64_t(u) * 16, q);
+template <class D, int K, int W, bool SHIFT>
+__device__ __forceinline__ void take(const RowAt& r, int t, int units, uint4 (&q)[K]) {
+  if constexpr (SHIFT) {
+    load_vectors<D>(r, unit_of<K, W, true>(t, 0), q);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int u = t + k * (32 * W);
+      q[k] = u < units ? ld_stream16(r.row + int64_t(u) * 16) : make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+template <class D, int K, int W, bool SHIFT>
+__device__ __forceinline__ void put(unsigned char* row, int t, int units, int n, const uint4 (&q)[K]) {
+  if constexpr (SHIFT) {
+    store_vectors<D>(row, unit_of<K, W, true>(t, 0), n, q);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int u = t + k * (32 * W);
+      if (u < units) st_stream16(row + int64_t(u) * 16, q[k]);
+    }
+  }
 }
 
 // The sum of v over the W warps of a group, the same in all threads.  slots: W floats of the group, another set for the next call.
@@ -278,28 +298,28 @@ __device__ __forceinline__ void store_codes(unsigned char* row, int u, int left,
 
 __host__ __device__ constexpr int reg_threads(int warps) { return warps * 32 > 256 ? warps * 32 : 256; }
 
-// CTAs of 256 threads an SM: in 8 bits three (16384 x 8192 bf16 with a residual 156 us; two, which the compiler takes by
-// itself, 182; four 176), else four (16384 x 8192 bf16 84 us, three 93, six 91).
+// CTAs of 256 threads an SM: in 8 bits three for 16-bit rows (16384 x 8192 bf16 with a residual 164 us; two 197, four 170), else
+// four (into e4m3 16384 x 4096 fp32 with a residual 150 us, three 181; 16384 x 8192 bf16 84 us, three 93, six 91).
 template <class D, int K, int W, bool SHIFT, bool E4M3>
-__global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 ? 3 : 4) * 256 / reg_threads(W)) k_rms_norm(NormArgs a) {
+__global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes == 2 ? 3 : 4) * 256 / reg_threads(W)) k_rms_norm(NormArgs a) {
   constexpr int E = D::kVec, GT = W * 32, G = reg_threads(W) / GT;
   __shared__ float sums[2][reg_threads(W) / 32], tops[2][reg_threads(W) / 32];
   const int group = threadIdx.x / GT, t = threadIdx.x % GT, lane = t & 31;
   const int n = int(a.N), units = (n + E - 1) / E;
   const int64_t bytes = a.N * D::kBytes;
   const Bytes xm = bytes_of(a.x, a.M, a.x_pitch, bytes), rm = bytes_of(a.r, a.M, a.r_pitch, bytes);
+  constexpr bool PACKED = !SHIFT && E4M3;
+  const bool packed = a.w && !(a.w_f32 && D::kBytes == 2);
   int it = 0;
   for (int64_t row = int64_t(blockIdx.x) * G + group; row < a.M; row += int64_t(gridDim.x) * G, it ^= 1) {
-    const unsigned char* xr = a.x + row * a.x_pitch;
+    const RowAt xr = row_at<D>(a.x + row * a.x_pitch, n, xm);
     uint4 h[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) h[k] = take<D, SHIFT>(xr, t + k * GT, units, n, xm);
+    take<D, K, W, SHIFT>(xr, t, units, h);
     if (a.r) {
-      const unsigned char* rr = a.r + row * a.r_pitch;
+      const RowAt rr = row_at<D>(a.r + row * a.r_pitch, n, rm);
       unsigned char* to = a.h + row * a.h_pitch;
       uint4 r[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) r[k] = take<D, SHIFT>(rr, t + k * GT, units, n, rm);
+      take<D, K, W, SHIFT>(rr, t, units, r);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         float v[E], w[E];
@@ -308,8 +328,8 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 ? 3 : 4) * 2
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] += w[e];
         h[k] = D::pack(v);
-        put<D, SHIFT>(to, t + k * GT, units, n, h[k]);
       }
+      put<D, K, W, SHIFT>(to, t, units, n, h);
     }
     float sum = 0.f;
 #pragma unroll
@@ -319,15 +339,26 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 ? 3 : 4) * 2
 #pragma unroll
       for (int e = 0; e < E; ++e) sum = __fmaf_rn(v[e], v[e], sum);
     }
+    uint4 wq[K];  // the weights as they are, under way while the sum is joined (in 8 bits: 164 us against 198)
+    if (PACKED && packed) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) wq[k] = __ldg(static_cast<const uint4*>(a.w) + min(t + k * GT, units - 1));
+    }
     sum = group_sum<W>(sum, sums[it] + group * W, group, t);
     const float rstd = 1.f / sqrtf(sum / float(a.N) + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     unsigned char* yr = a.y + row * a.y_pitch;
     const auto value = [&](int k, float(&v)[E]) {  // y in 32 bits, 0 behind the row's end
-      const int u = t + k * GT;
+      const int u = unit_of<K, W, SHIFT>(t, k);
       float w[E];
       D::unpack(h[k], v);
-      weights<D, SHIFT>(a, min(u, units - 1), w);  // h is 0 behind the end
+      if (PACKED && packed) {
+        D::unpack(wq[k], w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] += a.offset;
+      } else {
+        weights<D, SHIFT>(a, min(u, units - 1), w);  // h is 0 behind the end
+      }
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = v[e] * rstd * w[e];
     };
@@ -336,8 +367,9 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 ? 3 : 4) * 2
       for (int k = 0; k < K; ++k) {
         float v[E];
         value(k, v);
-        put<D, SHIFT>(yr, t + k * GT, units, n, D::pack(v));
+        h[k] = D::pack(v);
       }
+      put<D, K, W, SHIFT>(yr, t, units, n, h);
     } else {
       const auto top_of = [&](const float(&v)[E]) {
         float m = fabsf(v[0]);
@@ -346,7 +378,7 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 ? 3 : 4) * 2
         return m;
       };
       const auto store = [&](int k, const float(&v)[E], float inv) {
-        const int u = t + k * GT;
+        const int u = unit_of<K, W, SHIFT>(t, k);
         if (u < units) store_codes<E, SHIFT>(yr, u, n - u * E, v, inv);
       };
       if (a.groups == 1 && a.N > kGroup) {
@@ -357,7 +389,7 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 ? 3 : 4) * 2
           top = fmaxf(top, top_of(y[k]));
         }
         top = group_max<W>(top, tops[it] + group * W, group, t);
-        const float scale = fmaxf(top / kE4m3Max, kScaleMin), inv = 1.f / scale;
+        const float scale = scale_of(top), inv = __fdividef(1.f, scale);
         if (t == 0) a.scales[row] = scale;
 #pragma unroll
         for (int k = 0; k < K; ++k) store(k, y[k], inv);
@@ -370,8 +402,8 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 ? 3 : 4) * 2
           float top = top_of(y);
 #pragma unroll
           for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-          const float scale = fmaxf(top / kE4m3Max, kScaleMin), inv = 1.f / scale;
-          const int u = t + k * GT;
+          const float scale = scale_of(top), inv = __fdividef(1.f, scale);
+          const int u = unit_of<K, W, SHIFT>(t, k);
           if (u < units && (lane & (lanes - 1)) == 0) a.scales[row * a.groups + u / lanes] = scale;
           store(k, y, inv);
         }
@@ -394,18 +426,20 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
   int it = 0;
   for (int64_t row = int64_t(blockIdx.x) * G + group; row < a.M; row += step, it ^= 1) {
     uint4 dy[K], h[K], sg[K];
+    const RowAt dr = row_at<D>(a.dy + row * a.dy_pitch, n, dm), hr = row_at<D>(a.h + row * a.h_pitch, n, hm), gr = row_at<D>(a.sg + row * a.sg_pitch, n, gm);
+    take<D, K, W, SHIFT>(dr, t, units, dy);
+    take<D, K, W, SHIFT>(hr, t, units, h);
+    if (a.sg) {
+      take<D, K, W, SHIFT>(gr, t, units, sg);
+    } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int u = t + k * GT;
-      dy[k] = take<D, SHIFT>(a.dy + row * a.dy_pitch, u, units, n, dm);
-      h[k] = take<D, SHIFT>(a.h + row * a.h_pitch, u, units, n, hm);
-      sg[k] = a.sg ? take<D, SHIFT>(a.sg + row * a.sg_pitch, u, units, n, gm) : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < K; ++k) sg[k] = make_uint4(0, 0, 0, 0);
     }
     const float rstd = a.rstd[row];
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = t + k * GT;
+      const int u = unit_of<K, W, SHIFT>(t, k);
       if (u >= units) continue;
       float d[E], x[E], w[E];
       D::unpack(dy[k], d);
@@ -423,7 +457,7 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
     unsigned char* to = a.dx + row * a.dx_pitch;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = t + k * GT;
+      const int u = unit_of<K, W, SHIFT>(t, k);
       float d[E], x[E], w[E] = {}, s[E];
       D::unpack(dy[k], d);
       D::unpack(h[k], x);
@@ -431,8 +465,9 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
       if (u < units) weights<D, SHIFT>(a, u, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) d[e] = __fmaf_rn(rstd, d[e] * w[e], __fmaf_rn(slope, x[e], s[e]));
-      put<D, SHIFT>(to, u, units, n, D::pack(d));
+      dy[k] = D::pack(d);
     }
+    put<D, K, W, SHIFT>(to, t, units, n, dy);
   }
   griddep_launch();
   if (!a.dw) return;
@@ -441,7 +476,7 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
     if (group == g) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int u = t + k * GT;
+        const int u = unit_of<K, W, SHIFT>(t, k);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           float* c = columns + (G > 1 ? (k * E + e) * GT + t : 0);
@@ -743,7 +778,7 @@ cudaError_t launch_grad_type(const RmsNormGrad& p, GradArgs a, const DeviceInfo&
   } else if (c) {
     const int threads = reg_threads(c->warps), groups = threads / 32 / c->warps;
     const int64_t ctas = (p.M + groups - 1) / groups;
-    const int64_t per_sm = threads > 256 ? 2 : kGradCtas;
+    const int64_t per_sm = threads > 256 ? 1 : 2;  // what the registers allow
     a.parts_n = int(ctas < dev.sm_count * per_sm ? ctas : dev.sm_count * per_sm);
     c->fn<<<unsigned(a.parts_n), threads, 0, p.stream>>>(a);
     if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;

@@ -48,8 +48,9 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStrea
 //
 // Vector u of a row are its elements u E .. u E + E - 1, 16 bytes.  Where rows are not on 16-byte boundaries a warp whose
 // lanes have consecutive vectors moves whole 16-byte lines of memory and shifts them over its lanes: each lane loads the
-// line that its vector begins in and has the rest from the next lane, and stores the line that begins in its vector.  (By single
-// elements the backward norm of 777 rows of 5003 fp16 elements took 74 us; so it takes 25.)
+// line that its vector begins in and has the rest from the next lane, and stores the line that begins in its vector; only
+// the ends of what a warp has are stored by single elements.  (By single
+// elements the backward norm of 777 rows of 5003 fp16 elements took 74 us; so it takes 30.)
 
 // The bytes of a matrix: whole lines are loaded only inside them.
 struct Bytes {
@@ -60,22 +61,18 @@ __device__ __forceinline__ Bytes bytes_of(const unsigned char* p, int64_t rows, 
   return Bytes{p, p + (rows - 1) * pitch + row_bytes};
 }
 
-// Bytes delta .. delta + 15 of a and b one after the other, delta even.
-__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int delta) {
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  const int words = delta >> 2;
-  if (words & 2) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (words & 1) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
+// Bytes delta .. delta + 15 of a and b one after the other, delta even and the same in all lanes.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int delta) {
   const uint32_t bits = (delta & 3) * 8;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  const auto from = [&](uint32_t v, uint32_t w, uint32_t x, uint32_t y, uint32_t z) {
+    return make_uint4(__funnelshift_r(v, w, bits), __funnelshift_r(w, x, bits), __funnelshift_r(x, y, bits), __funnelshift_r(y, z, bits));
+  };
+  switch (delta >> 2) {
+    case 0: return from(a.x, a.y, a.z, a.w, b.x);
+    case 1: return from(a.y, a.z, a.w, b.x, b.y);
+    case 2: return from(a.z, a.w, b.x, b.y, b.z);
+    default: return from(a.w, b.x, b.y, b.z, b.w);
+  }
 }
 
 // Elements [from, to) of a vector, the others fill (a word).
@@ -94,15 +91,16 @@ __device__ __forceinline__ uint4 keep(uint4 q, int from, int to, uint32_t fill) 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint4 next_lane(uint4 q) {
-  return make_uint4(__shfl_down_sync(~0u, q.x, 1), __shfl_down_sync(~0u, q.y, 1), __shfl_down_sync(~0u, q.z, 1), __shfl_down_sync(~0u, q.w, 1));
+// The next lane's q; for lane 31 lane 0's first.
+__device__ __forceinline__ uint4 next_lane(const uint4& q, const uint4& first) {
+  const int lane = threadIdx.x & 31, from = (lane + 1) & 31;
+  return make_uint4(__shfl_sync(~0u, lane ? q.x : first.x, from), __shfl_sync(~0u, lane ? q.y : first.y, from),
+                    __shfl_sync(~0u, lane ? q.z : first.z, from), __shfl_sync(~0u, lane ? q.w : first.w, from));
 }
 
-// The line at a: of the row's elements where it is not all inside the matrix.
+// The line at a, elements of the row [row, end) only: for the few lines that are not all inside the matrix.
 template <class D>
-__device__ __forceinline__ uint4 load_line(const unsigned char* a, const unsigned char* row, const unsigned char* end, const Bytes& m) {
-  if (a >= end || a + 16 <= row) return make_uint4(0, 0, 0, 0);
-  if (a >= m.lo && a + 16 <= m.hi) return ld_stream16(a);
+__device__ __noinline__ uint4 load_elements(const unsigned char* a, const unsigned char* row, const unsigned char* end) {
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int e = 0; e < D::kVec; ++e) {
@@ -114,24 +112,46 @@ __device__ __forceinline__ uint4 load_line(const unsigned char* a, const unsigne
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Vector u of a row of n elements, 0 behind its end.  All lanes of a warp, with consecutive u.
+// A row of n elements; inside: all lines that it has a part in are.
+struct RowAt {
+  const unsigned char* row;
+  const unsigned char* end;
+  int n, delta;  // delta: bytes from a line's start to a vector's
+  bool inside;
+};
 template <class D>
-__device__ __forceinline__ uint4 load_vector(const unsigned char* row, int u, int n, const Bytes& m) {
-  const unsigned char* p = row + int64_t(u) * 16;
-  const unsigned char* end = row + int64_t(n) * D::kBytes;
-  const int delta = int(reinterpret_cast<uintptr_t>(p) & 15);
-  uint4 q = load_line<D>(p - delta, row, end, m);
-  if (delta) {
-    uint4 b = next_lane(q);
-    if ((threadIdx.x & 31) == 31) b = load_line<D>(p - delta + 16, row, end, m);
-    q = shifted(q, b, delta);
-  }
-  const int left = n - u * D::kVec;
-  return left >= D::kVec ? q : keep<D>(q, 0, left, 0);
+__device__ __forceinline__ RowAt row_at(const unsigned char* row, int n, const Bytes& m) {
+  RowAt r{row, row + int64_t(n) * D::kBytes, n, int(reinterpret_cast<uintptr_t>(row) & 15), true};
+  r.inside = row - r.delta >= m.lo && r.end + (-reinterpret_cast<uintptr_t>(r.end) & 15) <= m.hi;
+  return r;
 }
 
+// Vectors u, u + 32, ... u + 32 (K - 1) of a row, 0 behind its end.  All lanes of a warp, with consecutive u.
+template <class D, int K>
+__device__ __forceinline__ void load_vectors(const RowAt& r, int u, uint4 (&q)[K]) {
+  const unsigned char* p = r.row + int64_t(u) * 16 - r.delta;
+  const auto line = [&](const unsigned char* a) {
+    if (a >= r.end) return make_uint4(0, 0, 0, 0);
+    return r.inside ? ld_stream16(a) : load_elements<D>(a, r.row, r.end);
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k) q[k] = line(p + k * 512);
+  if (r.delta) {
+    uint4 last = make_uint4(0, 0, 0, 0);  // lane 0: the line behind the warp's vectors
+    if ((threadIdx.x & 31) == 0) last = line(p + K * 512);
+#pragma unroll
+    for (int k = 0; k < K; ++k) q[k] = shifted(q[k], next_lane(q[k], k + 1 < K ? q[k + 1] : last), r.delta);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int left = r.n - (u + k * 32) * D::kVec;
+    if (left < D::kVec) q[k] = keep<D>(q[k], 0, left, 0);
+  }
+}
+
+// Elements [from, to) of a vector, to their places from p on.
 template <class D>
-__device__ __forceinline__ void store_elements(unsigned char* p, const uint4& q, int from, int to) {
+__device__ __noinline__ void store_elements(unsigned char* p, uint4 q, int from, int to) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int e = 0; e < D::kVec; ++e) {
@@ -141,22 +161,22 @@ __device__ __forceinline__ void store_elements(unsigned char* p, const uint4& q,
   }
 }
 
-// Stores what load_vector reads.
-template <class D>
-__device__ __forceinline__ void store_vector(unsigned char* row, int u, int n, const uint4& q) {
+// Stores what load_vectors reads.
+template <class D, int K>
+__device__ __forceinline__ void store_vectors(unsigned char* row, int u, int n, const uint4 (&q)[K]) {
+  const int delta = int(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x & 31;
+  // elements before the line that begins in a vector; the lane before stores them where its line is whole
+  const int head = delta ? (16 - delta) / D::kBytes : 0;
   unsigned char* p = row + int64_t(u) * 16;
-  const int delta = int(reinterpret_cast<uintptr_t>(p) & 15), left = n - u * D::kVec, lane = threadIdx.x & 31;
-  if (!delta) {
-    if (left >= D::kVec) st_stream16(p, q);
-    else store_elements<D>(p, q, 0, left);
-    return;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int left = n - (u + k * 32) * D::kVec;
+    uint4 line = q[k];
+    if (delta) line = shifted(line, next_lane(line, q[k + 1 < K ? k + 1 : k]), 16 - delta);
+    const bool whole = left >= D::kVec + head && (lane < 31 || k + 1 < K || !delta), first = delta && ((lane == 0 && k == 0) || left < head);
+    if (whole) st_stream16(p + k * 512 + (delta ? 16 - delta : 0), line);
+    if ((first || !whole) && left > 0) store_elements<D>(p + k * 512, q[k], first ? 0 : head, whole ? min(head, left) : min(D::kVec, left));
   }
-  // elements before the line that begins in this vector; the lane before stores them where its line is whole
-  const int head = (16 - delta) / D::kBytes;
-  const uint4 b = next_lane(q);
-  if (lane == 0 || left < head) store_elements<D>(p, q, 0, min(head, left));
-  if (lane < 31 && left >= D::kVec + head) st_stream16(p + 16 - delta, shifted(q, b, 16 - delta));
-  else store_elements<D>(p, q, head, min(D::kVec, left));
 }
 
 }  // namespace rwo

@@ -1,7 +1,7 @@
 """grad_norm and clip_grad_norm against float64.
 
-Tolerances: a thread adds up at most 40 squares in fp32, the rest is fp64: 41 2^-24 of the sum, half of that of the norm, and its
-rounding to fp32.  A scaled value is off by the norm's error and two roundings, then half a step of its type.
+Tolerances: a thread adds up at most 66 squares in fp32, in two chains, the rest is fp64: 35 2^-24 of the sum, half of that of the
+norm, and its rounding to fp32.  A scaled value is off by the norm's error and two roundings, then half a step of its type.
 """
 import math
 

@@ -35,7 +35,7 @@ def test_loss_faults(lib):
 
 
 def norm(M=4, N=256, dt=1, out=0, lib=None, **kw):
-    return lib.rms_norm_rows(train._Norm(**{**dict(x=X, y=X + 0x8000, eps=1e-6), **kw}), M, N, dt, out, None)
+    return lib.rms_norm_rows(ctypes.byref(train._Norm(**{**dict(x=X, y=X + 0x8000, eps=1e-6), **kw})), M, N, dt, out, None)
 
 
 def test_norm_faults(lib):
@@ -60,7 +60,7 @@ def test_norm_faults(lib):
 
 def test_norm_grad_faults(lib):
     def call(M=4, N=256, dt=1, ws=X, n=2 ** 40, **kw):
-        return lib.rms_norm_rows_backward(train._NormGrad(**{**dict(dy=X, h=X, rstd=X, dx=X), **kw}), M, N, dt, ws, n, None)
+        return lib.rms_norm_rows_backward(ctypes.byref(train._NormGrad(**{**dict(dy=X, h=X, rstd=X, dx=X), **kw})), M, N, dt, ws, n, None)
 
     assert lib.rms_norm_rows_backward(None, 4, 4, 0, X, 0, None) == BAD
     assert call(N=0) == BAD and call(M=-1) == BAD and call(dt=9) == BAD and call(N=2 ** 31) == NO
@@ -124,6 +124,11 @@ def test_grad_norm_faults(lib):
 
 def test_structures_match_the_header():
     assert ctypes.sizeof(train._Norm) == 13 * 8 + 8 and ctypes.sizeof(train._NormGrad) == 13 * 8 + 8 and ctypes.sizeof(train._Grad) == 32
+    for packed, whole, floats in ((train._NORM, train._Norm, 2), (train._NORM_GRAD, train._NormGrad, 1)):
+        names = [n for n, _ in whole._fields_]
+        a = whole.from_buffer_copy(packed.pack(*range(1, 14), *(0.5 * (k + 1) for k in range(floats))))
+        assert ctypes.sizeof(whole) == packed.size
+        assert [getattr(a, n) for n in names] == [*range(1, 14), *(0.5 * (k + 1) for k in range(floats))]
 
 
 def test_binding_refuses_on_the_host():
