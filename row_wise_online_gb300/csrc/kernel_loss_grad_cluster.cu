@@ -8,6 +8,9 @@
 // Rows start anywhere: the vectors are those of the gradient's 16-byte grid, so that whole vectors are stored; the copy takes
 // whole 16-byte lines of x, the few elements around them are copied one by one, and where x lies otherwise than the gradient
 // (SHIFT) a vector is put together from two of shared memory.
+#include <mutex>
+#include <vector>
+
 #include "loss_grad.cuh"
 
 namespace rwo {
@@ -254,6 +257,37 @@ Kernel pick(int threads, bool smooth, bool shift) {
   return threads == 512 ? pick<D, 512, 8>(smooth, shift) : threads == 256 ? pick<D, 256, 8>(smooth, shift) : pick<D, 128, 16>(smooth, shift);
 }
 
+// Clusters of a launch that the device holds at once, asked once for each configuration (each time, it would be half of a call's time
+// on the host).
+cudaError_t resident_clusters(Kernel fn, const cudaLaunchConfig_t& cfg, int cluster, const DeviceInfo& dev, int* out) {
+  struct Known {
+    int device;
+    Kernel fn;
+    int cluster;
+    size_t shared;
+    int clusters;
+  };
+  static std::mutex mutex;
+  static std::vector<Known> known;
+  std::lock_guard<std::mutex> lock(mutex);
+  for (const Known& k : known)
+    if (k.device == dev.device && k.fn == fn && k.cluster == cluster && k.shared == cfg.dynamicSmemBytes) {
+      *out = k.clusters;
+      return cudaSuccess;
+    }
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaFuncGetAttributes(&attr, (const void*)fn);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.max_smem_per_block_optin - int(attr.sharedSizeBytes));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(out, (const void*)fn, &cfg);
+  if (e == cudaSuccess) {
+    if (known.size() >= 256) known.clear();
+    known.push_back(Known{dev.device, fn, cluster, cfg.dynamicSmemBytes, *out});
+  }
+  return e;
+}
+
 int64_t vectors_of(const LossGrad& p) { return (p.N + (16 / elem_bytes(p.dtype)) - 1) / (16 / elem_bytes(p.dtype)) + 1; }
 
 constexpr int kHeld = 2048;  // vectors of a CTA of 128 or 256 threads
@@ -299,11 +333,8 @@ cudaError_t launch_loss_grad_cluster(const LossGrad& p, const LossArgs& args, co
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(unsigned(a.cluster));
-  cudaError_t e;
-  if ((e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, shared)) != cudaSuccess) return e;
-  if (a.cluster > 8 && (e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
   int clusters = 0;
-  if ((e = cudaOccupancyMaxActiveClusters(&clusters, (const void*)fn, &cfg)) != cudaSuccess) return e;
+  if (const cudaError_t e = resident_clusters(fn, cfg, a.cluster, dev, &clusters); e != cudaSuccess) return e;
   if (clusters < 1) return cudaErrorLaunchOutOfResources;
   const int64_t n = p.M < clusters ? p.M : clusters;
   cfg.gridDim = dim3(unsigned(n * a.cluster));
