@@ -26,7 +26,7 @@ int chunk_of(int64_t T, int64_t D) {
   return c;
 }
 
-constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCtas = 8;
+constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCtas = 16;
 constexpr int kDigitBits = 10;
 
 __device__ __forceinline__ int64_t token_at(const void* tokens, int bytes, int64_t i) {
@@ -48,13 +48,60 @@ struct LookupArgs {
   unsigned* status;
 };
 
-constexpr int kLookupThreads = 256, kLookupPer = 8;
+constexpr int kLookupThreads = 256;
+
+// The value of an element of a row that no table row gives: 0 for padding, else NaN.
+template <class D>
+__device__ __forceinline__ uint4 no_row(int64_t token) {
+  const float f = token < 0 ? 0.f : __int_as_float(0x7fc00000);
+  float2 v[D::kVec / 2];
+#pragma unroll
+  for (int e = 0; e < D::kVec / 2; ++e) v[e] = make_float2(f, f);
+  return D::pack2(v);
+}
+template <class D>
+__device__ __forceinline__ uint4 times(const uint4& q, float scale) {
+  const float2 s = make_float2(scale, scale);
+  float2 v[D::kVec / 2];
+  D::unpack2(q, v);
+#pragma unroll
+  for (int e = 0; e < D::kVec / 2; ++e) v[e] = __fmul2_rn(v[e], s);
+  return D::pack2(v);
+}
+
+// Short rows on 16-byte boundaries: 2^shift lanes a row, kLookupRows rows a lane at a time (200000 rows of 64 bf16 elements: 12 us, a
+// warp a row 43).
+constexpr int kLookupRows = 4;
+
+template <class D>
+__global__ void __launch_bounds__(kLookupThreads) k_embedding_short(LookupArgs a, int shift) {
+  const int64_t step = int64_t(gridDim.x) * kLookupThreads >> shift, thread = int64_t(blockIdx.x) * kLookupThreads + threadIdx.x;
+  const int u = int(thread & ((1 << shift) - 1));
+  if (u >= a.units) return;
+  for (int64_t t0 = thread >> shift; t0 < a.T; t0 += step * kLookupRows) {
+    int64_t token[kLookupRows];
+    uint4 q[kLookupRows];
+#pragma unroll
+    for (int k = 0; k < kLookupRows; ++k) token[k] = t0 + k * step < a.T ? token_at(a.tokens, a.token_bytes, t0 + k * step) : -1;
+#pragma unroll
+    for (int k = 0; k < kLookupRows; ++k) {
+      if (token[k] >= 0 && token[k] < a.V) {
+        q[k] = times<D>(ld_stream16(a.table + token[k] * a.table_pitch + u * 16), a.scale);
+      } else {
+        if (token[k] >= 0 && u == 0) atomicOr(a.status, kStatusBadIndex);
+        q[k] = no_row<D>(token[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kLookupRows; ++k)
+      if (t0 + k * step < a.T) st_stream16(a.y + (t0 + k * step) * a.y_pitch + u * 16, q[k]);
+  }
+}
 
 // A warp moves pieces of rows: kLookupPer vectors a lane, all loaded before the first is stored, and the next piece's token is
 // under way meanwhile.
-template <class D, bool SHIFT>
-__global__ void __launch_bounds__(kLookupThreads, 4) k_embedding(LookupArgs a) {
-  constexpr int E = D::kVec;
+template <class D, bool SHIFT, int kLookupPer>
+__global__ void __launch_bounds__(kLookupThreads, kLookupPer == 8 ? 4 : kLookupPer == 4 ? 5 : 6) k_embedding(LookupArgs a) {
   const int lane = threadIdx.x & 31, n = int(a.D);
   const int64_t warps = int64_t(gridDim.x) * (kLookupThreads / 32), items = a.T * a.pieces;
   const Bytes table = bytes_of(a.table, a.V, a.table_pitch, a.D * D::kBytes);
@@ -81,24 +128,13 @@ __global__ void __launch_bounds__(kLookupThreads, 4) k_embedding(LookupArgs a) {
           if (u0 + k * 32 < a.units) q[k] = ld_stream16(r.row + int64_t(u0 + k * 32) * 16);
       }
       if (a.scale != 1.f) {
-        const float2 s = make_float2(a.scale, a.scale);
 #pragma unroll
-        for (int k = 0; k < kLookupPer; ++k) {
-          float2 v[E / 2];
-          D::unpack2(q[k], v);
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) v[e] = __fmul2_rn(v[e], s);
-          q[k] = D::pack2(v);
-        }
+        for (int k = 0; k < kLookupPer; ++k) q[k] = times<D>(q[k], a.scale);
       }
     } else {
       if (token >= 0 && u0 == 0) atomicOr(a.status, kStatusBadIndex);
-      float2 v[E / 2];
-      const float f = token < 0 ? 0.f : __int_as_float(0x7fc00000);
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) v[e] = make_float2(f, f);
-#pragma unroll
-      for (int k = 0; k < kLookupPer; ++k) q[k] = D::pack2(v);
+      for (int k = 0; k < kLookupPer; ++k) q[k] = no_row<D>(token);
     }
     if constexpr (SHIFT) {
       store_vectors<D>(to, u0, n, q);
@@ -134,16 +170,31 @@ cudaError_t launch_lookup(const Embedding& p, const DeviceInfo& dev) {
   const bool vec = on16({reinterpret_cast<uintptr_t>(a.table), reinterpret_cast<uintptr_t>(a.y), uintptr_t(a.table_pitch), uintptr_t(a.y_pitch),
                          uintptr_t(p.D * D::kBytes)});
   a.units = int((p.D + D::kVec - 1) / D::kVec);
-  a.pieces = (a.units + kLookupPer * 32 - 1) / (kLookupPer * 32);
-  const int64_t per = kLookupThreads / 32, most = int64_t(dev.sm_count) * 4;
+  if (vec && a.units <= 16) {
+    int shift = 0;
+    while (1 << shift < a.units) ++shift;
+    const int64_t per = int64_t(kLookupThreads >> shift) * kLookupRows, most = int64_t(dev.sm_count) * (dev.max_threads_per_sm / kLookupThreads);
+    const int64_t ctas = (p.T + per - 1) / per;
+    k_embedding_short<D><<<unsigned(ctas < most ? ctas : most), kLookupThreads, 0, p.stream>>>(a, shift);
+    return cudaGetLastError();
+  }
+  const int held = a.units <= 64 ? 2 : a.units <= 128 ? 4 : 8;  // vectors of a lane
+  a.pieces = (a.units + held * 32 - 1) / (held * 32);
+  const int64_t per = kLookupThreads / 32, most = int64_t(dev.sm_count) * (held == 8 ? 4 : held == 4 ? 5 : 6);
   const int64_t ctas = p.T > most * per ? most : (p.T * a.pieces + per - 1) / per;
   const unsigned grid = unsigned(ctas < most ? ctas : most);
-  if (vec) k_embedding<D, false><<<grid, kLookupThreads, 0, p.stream>>>(a);
-  else k_embedding<D, true><<<grid, kLookupThreads, 0, p.stream>>>(a);
+  const auto fn = vec ? (held == 8 ? k_embedding<D, false, 8> : held == 4 ? k_embedding<D, false, 4> : k_embedding<D, false, 2>)
+                      : (held == 8 ? k_embedding<D, true, 8> : held == 4 ? k_embedding<D, true, 4> : k_embedding<D, true, 2>);
+  fn<<<grid, kLookupThreads, 0, p.stream>>>(a);
   return cudaGetLastError();
 }
 
 // ---- gradient: the sort ---------------------------------------------------------------------------------------------
+
+// A run of equal tokens over many chunks: where it begins, and its partial sums.
+struct LongRun {
+  int64_t chunk, parts;
+};
 
 struct GradArgs {
   const unsigned char* dy;
@@ -154,12 +205,16 @@ struct GradArgs {
   const uint32_t* sorted_keys;
   const uint32_t* sorted_pos;
   uint32_t* bits;  // rows that a token names
+  uint32_t* long_count;
+  LongRun* long_runs;
   float* parts;    // [chunk][2][part_pitch]: sums of the run that came from the chunk before, of the one that goes on
   int64_t T, V, D;
   int64_t dy_pitch, g_pitch;  // bytes
   int64_t part_pitch;         // floats
   int64_t chunks;
+  int64_t groups;             // of chunks that a CTA has
   int chunk;                  // tokens of one
+  bool small;                 // rows of at most 32 vectors: a warp a chunk
   int units;                  // vectors of a row of dy
   int slices;                 // CTAs of a chunk
   int64_t fill_rows;          // rows of a zeroing CTA
@@ -187,6 +242,7 @@ __global__ void __launch_bounds__(kSortThreads) k_rank_tokens(GradArgs a) {
   const int n = int(a.T), tid = threadIdx.x, lane = tid & 31;
   const int64_t words = (a.V + 31) / 32, mine = (words + gridDim.x - 1) / gridDim.x;
   const int64_t w0 = blockIdx.x * mine < words ? blockIdx.x * mine : words, w1 = w0 + mine < words ? w0 + mine : words;
+  if (blockIdx.x == 0 && tid == 0) *a.long_count = 0;
   for (int i = tid; i < n; i += kSortThreads) keys[i] = key_of(a, i);
   for (int w = tid; w < int(w1 - w0); w += kSortThreads) bits[w] = 0;
   __syncthreads();
@@ -216,7 +272,20 @@ __global__ void __launch_bounds__(kSortThreads) k_rank_tokens(GradArgs a) {
 // lane at a time, and stays in registers between counting and moving where that is all of it.
 constexpr int kRun = 8;
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) k_sort_tokens(GradArgs a) {
+// The lanes whose digit is this lane's, of those that have one.  A vote for each bit: __match_any_sync's time goes with the number of
+// different digits (32768 tokens: the sort takes 33 us with it).
+__device__ __forceinline__ uint32_t alike(uint32_t digit, bool on, int bits) {
+  uint32_t same = __ballot_sync(~0u, on);
+#pragma unroll
+  for (int b = 0; b < kDigitBits; ++b) {
+    if (b >= bits) break;
+    const uint32_t ones = __ballot_sync(~0u, digit >> b & 1);
+    same &= digit >> b & 1 ? ones : ~ones;
+  }
+  return same;
+}
+
+__global__ void __launch_bounds__(kSortThreads) k_sort_tokens(GradArgs a) {
   extern __shared__ uint32_t shared[];
   const int bins = 1 << a.digit_bits, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* total = shared;                             // [bins], read by the cluster's other CTAs
@@ -257,8 +326,8 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       for (int k = 0; k < kRun; ++k) {
         if (i + k * 32 >= i1) break;
         const bool on = i + k * 32 + lane < i1;
-        const uint32_t d = on ? key[k] >> shift & (bins - 1) : 0xffffffffu;
-        const uint32_t same = __match_any_sync(~0u, d);
+        const uint32_t d = key[k] >> shift & (bins - 1);
+        const uint32_t same = alike(d, on, a.digit_bits);
         if (on && !(same & below)) counts[d * 33 + warp] += __popc(same);
         __syncwarp();
       }
@@ -308,8 +377,8 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       for (int k = 0; k < kRun; ++k) {
         if (i + k * 32 >= i1) break;
         const bool on = i + k * 32 + lane < i1;
-        const uint32_t d = on ? key[k] >> shift & (bins - 1) : 0xffffffffu;
-        const uint32_t same = __match_any_sync(~0u, d);
+        const uint32_t d = key[k] >> shift & (bins - 1);
+        const uint32_t same = alike(d, on, a.digit_bits);
         if (on) {
           const uint32_t to = base[d] + counts[d * 33 + warp] + __popc(same & below);
           to_keys[to] = key[k];
@@ -322,6 +391,7 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     }
     cluster_sync();
   }
+  if (cta == 0 && tid == 0) *a.long_count = 0;
   if (a.accumulate) return;
   const int64_t words = (a.V + 31) / 32;
   for (int64_t i = int64_t(cta) * kSortThreads + tid; i < words; i += kSortCtas * kSortThreads) a.bits[i] = 0;
@@ -384,30 +454,43 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding_rows(GradArgs a) {
   constexpr int E = D::kVec;
   griddep_wait();
   griddep_launch();
-  const int64_t chunk_ctas = a.chunks * a.slices;
+  const int64_t chunk_ctas = a.groups * a.slices;
   if (blockIdx.x >= chunk_ctas) {
     // rows without a token
     const int64_t v0 = (blockIdx.x - chunk_ctas) * a.fill_rows, v1 = v0 + a.fill_rows < a.V ? v0 + a.fill_rows : a.V;
-    for (int64_t v = v0; v < v1; ++v) {
-      if (a.bits[v / 32] >> (v % 32) & 1) continue;
-      unsigned char* row = a.g + v * a.g_pitch;
-      if (a.fill_vec)
-        for (int64_t o = threadIdx.x * 16; o < a.D * G::kBytes; o += kRowThreads * 16) st_stream16(row + o, make_uint4(0, 0, 0, 0));
-      else
-        for (int64_t i = threadIdx.x; i < a.D; i += kRowThreads) G::store1(row, i, 0.f);
+    const uint32_t per = uint32_t(a.fill_vec ? a.D * G::kBytes / 16 : a.D), rows = uint32_t(v1 - v0);
+    uint32_t row = threadIdx.x / per, at = threadIdx.x - row * per;  // vectors, or elements, of the rows in one line
+    const uint32_t rows_on = kRowThreads / per, at_on = kRowThreads - rows_on * per;
+    while (row < rows) {
+      const int64_t v = v0 + row;
+      if (!(a.bits[v / 32] >> (v % 32) & 1)) {
+        unsigned char* to = a.g + v * a.g_pitch;
+        if (a.fill_vec) st_stream16(to + int64_t(at) * 16, make_uint4(0, 0, 0, 0));
+        else G::store1(to, at, 0.f);
+      }
+      row += rows_on;
+      at += at_on;
+      if (at >= per) {
+        at -= per;
+        ++row;
+      }
     }
     return;
   }
-  __shared__ uint32_t keys[kMostChunk + 2], pos[kMostChunk];
-  const int64_t chunk = blockIdx.x / a.slices, first = chunk * a.chunk;
-  const int u = int(blockIdx.x - chunk * a.slices) * kRowThreads + int(threadIdx.x);
-  if (threadIdx.x < a.chunk + 2) {
-    const int64_t i = first + int(threadIdx.x) - 1;
-    keys[threadIdx.x] = i >= 0 && i < a.T ? a.sorted_keys[i] : 0xffffffffu;
-    if (threadIdx.x >= 1 && threadIdx.x <= a.chunk && i < a.T) pos[threadIdx.x - 1] = a.sorted_pos[i];
+  // a CTA has a chunk's columns, or, of short rows, a warp has a chunk
+  __shared__ uint32_t all_keys[kRowThreads / 32][kMostChunk + 2], all_pos[kRowThreads / 32][kMostChunk];
+  const int part = a.small ? int(threadIdx.x) >> 5 : 0, t = a.small ? int(threadIdx.x) & 31 : int(threadIdx.x);
+  const int64_t group = blockIdx.x / a.slices, chunk = a.small ? group * (kRowThreads / 32) + part : group, first = chunk * a.chunk;
+  const int u = int(blockIdx.x - group * a.slices) * kRowThreads + t;
+  uint32_t* keys = all_keys[part];
+  uint32_t* pos = all_pos[part];
+  for (int k = t; k < a.chunk + 2; k += a.small ? 32 : kRowThreads) {
+    const int64_t i = first + k - 1;
+    keys[k] = i >= 0 && i < a.T ? a.sorted_keys[i] : 0xffffffffu;
+    if (k >= 1 && k <= a.chunk && i < a.T) pos[k - 1] = a.sorted_pos[i];
   }
   __syncthreads();
-  if ((u & ~31) >= a.units) return;  // warps stay whole
+  if ((u & ~31) >= a.units || chunk >= a.chunks) return;  // warps stay whole
   const int n = int(a.D);
   const Bytes dm = bytes_of(a.dy, a.T, a.dy_pitch, a.D * D::kBytes), gm = bytes_of(a.g, a.V, a.g_pitch, a.D * G::kBytes);
   float sum[E] = {};
@@ -447,9 +530,13 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding_rows(GradArgs a) {
   }
 }
 
-// Runs that go over the end of the chunk they begin in: a warp looks at one chunk for its run, and adds up the partial sums where they
-// are few; those of longer runs the CTA's warps take together, every eighth each.
-constexpr int kJoinWarps = 8, kJoinAlone = 16, kJoinColumns = 128;  // columns of a warp at a time, four a lane
+// Runs that go over the end of the chunk they begin in: a warp looks at one chunk for its run, and adds up the partial sums.  Runs
+// of many parts it puts on a list for k_embedding_long, where 32 warps share one's (262144 tokens of which 43000 are one: 510 us
+// with the CTA's eight warps here).
+constexpr int kJoinWarps = 8, kJoinColumns = 128;  // columns of a warp at a time, four a lane
+constexpr int kLongWarps = 32, kLongCtas = 32;
+constexpr int kAlone = 16;          // parts of a run that one warp adds up ...
+constexpr int64_t kFewChunks = 256;  // ... or all of them, where no run can have more parts than this
 
 template <class G>
 __device__ __forceinline__ void write_four(const GradArgs& a, uint32_t key, int64_t c, const float4& sum) {
@@ -461,64 +548,67 @@ __device__ __forceinline__ void write_four(const GradArgs& a, uint32_t key, int6
 }
 __device__ __forceinline__ void add(float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
 
+// Four columns' sums of part k of the run that begins in chunk `first`: that chunk's second, then the first of each that follows.
+__device__ __forceinline__ float4 part_of(const GradArgs& a, int64_t first, int64_t k, int64_t c) {
+  return *reinterpret_cast<const float4*>(a.parts + ((first + k) * 2 + (k == 0)) * a.part_pitch + c);
+}
+
 template <class G>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_embedding_join(GradArgs a) {
-  __shared__ float4 sums[kJoinWarps][32];
-  __shared__ int64_t lengths[kJoinWarps];
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x & 31;
+  const uint32_t* keys = a.sorted_keys;
+  const int64_t C = a.chunk, chunk = int64_t(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5), end = (chunk + 1) * C;
+  if (end >= a.T) return;
+  const uint32_t key = keys[end];
+  if (key >= a.V || keys[end - 1] != key || (chunk > 0 && keys[chunk * C] == key && keys[chunk * C - 1] == key)) return;  // none begins here
+  // the last chunk that the run reaches: its first token is the run's
+  int64_t lo = chunk + 1, step = 1;
+  while (lo + step < a.chunks && keys[(lo + step) * C] == key) {
+    lo += step;
+    step *= 2;
+  }
+  int64_t hi = lo + step < a.chunks ? lo + step : a.chunks;  // lo is the run's, hi is not
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (keys[mid * C] == key) lo = mid;
+    else hi = mid;
+  }
+  const int64_t n = lo - chunk + 1;
+  if (n > kAlone && a.chunks > kFewChunks) {
+    if (blockIdx.y == 0 && lane == 0) a.long_runs[atomicAdd(a.long_count, 1u)] = LongRun{chunk, n};
+    return;
+  }
+  for (int64_t c = int64_t(blockIdx.y) * kJoinColumns + lane * 4; c < a.D; c += int64_t(gridDim.y) * kJoinColumns) {
+    float4 sum = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int64_t k = 0; k < n; ++k) add(sum, part_of(a, chunk, k, c));
+    write_four<G>(a, key, c, sum);
+  }
+}
+
+template <class G>
+__global__ void __launch_bounds__(kLongWarps * 32) k_embedding_long(GradArgs a) {
+  __shared__ float4 sums[kLongWarps][32];
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t* keys = a.sorted_keys;
-  const int64_t C = a.chunk, chunk0 = int64_t(blockIdx.x) * kJoinWarps, chunk = chunk0 + warp, end = (chunk + 1) * C;
-  uint32_t key = 0;
-  int64_t n = 0;  // parts of the run that begins in this warp's chunk: the chunk's second, then the first of each that follows
-  if (end < a.T) {
-    key = keys[end];
-    const bool begins = key < a.V && keys[end - 1] == key && !(chunk > 0 && keys[chunk * C] == key && keys[chunk * C - 1] == key);
-    if (begins) {
-      // the last chunk that the run reaches: its first token is the run's
-      int64_t lo = chunk + 1, step = 1;
-      while (lo + step < a.chunks && keys[(lo + step) * C] == key) {
-        lo += step;
-        step *= 2;
-      }
-      int64_t hi = lo + step < a.chunks ? lo + step : a.chunks;  // lo is the run's, hi is not
-      while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        if (keys[mid * C] == key) lo = mid;
-        else hi = mid;
-      }
-      n = lo - chunk + 1;
-    }
-  }
-  const int64_t c0 = int64_t(blockIdx.y) * kJoinColumns + lane * 4, step = int64_t(gridDim.y) * kJoinColumns;
-  const auto part = [&](int64_t first, int64_t k, int64_t c) {
-    return *reinterpret_cast<const float4*>(a.parts + ((first + k) * 2 + (k == 0)) * a.part_pitch + c);
-  };
-  if (n > 0 && n <= kJoinAlone)
-    for (int64_t c = c0; c < a.D; c += step) {
-      float4 sum = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-      for (int64_t k = 0; k < n; ++k) add(sum, part(chunk, k, c));
-      write_four<G>(a, key, c, sum);
-    }
-  if (lane == 0) lengths[warp] = n > kJoinAlone ? n : 0;
-  __syncthreads();
-  for (int w = 0; w < kJoinWarps; ++w) {
-    n = lengths[w];
-    if (n == 0) continue;
-    key = keys[(chunk0 + w + 1) * C];
-    for (int64_t c = c0; c - lane * 4 < a.D; c += step) {
+  const uint32_t count = *a.long_count;
+  for (uint32_t i = blockIdx.x; i < count; i += gridDim.x) {
+    const LongRun run = a.long_runs[i];
+    const uint32_t key = a.sorted_keys[(run.chunk + 1) * a.chunk];
+    for (int64_t c0 = int64_t(blockIdx.y) * kJoinColumns; c0 < a.D; c0 += int64_t(gridDim.y) * kJoinColumns) {
+      const int64_t c = c0 + lane * 4;
       float4 sum = make_float4(0, 0, 0, 0);
       if (c < a.D) {
 #pragma unroll 8
-        for (int64_t k = warp; k < n; k += kJoinWarps) add(sum, part(chunk0 + w, k, c));
+        for (int64_t k = warp; k < run.parts; k += kLongWarps) add(sum, part_of(a, run.chunk, k, c));
       }
       __syncthreads();
       sums[warp][lane] = sum;
       __syncthreads();
       if (warp == 0 && c < a.D) {
-#pragma unroll
-        for (int i = 1; i < kJoinWarps; ++i) add(sum, sums[i][lane]);
+        for (int w = 1; w < kLongWarps; ++w) add(sum, sums[w][lane]);
         write_four<G>(a, key, c, sum);
       }
     }
@@ -529,7 +619,7 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Workspace: keys and positions twice, the bit map, the partial sums.
 struct Scratch {
-  size_t list, bits, parts, bytes;
+  size_t list, bits, runs, parts, bytes;
   int64_t part_pitch, chunks;
   int chunk;
 };
@@ -541,7 +631,8 @@ Scratch scratch_of(int64_t T, int64_t V, int64_t D) {
   s.chunk = chunk_of(T, D);
   s.chunks = (T + s.chunk - 1) / s.chunk;
   s.parts = up256(size_t(s.chunks) * 2 * size_t(s.part_pitch) * 4);
-  s.bytes = 4 * s.list + s.bits + s.parts + 256;
+  s.runs = up256(size_t(s.chunks / kAlone + 1) * sizeof(LongRun));
+  s.bytes = 4 * s.list + s.bits + s.parts + s.runs + 256;
   return s;
 }
 
@@ -559,6 +650,8 @@ cudaError_t launch_grad(const EmbeddingGrad& p, const DeviceInfo& dev) {
   }
   a.bits = reinterpret_cast<uint32_t*>(w + 4 * s.list);
   a.parts = reinterpret_cast<float*>(w + 4 * s.list + s.bits);
+  a.long_runs = reinterpret_cast<LongRun*>(w + 4 * s.list + s.bits + s.parts);
+  a.long_count = reinterpret_cast<uint32_t*>(w + 4 * s.list + s.bits + s.parts + s.runs);
   a.T = p.T;
   a.V = p.V;
   a.D = p.D;
@@ -581,6 +674,8 @@ cudaError_t launch_grad(const EmbeddingGrad& p, const DeviceInfo& dev) {
   const bool vec = a.fill_vec && on16({reinterpret_cast<uintptr_t>(a.dy), uintptr_t(a.dy_pitch), uintptr_t(p.D * D::kBytes)});
   a.units = int((p.D + D::kVec - 1) / D::kVec);
   a.slices = (a.units + kRowThreads - 1) / kRowThreads;
+  a.small = a.units <= 32;
+  a.groups = a.small ? (a.chunks + kRowThreads / 32 - 1) / (kRowThreads / 32) : a.chunks;
   a.fill_rows = (65536 + p.D * G::kBytes - 1) / (p.D * G::kBytes);
   const int64_t fill = p.accumulate ? 0 : (p.V + a.fill_rows - 1) / a.fill_rows;
   cudaError_t e;
@@ -591,17 +686,32 @@ cudaError_t launch_grad(const EmbeddingGrad& p, const DeviceInfo& dev) {
   } else {
     const size_t shared = (size_t(1) << a.digit_bits) * 35 * 4;
     if ((e = cudaFuncSetAttribute(k_sort_tokens, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared))) != cudaSuccess) return e;
-    k_sort_tokens<<<kSortCtas, kSortThreads, shared, p.stream>>>(a);
+    if ((e = cudaFuncSetAttribute(k_sort_tokens, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortCtas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = p.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSortCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, k_sort_tokens, a)) != cudaSuccess) return e;
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t ctas = a.chunks * a.slices + fill;
+  const int64_t ctas = a.groups * a.slices + fill;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (ctas > 0 && (e = launch_after(vec ? k_embedding_rows<D, G, false> : k_embedding_rows<D, G, true>, dim3(unsigned(ctas)), kRowThreads, p.stream, a)) != cudaSuccess)
     return e;
   if (a.chunks > 1) {
-    const int64_t columns = (p.D + kJoinColumns - 1) / kJoinColumns;
-    return launch_after(k_embedding_join<G>, dim3(unsigned((a.chunks + kJoinWarps - 1) / kJoinWarps), unsigned(columns < 32 ? columns : 32)), kJoinWarps * 32,
-                        p.stream, a);
+    const int64_t columns = (p.D + kJoinColumns - 1) / kJoinColumns, across = (a.chunks + kJoinWarps - 1) / kJoinWarps;
+    int64_t down = (int64_t(dev.sm_count) * 8 + across - 1) / across;  // a CTA's columns are as few as one round of CTAs allows
+    if (down > columns) down = columns;
+    if ((e = launch_after(k_embedding_join<G>, dim3(unsigned(across), unsigned(down)), kJoinWarps * 32, p.stream, a)) != cudaSuccess) return e;
+    if (a.chunks > kFewChunks)
+      return launch_after(k_embedding_long<G>, dim3(kLongCtas, unsigned(columns < 64 ? columns : 64)), kLongWarps * 32, p.stream, a);
   }
   return cudaSuccess;
 }
