@@ -34,6 +34,9 @@ int check_matrix(const void* p, int64_t* ld, int64_t M, int64_t N, int64_t bytes
   return aligned(p, uintptr_t(bytes)) ? SOFTMAX_OK : SOFTMAX_ERR_MISALIGNED;
 }
 
+// Whether two matrices that share their first element also share their pitch, as a call in place needs it.
+bool alike(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M) { return a != b || lda == ldb || M < 2; }
+
 bool finite(float v) { return std::isfinite(v); }
 
 int done(cudaError_t err) { return err == cudaSuccess ? SOFTMAX_OK : cuda_failure(err); }
@@ -56,7 +59,7 @@ int cross_entropy_rows_grad(const void* x, int64_t ldx, const int64_t* labels, c
   if ((st = check_matrix(x, &ldx, M, N, s)) != SOFTMAX_OK || (st = check_matrix(grad, &ldg, M, N, s)) != SOFTMAX_OK) return st;
   if (M == 0) return SOFTMAX_OK;
   if (!labels || !loss) return SOFTMAX_ERR_INVALID_ARG;
-  if (x == grad && ldx != ldg && M > 1) return SOFTMAX_ERR_INVALID_ARG;
+  if (!alike(x, ldx, grad, ldg, M)) return SOFTMAX_ERR_INVALID_ARG;
   if (!aligned(labels, 8) || !aligned(upstream, 4) || !aligned(loss, 4) || !aligned(lse_out, 4)) return SOFTMAX_ERR_MISALIGNED;
   const DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != SOFTMAX_OK) return st;
@@ -102,6 +105,11 @@ int rms_norm_rows(const rms_norm_args* args, int64_t M, int64_t N, int dtype, in
   if (M == 0) return SOFTMAX_OK;
   if (e4m3 && !a.scales) return SOFTMAX_ERR_INVALID_ARG;
   if (a.residual && a.y == a.sum_out) return SOFTMAX_ERR_INVALID_ARG;
+  if (e4m3 && (a.y == a.x || a.y == a.residual)) return SOFTMAX_ERR_INVALID_ARG;  // elements of another size
+  if (!alike(a.x, a.ldx, a.y, a.ldy, M) ||
+      (a.residual && (!alike(a.x, a.ldx, a.sum_out, a.ld_sum, M) || !alike(a.residual, a.ld_residual, a.sum_out, a.ld_sum, M) ||
+                      !alike(a.residual, a.ld_residual, a.y, a.ldy, M))))
+    return SOFTMAX_ERR_INVALID_ARG;
   if (!aligned(a.weight, a.weight_f32 ? 4 : uintptr_t(s)) || !aligned(a.scales, 4) || !aligned(a.rstd_out, 4)) return SOFTMAX_ERR_MISALIGNED;
   const DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != SOFTMAX_OK) return st;
@@ -136,6 +144,8 @@ int rms_norm_rows_backward(const rms_norm_grad_args* args, int64_t M, int64_t N,
     return st;
   if (M == 0 && (!a.dweight || a.accumulate)) return SOFTMAX_OK;
   if (M > 0 && !a.rstd) return SOFTMAX_ERR_INVALID_ARG;
+  if (!alike(a.dy, a.ld_dy, a.dx, a.ld_dx, M) || !alike(a.h, a.ldh, a.dx, a.ld_dx, M) || (a.sum_grad && !alike(a.sum_grad, a.ld_sum_grad, a.dx, a.ld_dx, M)))
+    return SOFTMAX_ERR_INVALID_ARG;
   if (!aligned(a.weight, a.weight_f32 ? 4 : uintptr_t(s)) || !aligned(a.rstd, 4) || !aligned(a.dweight, 4)) return SOFTMAX_ERR_MISALIGNED;
   const DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != SOFTMAX_OK) return st;

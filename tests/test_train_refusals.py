@@ -55,6 +55,9 @@ def test_norm_faults(lib):
     assert norm(lib=lib, residual=X, sum_out=X, ld_residual=3) == BAD and norm(lib=lib, residual=X, sum_out=X, ld_sum=3) == BAD
     assert norm(lib=lib, x=X + 1) == ODD and norm(lib=lib, weight=X + 1) == ODD and norm(lib=lib, weight=X + 2, weight_f32=1) == ODD
     assert norm(lib=lib, rstd_out=X + 2) == ODD and norm(lib=lib, out=1, scales=X + 2) == ODD and norm(lib=lib, residual=X + 1, sum_out=X) == ODD
+    assert norm(lib=lib, out=1, scales=X, y=X) == BAD and norm(lib=lib, out=1, scales=X, y=X + 64, residual=X + 64, sum_out=X) == BAD  # 8 bits over 16
+    assert norm(lib=lib, y=X, ldx=300) == BAD  # in place with two pitches
+    assert norm(lib=lib, residual=X + 64, sum_out=X, ldx=300) == BAD and norm(lib=lib, residual=X + 64, sum_out=X + 64, ld_sum=300) == BAD
     assert norm(lib=lib, M=0, x=None, y=None) == OK
 
 
@@ -71,6 +74,7 @@ def test_norm_grad_faults(lib):
     for ld in ("ld_dy", "ldh", "ld_dx"):
         assert call(**{ld: 100}) == BAD
     assert call(sum_grad=X, ld_sum_grad=100) == BAD
+    assert call(ldh=300) == BAD and call(dx=X + 64, sum_grad=X + 64, ld_dx=300) == BAD  # in place with two pitches
     assert call(offset=math.nan) == BAD and call(accumulate=2) == BAD and call(weight_f32=-1) == BAD
     assert call(M=0, dy=None, h=None, rstd=None, dx=None) == OK
     assert lib.rms_norm_backward_workspace(4, 0, 0) == -1 and lib.rms_norm_backward_workspace(4, 4, 5) == -1
