@@ -190,34 +190,34 @@ __global__ void __launch_bounds__(kThreads) k_rms_weight_grad(GradArgs a) {
 
 // ---- rows in registers ------------------------------------------------------------------------------------------------
 //
-// W warps own a row, K vectors a thread: those of a warp 32 W apart, or, with SHIFT, one run of 32 K (rows that start anywhere, of any
-// length: load_vectors, store_vectors); without, rows are on 16-byte boundaries.  The 128 elements that share a scale in 8 bits
-// lie in one warp.
+// W warps own a row, K vectors a thread; a warp's 32 K vectors lie together.  SHIFT: rows that start anywhere, of any length
+// (load_vectors, store_vectors); without, rows are on 16-byte boundaries.  The 128 elements that share a scale in 8 bits lie in
+// one warp.
 
-template <int K, int W, bool SHIFT>
+template <int K>
 __device__ __forceinline__ int unit_of(int t, int k) {
-  return SHIFT ? (t >> 5) * (32 * K) + k * 32 + (t & 31) : t + k * (32 * W);
+  return (t >> 5) * (32 * K) + k * 32 + (t & 31);
 }
-template <class D, int K, int W, bool SHIFT>
+template <class D, int K, bool SHIFT>
 __device__ __forceinline__ void take(const RowAt& r, int t, int units, uint4 (&q)[K]) {
   if constexpr (SHIFT) {
-    load_vectors<D>(r, unit_of<K, W, true>(t, 0), q);
+    load_vectors<D>(r, unit_of<K>(t, 0), q);
   } else {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = t + k * (32 * W);
+      const int u = unit_of<K>(t, k);
       q[k] = u < units ? ld_stream16(r.row + int64_t(u) * 16) : make_uint4(0, 0, 0, 0);
     }
   }
 }
-template <class D, int K, int W, bool SHIFT>
+template <class D, int K, bool SHIFT>
 __device__ __forceinline__ void put(unsigned char* row, int t, int units, int n, const uint4 (&q)[K]) {
   if constexpr (SHIFT) {
-    store_vectors<D>(row, unit_of<K, W, true>(t, 0), n, q);
+    store_vectors<D>(row, unit_of<K>(t, 0), n, q);
   } else {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = t + k * (32 * W);
+      const int u = unit_of<K>(t, k);
       if (u < units) st_stream16(row + int64_t(u) * 16, q[k]);
     }
   }
@@ -290,7 +290,7 @@ __device__ __forceinline__ void store_codes(unsigned char* row, int u, int left,
     for (int e = 0; e < E; ++e)
       if (e < left) p[e] = (unsigned char)(c[e / 2] >> (e & 1) * 8);
   } else if constexpr (E == 8) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(c[0] | uint32_t(c[1]) << 16, c[2] | uint32_t(c[3]) << 16);
+    asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(c[0] | uint32_t(c[1]) << 16), "r"(c[2] | uint32_t(c[3]) << 16) : "memory");
   } else {
     *reinterpret_cast<uint32_t*>(p) = c[0] | uint32_t(c[1]) << 16;
   }
@@ -298,8 +298,8 @@ __device__ __forceinline__ void store_codes(unsigned char* row, int u, int left,
 
 __host__ __device__ constexpr int reg_threads(int warps) { return warps * 32 > 256 ? warps * 32 : 256; }
 
-// CTAs of 256 threads an SM: in 8 bits three for 16-bit rows (16384 x 8192 bf16 with a residual 164 us; two 197, four 170), else
-// four (into e4m3 16384 x 4096 fp32 with a residual 150 us, three 181; 16384 x 8192 bf16 84 us, three 93, six 91).
+// CTAs of 256 threads an SM: in 8 bits three for 16-bit rows (16384 x 4096 bf16 with a residual 74 us; two 101, four 97), else
+// four (16384 x 8192 bf16 84 us, three 93, six 91).
 template <class D, int K, int W, bool SHIFT, bool E4M3>
 __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes == 2 ? 3 : 4) * 256 / reg_threads(W)) k_rms_norm(NormArgs a) {
   constexpr int E = D::kVec, GT = W * 32, G = reg_threads(W) / GT;
@@ -314,12 +314,12 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
   for (int64_t row = int64_t(blockIdx.x) * G + group; row < a.M; row += int64_t(gridDim.x) * G, it ^= 1) {
     const RowAt xr = row_at<D>(a.x + row * a.x_pitch, n, xm);
     uint4 h[K];
-    take<D, K, W, SHIFT>(xr, t, units, h);
+    take<D, K, SHIFT>(xr, t, units, h);
     if (a.r) {
       const RowAt rr = row_at<D>(a.r + row * a.r_pitch, n, rm);
       unsigned char* to = a.h + row * a.h_pitch;
       uint4 r[K];
-      take<D, K, W, SHIFT>(rr, t, units, r);
+      take<D, K, SHIFT>(rr, t, units, r);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         float v[E], w[E];
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
         for (int e = 0; e < E; ++e) v[e] += w[e];
         h[k] = D::pack(v);
       }
-      put<D, K, W, SHIFT>(to, t, units, n, h);
+      put<D, K, SHIFT>(to, t, units, n, h);
     }
     float sum = 0.f;
 #pragma unroll
@@ -342,14 +342,14 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
     uint4 wq[K];  // the weights as they are, under way while the sum is joined (in 8 bits: 164 us against 198)
     if (PACKED && packed) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) wq[k] = __ldg(static_cast<const uint4*>(a.w) + min(t + k * GT, units - 1));
+      for (int k = 0; k < K; ++k) wq[k] = __ldg(static_cast<const uint4*>(a.w) + min(unit_of<K>(t, k), units - 1));
     }
     sum = group_sum<W>(sum, sums[it] + group * W, group, t);
     const float rstd = 1.f / sqrtf(sum / float(a.N) + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     unsigned char* yr = a.y + row * a.y_pitch;
     const auto value = [&](int k, float(&v)[E]) {  // y in 32 bits, 0 behind the row's end
-      const int u = unit_of<K, W, SHIFT>(t, k);
+      const int u = unit_of<K>(t, k);
       float w[E];
       D::unpack(h[k], v);
       if (PACKED && packed) {
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
         value(k, v);
         h[k] = D::pack(v);
       }
-      put<D, K, W, SHIFT>(yr, t, units, n, h);
+      put<D, K, SHIFT>(yr, t, units, n, h);
     } else {
       const auto top_of = [&](const float(&v)[E]) {
         float m = fabsf(v[0]);
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
         return m;
       };
       const auto store = [&](int k, const float(&v)[E], float inv) {
-        const int u = unit_of<K, W, SHIFT>(t, k);
+        const int u = unit_of<K>(t, k);
         if (u < units) store_codes<E, SHIFT>(yr, u, n - u * E, v, inv);
       };
       if (a.groups == 1 && a.N > kGroup) {
@@ -394,7 +394,8 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
 #pragma unroll
         for (int k = 0; k < K; ++k) store(k, y[k], inv);
       } else {
-        constexpr int lanes = kGroup / E;  // of a group
+        constexpr int lanes = kGroup / E, per = 32 / lanes;  // of a group; groups of a warp's 32 vectors
+        float mine = 0.f;  // lane i: scale i of the warp's
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           float y[E];
@@ -403,10 +404,13 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
 #pragma unroll
           for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
           const float scale = scale_of(top), inv = __fdividef(1.f, scale);
-          const int u = unit_of<K, W, SHIFT>(t, k);
-          if (u < units && (lane & (lanes - 1)) == 0) a.scales[row * a.groups + u / lanes] = scale;
+          const float theirs = __shfl_sync(~0u, scale, (lane & (per - 1)) * lanes);
+          if (lane / per == k) mine = theirs;
           store(k, y, inv);
         }
+        // one store for the warp's groups, which lie together: by twos, as they came, 16384 x 8192 took 163 us instead of 144
+        const int g = unit_of<K>(t - lane, 0) / lanes + lane;
+        if (lane < K * per && g < a.groups) a.scales[row * a.groups + g] = mine;
       }
     }
   }
@@ -427,10 +431,10 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
   for (int64_t row = int64_t(blockIdx.x) * G + group; row < a.M; row += step, it ^= 1) {
     uint4 dy[K], h[K], sg[K];
     const RowAt dr = row_at<D>(a.dy + row * a.dy_pitch, n, dm), hr = row_at<D>(a.h + row * a.h_pitch, n, hm), gr = row_at<D>(a.sg + row * a.sg_pitch, n, gm);
-    take<D, K, W, SHIFT>(dr, t, units, dy);
-    take<D, K, W, SHIFT>(hr, t, units, h);
+    take<D, K, SHIFT>(dr, t, units, dy);
+    take<D, K, SHIFT>(hr, t, units, h);
     if (a.sg) {
-      take<D, K, W, SHIFT>(gr, t, units, sg);
+      take<D, K, SHIFT>(gr, t, units, sg);
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k) sg[k] = make_uint4(0, 0, 0, 0);
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = unit_of<K, W, SHIFT>(t, k);
+      const int u = unit_of<K>(t, k);
       if (u >= units) continue;
       float d[E], x[E], w[E];
       D::unpack(dy[k], d);
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
     unsigned char* to = a.dx + row * a.dx_pitch;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = unit_of<K, W, SHIFT>(t, k);
+      const int u = unit_of<K>(t, k);
       float d[E], x[E], w[E] = {}, s[E];
       D::unpack(dy[k], d);
       D::unpack(h[k], x);
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
       for (int e = 0; e < E; ++e) d[e] = __fmaf_rn(rstd, d[e] * w[e], __fmaf_rn(slope, x[e], s[e]));
       dy[k] = D::pack(d);
     }
-    put<D, K, W, SHIFT>(to, t, units, n, dy);
+    put<D, K, SHIFT>(to, t, units, n, dy);
   }
   griddep_launch();
   if (!a.dw) return;
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
     if (group == g) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int u = unit_of<K, W, SHIFT>(t, k);
+        const int u = unit_of<K>(t, k);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           float* c = columns + (G > 1 ? (k * E + e) * GT + t : 0);
@@ -711,7 +715,7 @@ template <class D>
 cudaError_t launch_norm_type(const RmsNorm& p, const NormArgs& a, const DeviceInfo& dev) {
   // at most 64 elements a thread
   static const NormConfig aligned[] = {norm_cfg<D, 1, 1, false>(), norm_cfg<D, 2, 1, false>(), norm_cfg<D, 4, 1, false>(), norm_cfg<D, 4, 2, false>(),
-                                       norm_cfg<D, 4, 4, false>(), norm_cfg<D, 4, 8, false>(), norm_cfg<D, 4, 16, false>(), norm_cfg<D, 8, 16, false>()};
+                                       norm_cfg<D, 3, 4, false>(), norm_cfg<D, 4, 4, false>(), norm_cfg<D, 3, 8, false>(), norm_cfg<D, 4, 8, false>(), norm_cfg<D, 4, 16, false>(), norm_cfg<D, 8, 16, false>()};
   static const NormConfig anywhere[] = {norm_cfg<D, 1, 1, true>(), norm_cfg<D, 4, 1, true>(), norm_cfg<D, 4, 4, true>(), norm_cfg<D, 4, 8, true>(),
                                         norm_cfg<D, 4, 16, true>(), norm_cfg<D, 8, 16, true>()};
   const bool e4m3 = p.out == RMS_NORM_OUT_E4M3;
