@@ -400,8 +400,9 @@ int logits_process_rows(const logits_rows* a, int64_t M, int64_t N, int dtype, i
  *
  * Rows lie at pitches (ld..., in elements, >= N, 0: N).  Every pointer is aligned to its elements (else
  * SOFTMAX_ERR_MISALIGNED); any length and pitch is taken, and runs faster where rows start on 16-byte
- * boundaries.  Sums are held in fp32, added up in an order that the sizes alone fix: the same call gives the same
- * bits.  Each workspace is device memory, 256-byte aligned, that no other call uses until this one is done
+ * boundaries.  Sums are held in fp32, added up in an order that the sizes, pitches, alignments and tokens fix: the same
+ * call gives the same bits.  A matrix that a call writes in place of another has that one's pitch (else
+ * SOFTMAX_ERR_INVALID_ARG); other overlaps are undefined.  Each workspace is device memory, 256-byte aligned, that no other call uses until this one is done
  * (calls that may run at the same time, captured graphs among them, need one each); nothing in it is kept from
  * call to call.  A count of rows, tokens or tensors of 0 is a no-op unless an output is left to be written.
  */
@@ -436,7 +437,7 @@ int cross_entropy_rows_grad(const void* x, int64_t ldx, const int64_t* labels, c
  *   weight      -- [N], dtype elements or fp32 (weight_f32 = 1), or NULL for 1 - offset.
  *   eps         -- finite, >= 0.   offset -- finite (1 where weights are kept as their difference from 1).
  *   y           -- out = RMS_NORM_OUT_SAME: dtype elements.  May be x, or residual, where sum_out is not.
- *                  out = RMS_NORM_OUT_E4M3: 8-bit floats (e4m3, largest 448), with fp32 scales: the value is
+ *                  out = RMS_NORM_OUT_E4M3 (y a matrix of its own): 8-bit floats (e4m3, largest 448), with fp32 scales: the value is
  *                  code * scale, scale = max(max |y| / 448, 2^-126) over a group, code = y * (1 / scale) rounded to
  *                  the nearest (ties to even).
  *   scales      -- e4m3 only: [M][groups], groups = 1 for group = 0 (a scale for each row), else ceil(N / group).

@@ -1,19 +1,23 @@
-// kernel_loss_grad.cu -- the cross-entropy loss and its gradient (loss_grad.cuh): short rows in registers, two passes
+// kernel_loss_grad.cu -- the cross-entropy loss and its gradient (loss_grad.cuh): rows of up to 64 KiB in registers, two passes
 // for rows that are too long for a cluster, and the choice.
 #include "loss_grad.cuh"
 
 namespace rwo {
 namespace {
 
-// ---- short rows: W warps a row, the row in registers ------------------------------------------------------------------
+// ---- rows of up to 64 KiB: W warps a row, the row in registers --------------------------------------------------------
+//
+// Loaded once as packed vectors, 64 registers a thread, CTAs beside each other hide the waits.  Measured (bf16; in clusters with the next
+// row's copy under way): rows of 16 KiB 324 us a 2 GiB launch (468), of 32 KiB 157 us a GiB (181), of 64 KiB 318 us (328), and 4.1
+// us for 16 rows of 64 KiB (5.6).
 
-constexpr int kRegThreads = 256;
+__host__ __device__ constexpr int reg_threads(int warps) { return warps * 32 > 256 ? warps * 32 : 256; }
 
 // VEC: 16-byte vectors, K a thread; else K single elements.
 template <class D, int K, int W, bool VEC, bool SMOOTH>
-__global__ void __launch_bounds__(kRegThreads) k_loss_grad_reg(LossArgs a) {
-  constexpr int E = VEC ? D::kVec : 1, GT = W * 32, G = kRegThreads / GT;
-  __shared__ Fold parts[2][kRegThreads / 32];
+__global__ void __launch_bounds__(reg_threads(W), 1024 / reg_threads(W)) k_loss_grad_reg(LossArgs a) {
+  constexpr int E = VEC ? D::kVec : 1, GT = W * 32, G = reg_threads(W) / GT;
+  __shared__ Fold parts[2][reg_threads(W) / 32];
   const int group = threadIdx.x / GT, t = threadIdx.x % GT, lane = threadIdx.x & 31, warp = t >> 5;
   const int units = int(a.N / E);
   int it = 0;
@@ -161,18 +165,19 @@ constexpr RegConfig reg() {
 
 template <class D>
 cudaError_t launch_type(const LossGrad& p, const LossArgs& a, const DeviceInfo& dev) {
-  static const RegConfig vectors[] = {reg<D, 1, 1, true>(), reg<D, 2, 1, true>(), reg<D, 4, 1, true>(), reg<D, 4, 2, true>(), reg<D, 4, 4, true>(), reg<D, 4, 8, true>()};
+  static const RegConfig vectors[] = {reg<D, 1, 1, true>(), reg<D, 2, 1, true>(), reg<D, 4, 1, true>(), reg<D, 4, 2, true>(), reg<D, 4, 4, true>(), reg<D, 4, 8, true>(), reg<D, 8, 8, true>(), reg<D, 8, 16, true>()};
   static const RegConfig elements[] = {reg<D, 2, 1, false>(), reg<D, 8, 1, false>(), reg<D, 8, 4, false>()};
   const bool smooth = p.smoothing > 0.f;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.g) | uintptr_t(a.x_pitch) | uintptr_t(a.g_pitch) |
                      uintptr_t(p.N * D::kBytes)) & 15) == 0;
   const int64_t units = vec ? p.N / D::kVec : p.N;
   const RegConfig* tab = vec ? vectors : elements;
-  for (int i = 0; i < (vec ? 6 : 3); ++i) {
+  for (int i = 0; i < (vec ? 8 : 3); ++i) {
     if (units > tab[i].units) continue;
-    const int64_t groups = kRegThreads / 32 / tab[i].warps, ctas = (p.M + groups - 1) / groups;
-    const int64_t slots = int64_t(dev.sm_count) * (dev.max_threads_per_sm / kRegThreads) * 4;
-    tab[i].fn[smooth]<<<unsigned(ctas < slots ? ctas : slots), kRegThreads, 0, p.stream>>>(a);
+    const int threads = reg_threads(tab[i].warps);
+    const int64_t groups = threads / 32 / tab[i].warps, ctas = (p.M + groups - 1) / groups;
+    const int64_t slots = int64_t(dev.sm_count) * (dev.max_threads_per_sm / threads) * 4;
+    tab[i].fn[smooth]<<<unsigned(ctas < slots ? ctas : slots), threads, 0, p.stream>>>(a);
     return cudaGetLastError();
   }
   if (loss_grad_cluster_fits(p)) return launch_loss_grad_cluster(p, a, dev);
