@@ -506,6 +506,7 @@ int64_t rms_norm_backward_workspace(int64_t M, int64_t N, int dtype);
  *   tokens -- int32 (token_bytes = 4) or int64 (8), [T].  A negative token is padding: its row is 0.  A token >= V
  *             gives a row of NaN, is not followed, and softmax_get_status returns SOFTMAX_ERR_INVALID_ARG.
  *   scale  -- finite; the product is rounded once.
+ * D up to 2^30 (else SOFTMAX_ERR_UNSUPPORTED), here and in the backward pass.
  */
 int embedding_rows(const void* table, int64_t ld_table, const void* tokens, int token_bytes, void* y, int64_t ldy,
                    int64_t T, int64_t V, int64_t D, float scale, int dtype, void* stream);

@@ -10,6 +10,7 @@ namespace {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 constexpr int64_t kMaxLength = (int64_t(1) << 31) - 256;  // a row's length is 32-bit in the kernels
+constexpr int64_t kMaxDim = int64_t(1) << 30;  // of an embedding: vectors behind a row's end are counted in 32 bits too
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxVocab = (int64_t(1) << 31) - 2;
 constexpr int64_t kMaxTensors = int64_t(1) << 20;
@@ -174,6 +175,7 @@ int embedding_rows(const void* table, int64_t ld_table, const void* tokens, int 
   if (st == SOFTMAX_OK) st = check_tokens(tokens, token_bytes, T, V);
   if (st != SOFTMAX_OK) return st;
   if (!finite(scale)) return SOFTMAX_ERR_INVALID_ARG;
+  if (D > kMaxDim) return SOFTMAX_ERR_UNSUPPORTED;
   const int64_t s = elem_bytes(dtype);
   if ((st = check_matrix(table, &ld_table, T > 0 ? V : 0, D, s)) != SOFTMAX_OK || (st = check_matrix(y, &ldy, T, D, s)) != SOFTMAX_OK) return st;
   if (T == 0) return SOFTMAX_OK;
@@ -197,7 +199,7 @@ int embedding_rows(const void* table, int64_t ld_table, const void* tokens, int 
 
 static int check_embedding_grad(int64_t T, int64_t V, int64_t D) {
   if (T < 0 || V < 1 || D < 1) return SOFTMAX_ERR_INVALID_ARG;
-  return T > kMaxTokens || V > kMaxVocab || D > kMaxLength || (T > 0 && D > INT64_MAX / 16 / T) ? SOFTMAX_ERR_UNSUPPORTED : SOFTMAX_OK;
+  return T > kMaxTokens || V > kMaxVocab || D > kMaxDim || (T > 0 && D > INT64_MAX / 16 / T) ? SOFTMAX_ERR_UNSUPPORTED : SOFTMAX_OK;
 }
 
 int64_t embedding_backward_workspace(int64_t T, int64_t V, int64_t D) {

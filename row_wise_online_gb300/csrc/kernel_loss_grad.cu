@@ -166,13 +166,15 @@ constexpr RegConfig reg() {
 template <class D>
 cudaError_t launch_type(const LossGrad& p, const LossArgs& a, const DeviceInfo& dev) {
   static const RegConfig vectors[] = {reg<D, 1, 1, true>(), reg<D, 2, 1, true>(), reg<D, 4, 1, true>(), reg<D, 4, 2, true>(), reg<D, 4, 4, true>(), reg<D, 4, 8, true>(), reg<D, 8, 8, true>(), reg<D, 8, 16, true>()};
-  static const RegConfig elements[] = {reg<D, 2, 1, false>(), reg<D, 8, 1, false>(), reg<D, 8, 4, false>()};
+  static const RegConfig elements[] = {reg<D, 2, 1, false>(), reg<D, 8, 1, false>(), reg<D, 8, 4, false>(), reg<D, 16, 4, false>(), reg<D, 16, 8, false>(), reg<D, 32, 8, false>()};
   const bool smooth = p.smoothing > 0.f;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.g) | uintptr_t(a.x_pitch) | uintptr_t(a.g_pitch) |
                      uintptr_t(p.N * D::kBytes)) & 15) == 0;
   const int64_t units = vec ? p.N / D::kVec : p.N;
   const RegConfig* tab = vec ? vectors : elements;
-  for (int i = 0; i < (vec ? 8 : 3); ++i) {
+  // rows on no boundary by single elements: up to 4096, in 32 bits 8192 (clusters in their place: 20000 rows of 3001 bf16 139 us
+  // against 111, 10000 of 7999 fp32 109 against 98; but 10000 of 8001 bf16 82 against 117)
+  for (int i = 0; i < (vec ? 8 : D::kBytes == 4 ? 6 : 5); ++i) {
     if (units > tab[i].units) continue;
     const int threads = reg_threads(tab[i].warps);
     const int64_t groups = threads / 32 / tab[i].warps, ctas = (p.M + groups - 1) / groups;

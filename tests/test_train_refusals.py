@@ -87,14 +87,14 @@ def test_embedding_faults(lib):
     assert look(T=-1) == BAD and look(V=0) == BAD and look(D=0) == BAD and look(kb=2) == BAD and look(dt=3) == BAD and look(scale=math.inf) == BAD
     assert look(table=None) == BAD and look(tok=None) == BAD and look(y=None) == BAD and look(ldt=63) == BAD and look(ldy=63) == BAD
     assert look(tok=X + 4) == ODD and look(tok=X + 2, kb=4) == ODD and look(table=X + 1) == ODD and look(y=X + 1) == ODD
-    assert look(T=0, table=None, tok=None, y=None) == OK
+    assert look(T=0, table=None, tok=None, y=None) == OK and look(D=2 ** 30 + 1) == NO
 
     def grad(dy=X, ldd=0, tok=X, kb=8, g=X, ldg=0, T=4, V=10, D=64, scale=1.0, acc=0, dt=1, gdt=0, ws=X, n=2 ** 40):
         return lib.embedding_rows_backward(dy, ldd, tok, kb, g, ldg, T, V, D, scale, acc, dt, gdt, ws, n, None)
 
     assert grad(T=-1) == BAD and grad(V=0) == BAD and grad(D=0) == BAD and grad(kb=1) == BAD and grad(dt=3) == BAD and grad(gdt=3) == BAD
     assert grad(dt=1, gdt=2) == NO and grad(dt=0, gdt=1) == NO and grad(scale=math.nan) == BAD and grad(acc=2) == BAD
-    assert grad(T=2 ** 24 + 1) == NO and grad(V=2 ** 31 - 1) == NO
+    assert grad(T=2 ** 24 + 1) == NO and grad(V=2 ** 31 - 1) == NO and grad(D=2 ** 30 + 1) == NO
     assert grad(dy=None) == BAD and grad(tok=None) == BAD and grad(g=None) == BAD and grad(ldd=63) == BAD and grad(ldg=63) == BAD
     assert grad(ws=None) == BAD and grad(n=10) == BAD and grad(ws=X + 128) == ODD
     assert grad(dy=X + 1) == ODD and grad(g=X + 2) == ODD and grad(tok=X + 4) == ODD
