@@ -498,17 +498,44 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
 // next, copied by cp.async.bulk, and is read twice.  The copies of up to kMostSlots turns are under way while one is worked on,
 // whatever the registers leave of the SM's warps: 16384 x 4096 bf16 takes 88 us, with the rows in registers 103 (at the best
 // number of CTAs an SM).  Arithmetic in pairs of fp32: with single operations, 104 us.
+// LINES: rows on no boundary, which start at the same place of their 16-byte lines in all matrices.  That place comes again
+// after 16 bytes' worth of rows, and a CTA's turns are a multiple of those apart: it is one for all rows of a group, so lines are
+// worked on where they are, with the weights and the sums of dw moved instead (16384 x 5003 bf16 153 us; vectors shifted out of the
+// slots' lines 237, out of lines in registers 387).
 constexpr int kMostSlots = 4;
 
 struct RingArgs {
   GradArgs g;
   int slots;  // at least 2
-  uint32_t row_bytes, slot_bytes;
+  uint32_t row_bytes, slot_row, slot_bytes;  // slot_row: from row to row of a slot
   unsigned* status;
   uint64_t wait_ns;
 };
 
-template <class D, int K, int W>
+// A lane's row with LINES: the 16-byte lines that it has a part in, to their places from `to` on.  Where not all of them lie inside
+// the matrix, the first and the last one's elements are read by themselves.  Returns the bytes to copy, and what from.
+template <class D>
+__device__ __forceinline__ uint32_t edges(const RowAt& r, uint32_t& to, const unsigned char*& from) {
+  const unsigned char* end = r.end + (-reinterpret_cast<uintptr_t>(r.end) & 15);
+  from = r.row - r.delta;
+  if (!r.inside) {
+    sts16(to, load_elements<D>(from, r.row, r.end));
+    if (end - from > 16) sts16(to + uint32_t(end - from) - 16, load_elements<D>(end - 16, r.row, r.end));
+    from += 16, to += 16, end -= 16;
+  }
+  return end > from ? uint32_t(end - from) : 0;
+}
+
+// Vector u of a row in a slot, whose elements are the from-th to the end-th of its lines; 0 around them.
+template <class D, bool LINES>
+__device__ __forceinline__ uint4 slot_vector(uint32_t row, int u, int from, int end) {
+  const uint4 q = lds16(row + u * 16);
+  if constexpr (!LINES) return q;
+  const int b = u * D::kVec;
+  return b < from || b + D::kVec > end ? keep<D>(q, from - b, end - b, 0) : q;
+}
+
+template <class D, int K, int W, bool LINES>
 __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_grad_ring(RingArgs r) {
   constexpr int E = D::kVec, GT = W * 32, G = reg_threads(W) / GT;
   extern __shared__ __align__(128) unsigned char shared[];
@@ -516,7 +543,10 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
   __shared__ float sums[2][reg_threads(W) / 32];
   const GradArgs& a = r.g;
   const int tid = threadIdx.x, group = tid / GT, t = tid % GT;
-  const int units = int(a.N / E);
+  const int n = int(a.N);
+  int64_t row = int64_t(blockIdx.x) * G + group;
+  const int from = LINES ? int(reinterpret_cast<uintptr_t>(a.dy + row * a.dy_pitch) & 15) / D::kBytes : 0, end = from + n, units = (end + E - 1) / E;
+  const Bytes dm = bytes_of(a.dy, a.M, a.dy_pitch, r.row_bytes), hm = bytes_of(a.h, a.M, a.h_pitch, r.row_bytes), gm = bytes_of(a.sg, a.M, a.sg_pitch, r.row_bytes);
   const int64_t turns = (a.M + G - 1) / G, mine = turns > blockIdx.x ? (turns - 1 - blockIdx.x) / gridDim.x + 1 : 0;
   const uint64_t policy = policy_evict_first();
   bool timed_out = false;
@@ -526,15 +556,21 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
     const int64_t row0 = (blockIdx.x + i * gridDim.x) * G;
     const int rows = int(a.M - row0 < G ? a.M - row0 : G);
     const uint32_t bar = smem_addr(&full[s]), slot = smem_addr(shared) + s * r.slot_bytes;
-    if (tid == 0) mbar_arrive_expect_tx(bar, uint32_t(rows * arrays) * r.row_bytes);
-    __syncwarp();
-    if (tid < rows * arrays) {
-      const int which = tid / rows, row = tid % rows;
-      const unsigned char* from = which == 0   ? a.dy + (row0 + row) * a.dy_pitch
-                                  : which == 1 ? a.h + (row0 + row) * a.h_pitch
-                                               : a.sg + (row0 + row) * a.sg_pitch;
-      bulk_g2s(slot + uint32_t(which * G + row) * r.row_bytes, from, r.row_bytes, bar, policy);
+    const int which = tid / rows, row = tid % rows;
+    const unsigned char* at = which == 0   ? a.dy + (row0 + row) * a.dy_pitch
+                              : which == 1 ? a.h + (row0 + row) * a.h_pitch
+                                           : a.sg + (row0 + row) * a.sg_pitch;
+    uint32_t to = slot + uint32_t(which * G + row) * r.slot_row, bytes = r.row_bytes, all = uint32_t(rows * arrays) * r.row_bytes;
+    if constexpr (LINES) {
+      bytes = 0;
+      if (tid < rows * arrays) bytes = edges<D>(row_at<D>(at, n, which == 0 ? dm : which == 1 ? hm : gm), to, at);
+      all = __reduce_add_sync(~0u, bytes);
+      fence_proxy_async_smem();  // elements stored here, now or in an earlier turn, before what is copied over them
+      __syncwarp();              // and before the arrival
     }
+    if (tid == 0) mbar_arrive_expect_tx(bar, all);
+    __syncwarp();
+    if (tid < rows * arrays && bytes > 0) bulk_g2s(to, at, bytes, bar, policy);
   };
   if (tid == 0) {
     for (int s = 0; s < r.slots; ++s) mbar_init(smem_addr(&full[s]), 1);
@@ -547,11 +583,16 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float f[E] = {};
-    if (t + k * GT < units) weights<D, false>(a, t + k * GT, f);
+    const int u = t + k * GT;
+    if constexpr (LINES) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = u * E + e >= from && u * E + e < end ? weight1<D>(a, u * E + e - from) : 0.f;
+    } else {
+      if (u < units) weights<D, false>(a, u, f);
+    }
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) w[k][e] = make_float2(f[2 * e], f[2 * e + 1]), dw[k][e] = make_float2(0.f, 0.f);
   }
-  int64_t row = int64_t(blockIdx.x) * G + group;
   const int64_t step = int64_t(gridDim.x) * G;
   float next_rstd = row < a.M ? a.rstd[row] : 0.f;
   int s = 0;
@@ -559,7 +600,7 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
   for (int64_t i = 0; i < mine; ++i, row += step) {
     const float rstd = next_rstd;
     if (row + step < a.M) next_rstd = a.rstd[row + step];
-    const uint32_t dys = smem_addr(shared) + s * r.slot_bytes + group * r.row_bytes, hs = dys + G * r.row_bytes, sgs = hs + G * r.row_bytes;
+    const uint32_t dys = smem_addr(shared) + s * r.slot_bytes + group * r.slot_row, hs = dys + G * r.slot_row, sgs = hs + G * r.slot_row;
     const bool on = row < a.M;
     if (!mbar_wait(smem_addr(&full[s]), parity, r.wait_ns)) timed_out = true;
     const float2 rstd2 = make_float2(rstd, rstd);
@@ -570,8 +611,8 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
         const int u = t + k * GT;
         if (u >= units) continue;
         float2 d[E / 2], x[E / 2];
-        D::unpack2(lds16(dys + u * 16), d);
-        D::unpack2(lds16(hs + u * 16), x);
+        D::unpack2(slot_vector<D, LINES>(dys, u, from, end), d);
+        D::unpack2(slot_vector<D, LINES>(hs, u, from, end), x);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
           const float2 p = __fmul2_rn(d[e], x[e]);
@@ -596,18 +637,20 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
     if (on) {
       const float slope = -(rstd * rstd * rstd) * (sum / float(a.N));  // dx = rstd g + slope h + sum_grad
       const float2 slope2 = make_float2(slope, slope);
-      unsigned char* to = a.dx + row * a.dx_pitch;
+      unsigned char* to = a.dx + row * a.dx_pitch - from * D::kBytes;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int u = t + k * GT;
         if (u >= units) continue;
         float2 d[E / 2], x[E / 2], g[E / 2] = {};
-        D::unpack2(lds16(dys + u * 16), d);
-        D::unpack2(lds16(hs + u * 16), x);
-        if (a.sg) D::unpack2(lds16(sgs + u * 16), g);
+        D::unpack2(slot_vector<D, LINES>(dys, u, from, end), d);
+        D::unpack2(slot_vector<D, LINES>(hs, u, from, end), x);
+        if (a.sg) D::unpack2(slot_vector<D, LINES>(sgs, u, from, end), g);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) d[e] = __ffma2_rn(__fmul2_rn(d[e], w[k][e]), rstd2, __ffma2_rn(x[e], slope2, g[e]));
-        st_stream16(to + int64_t(u) * 16, D::pack2(d));
+        const int first = from - u * E, last = end - u * E;
+        if (LINES && (first > 0 || last < E)) store_elements<D>(to + int64_t(u) * 16, D::pack2(d), first, last);
+        else st_stream16(to + int64_t(u) * 16, D::pack2(d));
       }
     }
     if (++s == r.slots) {
@@ -628,12 +671,22 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
       for (int k = 0; k < K; ++k) {
         const int u = t + k * GT;
         if (u >= units) continue;
+        if constexpr (LINES) {  // the groups' rows start elsewhere in their lines
 #pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          float4 v = make_float4(dw[k][e / 2].x, dw[k][e / 2].y, dw[k][e / 2 + 1].x, dw[k][e / 2 + 1].y);
-          float4* c = reinterpret_cast<float4*>(columns + u * E + e);
-          if (g) v.x += c->x, v.y += c->y, v.z += c->z, v.w += c->w;
-          *(g == G - 1 ? reinterpret_cast<float4*>(part + u * E + e) : c) = v;
+          for (int e = 0; e < E; ++e) {
+            const int i = u * E + e - from;
+            if (i < 0 || i >= n) continue;
+            const float v = (e & 1 ? dw[k][e / 2].y : dw[k][e / 2].x) + (g ? columns[i] : 0.f);
+            (g == G - 1 ? part : columns)[i] = v;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 4) {
+            float4 v = make_float4(dw[k][e / 2].x, dw[k][e / 2].y, dw[k][e / 2 + 1].x, dw[k][e / 2 + 1].y);
+            float4* c = reinterpret_cast<float4*>(columns + u * E + e);
+            if (g) v.x += c->x, v.y += c->y, v.z += c->z, v.w += c->w;
+            *(g == G - 1 ? reinterpret_cast<float4*>(part + u * E + e) : c) = v;
+          }
         }
       }
     }
@@ -683,9 +736,9 @@ struct RingConfig {
   int warps, units;
   void (*fn)(RingArgs);
 };
-template <class D, int K, int W>
+template <class D, int K, int W, bool LINES>
 constexpr RingConfig ring_cfg() {
-  return RingConfig{W, 32 * W * K, k_rms_grad_ring<D, K, W>};
+  return RingConfig{W, 32 * W * K, k_rms_grad_ring<D, K, W, LINES>};
 }
 
 // The first configuration that holds a row.
@@ -743,21 +796,27 @@ template <class D>
 cudaError_t launch_grad_type(const RmsNormGrad& p, GradArgs a, const DeviceInfo& dev) {
   // at most 32 elements a thread, whose sums of dw stay in registers
   constexpr int F = D::kBytes / 2;  // fp32 vectors have half the elements
-  static const RingConfig rings[] = {ring_cfg<D, F, 1>(), ring_cfg<D, 2 * F, 1>(), ring_cfg<D, 4 * F, 1>(), ring_cfg<D, 4 * F, 2>(),
-                                     ring_cfg<D, 2 * F, 8>(), ring_cfg<D, 4 * F, 8>(), ring_cfg<D, 4 * F, 16>()};
+  static const RingConfig rings[] = {ring_cfg<D, F, 1, false>(), ring_cfg<D, 2 * F, 1, false>(), ring_cfg<D, 4 * F, 1, false>(), ring_cfg<D, 4 * F, 2, false>(),
+                                     ring_cfg<D, 2 * F, 8, false>(), ring_cfg<D, 4 * F, 8, false>(), ring_cfg<D, 4 * F, 16, false>()};
+  static const RingConfig lined[] = {ring_cfg<D, F, 1, true>(), ring_cfg<D, 2 * F, 1, true>(), ring_cfg<D, 4 * F, 1, true>(), ring_cfg<D, 4 * F, 2, true>(),
+                                      ring_cfg<D, 2 * F, 8, true>(), ring_cfg<D, 4 * F, 8, true>(), ring_cfg<D, 4 * F, 16, true>()};
   static const GradConfig aligned[] = {grad_cfg<D, 4 * F, 16, false>()};  // two slots of such rows may not fit an SM
   static const GradConfig anywhere[] = {grad_cfg<D, F, 1, true>(), grad_cfg<D, 2 * F, 2, true>(), grad_cfg<D, 2 * F, 8, true>(), grad_cfg<D, 4 * F, 8, true>(),
                                         grad_cfg<D, 4 * F, 16, true>()};
   const bool vec = on16({bits(a.dy), bits(a.h), bits(a.sg), bits(a.dx), bits(static_cast<const char*>(a.w)), uintptr_t(a.dy_pitch), uintptr_t(a.h_pitch),
                          a.sg ? uintptr_t(a.sg_pitch) : 0, uintptr_t(a.dx_pitch), uintptr_t(p.N * D::kBytes)});
   const int64_t units = (p.N + D::kVec - 1) / D::kVec;
-  const RingConfig* ring = vec ? pick(rings, units) : nullptr;
+  // all rows of a number start at the same place of their 16-byte lines
+  const auto same = [&](const unsigned char* q, int64_t pitch) { return ((bits(q) ^ bits(a.dy)) & 15) == 0 && ((pitch ^ a.dy_pitch) & 15) == 0; };
+  const bool lines = same(a.h, a.h_pitch) && (!a.sg || same(a.sg, a.sg_pitch)) && same(a.dx, a.dx_pitch);
+  const RingConfig* ring = vec ? pick(rings, units) : lines ? pick(lined, (p.N + 2 * D::kVec - 2) / D::kVec) : nullptr;
   RingArgs r;
   int ring_ctas = 0, shared = 0;  // of an SM
   if (ring) {
     const int threads = reg_threads(ring->warps), groups = threads / 32 / ring->warps, arrays = a.sg ? 3 : 2;
     r.row_bytes = uint32_t(p.N * D::kBytes);
-    r.slot_bytes = r.row_bytes * uint32_t(groups * arrays);
+    r.slot_row = vec ? r.row_bytes : (r.row_bytes + 15) / 16 * 16 + 16;  // lines that a row has parts in
+    r.slot_bytes = r.slot_row * uint32_t(groups * arrays);
     const auto slots = [&](int ctas) { return (dev.max_smem_per_sm / ctas - 2048) / int(r.slot_bytes); };
     for (ring_ctas = 512 / threads; ring_ctas > 1 && slots(ring_ctas) < 2;) --ring_ctas;
     r.slots = slots(ring_ctas) < kMostSlots ? slots(ring_ctas) : kMostSlots;
@@ -770,7 +829,7 @@ cudaError_t launch_grad_type(const RmsNormGrad& p, GradArgs a, const DeviceInfo&
     a.parts_n = 0;
   } else if (ring) {
     const int threads = reg_threads(ring->warps), groups = threads / 32 / ring->warps;
-    const int64_t turns = (p.M + groups - 1) / groups, most = int64_t(dev.sm_count) * ring_ctas;
+    const int64_t turns = (p.M + groups - 1) / groups, most = int64_t(dev.sm_count) * ring_ctas / D::kVec * D::kVec;  // LINES' rows
     a.parts_n = int(turns < most ? turns : most);
     r.g = a;
     r.status = dev.status;

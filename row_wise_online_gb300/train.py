@@ -446,11 +446,22 @@ def _grads(tensors, out):
     return w, index
 
 
+def _distinct(words):
+    """Refuses a tensor that a call would scale twice."""
+    to = words[1::4]
+    if len(set(to)) != len(to):
+        held = [p for p, n in zip(to, words[2::4]) if n]
+        if len(set(held)) != len(held):
+            raise ValueError("a gradient (or a tensor of out) is listed twice")
+
+
 def _grad_norm(tensors, out, max_norm, scale, norm_out, workspace, stream):
     import torch
 
     tensors = tensors if isinstance(tensors, (list, tuple)) else list(tensors)
     words, index = _grads(tensors, out)
+    if max_norm is not None:
+        _distinct(words)
     s = _stream_of(index, stream)
     if s is None:
         with _switched(index, stream):
@@ -477,7 +488,7 @@ def grad_norm(tensors, scale: float = 1.0, norm_out=None, workspace=None, stream
 
 
 def clip_grad_norm(tensors, max_norm: float, out=None, scale: float = 1.0, norm_out=None, workspace=None, stream=None):
-    """Scale gradients by ``scale * min(1, max_norm / norm)``, norm = grad_norm(tensors, scale), which is returned.
+    """Scale gradients, each listed once, by ``scale * min(1, max_norm / norm)``, norm = grad_norm(tensors, scale), which is returned.
 
     In place, or into ``out``: as many tensors, in the gradients' dtypes or float32.  A norm that is inf or NaN limits nothing;
     in place, gradients whose factor is 1 are not touched.
