@@ -416,6 +416,103 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
   }
 }
 
+// Forward into the element type for rows of x on no boundary (and a residual that starts at the same place of its 16-byte lines).  As
+// that place comes again after 16 bytes' worth of rows, and a CTA's turns are a multiple of those apart, it is one for all rows of a group: lines
+// are worked on where they are, and the weights lie moved in shared memory, each thread's for itself.  Taken by what is read alone:
+// a call in place gives the bits of one that is not.  16384 x 5003 bf16 with a residual 132 us (lines shifted in registers, for single rows, 243), 65536 x 333 fp32 71.
+template <class D, int K>
+constexpr int lines_shared(int threads) { return threads * K * D::kVec * 4; }
+constexpr int lines_ctas(int K, int threads) { return (K > 4 ? 2 : 4) * 256 / threads; }
+
+template <class D, int K, int W>
+__global__ void __launch_bounds__(reg_threads(W), lines_ctas(K, reg_threads(W))) k_rms_norm_lines(NormArgs a) {
+  constexpr int E = D::kVec, GT = W * 32, T = reg_threads(W), G = T / GT;
+  extern __shared__ float4 held[];  // [K][E / 4][T]
+  __shared__ float sums[2][T / 32];
+  const int group = threadIdx.x / GT, t = threadIdx.x % GT, n = int(a.N);
+  const int64_t bytes = a.N * D::kBytes;
+  const Bytes xm = bytes_of(a.x, a.M, a.x_pitch, bytes), rm = bytes_of(a.r, a.M, a.r_pitch, bytes);
+  int64_t row = int64_t(blockIdx.x) * G + group;
+  const int from = int(reinterpret_cast<uintptr_t>(a.x + row * a.x_pitch) & 15) / D::kBytes, end = from + n, units = (end + E - 1) / E;
+  const auto whole = [&](int u) { return u * E >= from && u * E + E <= end; };
+  const auto load = [&](const RowAt& r, uint4 (&q)[K]) {
+    const unsigned char* p = r.row - r.delta;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int u = t + k * GT;
+      q[k] = make_uint4(0, 0, 0, 0);
+      if (u < units) q[k] = whole(u) || r.inside ? ld_stream16(p + int64_t(u) * 16) : load_elements<D>(p + int64_t(u) * 16, r.row, r.end);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int u = t + k * GT;
+      if (u < units && !whole(u)) q[k] = keep<D>(q[k], from - u * E, end - u * E, 0);
+    }
+  };
+  const auto store = [&](unsigned char* to, int k, const uint4& q) {
+    const int u = t + k * GT, lane = t & 31, u0 = u - lane;
+    unsigned char* p = to - from * D::kBytes + int64_t(u) * 16;
+    if (reinterpret_cast<uintptr_t>(p) & 15 && u0 * E >= from && (u0 + 32) * E <= end) {  // an output that starts elsewhere: a warp's vectors
+      const uint4 one[1] = {q};
+      store_vectors<D>(p - lane * 16, lane, 32 * E, one);
+    } else if (u < units) {
+      if (!(reinterpret_cast<uintptr_t>(p) & 15) && whole(u)) st_stream16(p, q);
+      else store_elements<D>(p, q, from - u * E, end - u * E);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int b = (t + k * GT) * E;
+    float w[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] = b + e >= from && b + e < end ? weight1<D>(a, b + e - from) : 0.f;
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) held[(k * (E / 4) + i) * T + threadIdx.x] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+  int it = 0;
+  for (; row < a.M; row += int64_t(gridDim.x) * G, it ^= 1) {
+    uint4 h[K];
+    load(row_at<D>(a.x + row * a.x_pitch, n, xm), h);
+    if (a.r) {
+      uint4 r[K];
+      load(row_at<D>(a.r + row * a.r_pitch, n, rm), r);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float v[E], w[E];
+        D::unpack(h[k], v);
+        D::unpack(r[k], w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] += w[e];
+        h[k] = D::pack(v);
+        store(a.h + row * a.h_pitch, k, h[k]);
+      }
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float v[E];
+      D::unpack(h[k], v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum = __fmaf_rn(v[e], v[e], sum);
+    }
+    sum = group_sum<W>(sum, sums[it] + group * W, group, t);
+    const float rstd = 1.f / sqrtf(sum / float(a.N) + a.eps);
+    if (a.rstd && t == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float v[E];
+      D::unpack(h[k], v);
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        const float4 w = held[(k * (E / 4) + i) * T + threadIdx.x];
+        v[4 * i] = v[4 * i] * rstd * w.x, v[4 * i + 1] = v[4 * i + 1] * rstd * w.y;
+        v[4 * i + 2] = v[4 * i + 2] * rstd * w.z, v[4 * i + 3] = v[4 * i + 3] * rstd * w.w;
+      }
+      store(a.y + row * a.y_pitch, k, D::pack(v));
+    }
+  }
+}
+
 // Backward: every CTA walks its rows with the columns' sums of dw in registers, and leaves them as one part.
 template <class D, int K, int W, bool SHIFT>
 __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
@@ -741,6 +838,15 @@ constexpr RingConfig ring_cfg() {
   return RingConfig{W, 32 * W * K, k_rms_grad_ring<D, K, W, LINES>};
 }
 
+struct LinesConfig {
+  int warps, units, shared, ctas;
+  void (*fn)(NormArgs);
+};
+template <class D, int K, int W>
+constexpr LinesConfig lines_cfg() {
+  return LinesConfig{W, 32 * W * K, lines_shared<D, K>(reg_threads(W)), lines_ctas(K, reg_threads(W)), k_rms_norm_lines<D, K, W>};
+}
+
 // The first configuration that holds a row.
 template <class C, int n>
 const C* pick(const C (&table)[n], int64_t units) {
@@ -771,6 +877,8 @@ cudaError_t launch_norm_type(const RmsNorm& p, const NormArgs& a, const DeviceIn
                                        norm_cfg<D, 3, 4, false>(), norm_cfg<D, 4, 4, false>(), norm_cfg<D, 3, 8, false>(), norm_cfg<D, 4, 8, false>(), norm_cfg<D, 4, 16, false>(), norm_cfg<D, 8, 16, false>()};
   static const NormConfig anywhere[] = {norm_cfg<D, 1, 1, true>(), norm_cfg<D, 4, 1, true>(), norm_cfg<D, 4, 4, true>(), norm_cfg<D, 4, 8, true>(),
                                         norm_cfg<D, 4, 16, true>(), norm_cfg<D, 8, 16, true>()};
+  static const LinesConfig lined[] = {lines_cfg<D, 1, 1>(), lines_cfg<D, 2, 1>(), lines_cfg<D, 4, 1>(), lines_cfg<D, 4, 2>(), lines_cfg<D, 4, 4>(),
+                                      lines_cfg<D, 3, 8>(), lines_cfg<D, 4, 8>(), lines_cfg<D, 4, 16>(), lines_cfg<D, 8, 16>()};
   const bool e4m3 = p.out == RMS_NORM_OUT_E4M3;
   // codes of a vector are 8 or 4 bytes: half or a quarter of what the element types need
   const uintptr_t code = e4m3 ? 16 / D::kVec : 1;
@@ -778,7 +886,14 @@ cudaError_t launch_norm_type(const RmsNorm& p, const NormArgs& a, const DeviceIn
                          a.r ? uintptr_t(a.r_pitch | a.h_pitch) : 0, uintptr_t(a.y_pitch) * code, uintptr_t(p.N * D::kBytes)});
   const int64_t units = (p.N + D::kVec - 1) / D::kVec;
   const NormConfig* c = vec ? pick(aligned, units) : pick(anywhere, units);
-  if (c) {
+  const bool lines = !e4m3 && !on16({bits(a.x), uintptr_t(a.x_pitch)}) && (!a.r || !(((bits(a.r) ^ bits(a.x)) | uintptr_t(a.r_pitch ^ a.x_pitch)) & 15));
+  if (const LinesConfig* l = lines ? pick(lined, (p.N + 2 * D::kVec - 2) / D::kVec) : nullptr) {
+    const int threads = reg_threads(l->warps), groups = threads / 32 / l->warps;
+    const int64_t ctas = (p.M + groups - 1) / groups, most = int64_t(dev.sm_count) * l->ctas / D::kVec * D::kVec;
+    const cudaError_t e = cudaFuncSetAttribute((const void*)l->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, l->shared);
+    if (e != cudaSuccess) return e;
+    l->fn<<<unsigned(ctas < most ? ctas : most), threads, size_t(l->shared), p.stream>>>(a);
+  } else if (c) {
     const int threads = reg_threads(c->warps), groups = threads / 32 / c->warps;
     const int64_t ctas = (p.M + groups - 1) / groups, most = int64_t(dev.sm_count) * (dev.max_threads_per_sm / threads) * 4;
     c->fn[e4m3]<<<unsigned(ctas < most ? ctas : most), threads, 0, p.stream>>>(a);

@@ -301,3 +301,36 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
     assert torch.equal(y, rwo.rms_norm_rows(h, w, sg)[0])
+
+
+def framed(t, shift, pad):
+    """t at a pitch of pad more, its storage's other elements NaN."""
+    M, N = t.shape
+    buf = torch.full((shift + M * (N + pad) + 8,), math.nan, dtype=t.dtype, device="cuda")
+    v = buf[shift:shift + M * (N + pad)].view(M, N + pad)[:, :N]
+    v.copy_(t)
+    return buf, v
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("M,N", [(5000, 7), (3001, 333), (1700, 1501), (900, 5003), (400, 14001)])
+@pytest.mark.parametrize("shift,pad,other", [(0, 0, 0), (1, 2, 0), (5, 0, 0), (3, 1, 1)])
+def test_rows_on_no_boundary(M, N, dt, shift, pad, other):
+    """Many rows that start anywhere, all matrices alike (other = 0) or one elsewhere; what lies between the rows stays."""
+    dy, h, rstd, sg, w = grad_inputs(M, N, dt)
+    (_, hv), (_, sv), (_, rv) = framed(h, shift, pad), framed(sg, shift + other, pad), framed(dy, shift, pad)
+    buf, dv = framed(dy, shift, pad)
+    gaps = torch.isnan(buf)
+    dx, _ = grad_check(rv, hv, rstd.cuda(), w.cuda(), sg=sv, dx=framed(dy, shift, pad)[1])
+    again, _ = rwo.rms_norm_rows_backward(dv, hv, rstd.cuda(), w.cuda(), sum_grad=sv, dx=dv)
+    assert torch.equal(again, dx) and torch.equal(torch.isnan(buf), gaps)
+    check(hv, w.cuda(), sv)
+    buf, v = framed(h, shift, pad)
+    y, _ = rwo.rms_norm_rows(v, w.cuda(), sv, y=framed(h, shift, pad)[1], sum_out=v)
+    assert torch.equal(torch.isnan(buf), gaps)
+    buf, v = framed(h, shift, pad)
+    plain, _ = rwo.rms_norm_rows(v, w.cuda(), y=v)
+    assert torch.equal(torch.isnan(buf), gaps)
+    assert_close(plain, reference(h, w)[2], y_tol(reference(h, w)[2], N, dt))
+    ref = reference(h, w, sg)[2]
+    assert_close(y, ref, y_tol(ref, N, dt))
