@@ -158,3 +158,16 @@ def test_repeats_streams_and_graphs():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(norm, want) and all(torch.equal(a, b) for a, b in zip(out, held))
+
+
+def test_a_tensor_listed_twice():
+    a, b = (t.cuda() for t in make([100, 300], [F32]))
+    e = a[:0]
+    assert abs(float(rwo.grad_norm([a, a])) - float(a.double().pow(2).sum() * 2) ** 0.5) <= NORM * float(a.double().norm()) * 2 ** 0.5
+    keep = a.clone()
+    for call in (lambda: rwo.clip_grad_norm([a, b, a], 1.0), lambda: rwo.clip_grad_norm([a, a], 1.0, out=[keep, keep])):
+        with pytest.raises(ValueError, match="twice"):
+            call()
+    assert torch.equal(a, keep)
+    rwo.clip_grad_norm([a, e, e, b], 1.0)  # empty ones may come again
+    assert rwo.get_status() == rwo.OK
