@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
 }
 
 // dw = the parts added up: 32 columns a CTA, its warps every 32nd part.
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 1024, kAtOnce = 10;  // parts that a warp has under way: all of 304
 __global__ void __launch_bounds__(kJoinThreads) k_rms_weight_join(GradArgs a) {
   __shared__ float sums[kJoinThreads / 32][33];
   griddep_wait();
@@ -800,8 +800,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_rms_weight_join(GradArgs a) {
   const int64_t i = int64_t(blockIdx.x) * 32 + lane;
   float sum = 0.f;
   if (i < a.N) {
-#pragma unroll 16
-    for (int k = warp; k < a.parts_n; k += kJoinThreads / 32) sum += a.parts[k * a.N + i];
+    for (int k0 = warp; k0 < a.parts_n; k0 += kAtOnce * (kJoinThreads / 32)) {
+      float v[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int k = k0 + j * (kJoinThreads / 32);
+        v[j] = k < a.parts_n ? a.parts[k * a.N + i] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) sum += v[j];
+    }
   }
   sums[warp][lane] = sum;
   __syncthreads();
