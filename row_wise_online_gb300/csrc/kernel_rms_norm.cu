@@ -513,7 +513,9 @@ __global__ void __launch_bounds__(reg_threads(W), lines_ctas(K, reg_threads(W)))
   }
 }
 
-// Backward: every CTA walks its rows with the columns' sums of dw in registers, and leaves them as one part.
+// Backward: every CTA walks its rows with the columns' sums of dw in registers, and leaves them as one part.  h is multiplied by rstd before
+// dy meets it, and rstd stands before no power of itself: h dy and rstd^3 leave fp32's range long before xhat dy and rstd do (of
+// rows of magnitude 1e15 rstd^3 is 0, and dx would lose all of its second term).
 template <class D, int K, int W, bool SHIFT>
 __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
   constexpr int E = D::kVec, GT = W * 32, G = reg_threads(W) / GT;
@@ -548,13 +550,13 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
       weights<D, SHIFT>(a, u, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float p = d[e] * x[e];
+        const float p = d[e] * (x[e] * rstd);
         sum = __fmaf_rn(p, w[e], sum);
-        dw[k][e] = __fmaf_rn(p, rstd, dw[k][e]);
+        dw[k][e] += p;
       }
     }
     sum = group_sum<W>(sum, sums[it] + group * W, group, t);  // and every load of the row is done
-    const float slope = -(rstd * rstd * rstd) * (sum / float(a.N));
+    const float slope = -rstd * (sum / float(a.N));
     unsigned char* to = a.dx + row * a.dx_pitch;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
       D::unpack(sg[k], s);
       if (u < units) weights<D, SHIFT>(a, u, w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) d[e] = __fmaf_rn(rstd, d[e] * w[e], __fmaf_rn(slope, x[e], s[e]));
+      for (int e = 0; e < E; ++e) d[e] = __fmaf_rn(rstd, __fmaf_rn(slope, x[e], d[e] * w[e]), s[e]);
       dy[k] = D::pack(d);
     }
     put<D, K, SHIFT>(to, t, units, n, dy);
@@ -701,7 +703,7 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
     const bool on = row < a.M;
     if (!mbar_wait(smem_addr(&full[s]), parity, r.wait_ns)) timed_out = true;
     const float2 rstd2 = make_float2(rstd, rstd);
-    float2 sum2 = make_float2(0.f, 0.f);  // of g h
+    float2 sum2 = make_float2(0.f, 0.f);  // of g xhat
     if (on) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -712,9 +714,9 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
         D::unpack2(slot_vector<D, LINES>(hs, u, from, end), x);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
-          const float2 p = __fmul2_rn(d[e], x[e]);
+          const float2 p = __fmul2_rn(d[e], __fmul2_rn(x[e], rstd2));
           sum2 = __ffma2_rn(p, w[k][e], sum2);
-          dw[k][e] = __ffma2_rn(p, rstd2, dw[k][e]);
+          dw[k][e] = __fadd2_rn(dw[k][e], p);
         }
       }
     }
@@ -732,7 +734,7 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
       for (int o = W >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     }
     if (on) {
-      const float slope = -(rstd * rstd * rstd) * (sum / float(a.N));  // dx = rstd g + slope h + sum_grad
+      const float slope = -rstd * (sum / float(a.N));  // dx = rstd (g + slope h) + sum_grad
       const float2 slope2 = make_float2(slope, slope);
       unsigned char* to = a.dx + row * a.dx_pitch - from * D::kBytes;
 #pragma unroll
@@ -744,7 +746,7 @@ __global__ void __launch_bounds__(reg_threads(W), 512 / reg_threads(W)) k_rms_gr
         D::unpack2(slot_vector<D, LINES>(hs, u, from, end), x);
         if (a.sg) D::unpack2(slot_vector<D, LINES>(sgs, u, from, end), g);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) d[e] = __ffma2_rn(__fmul2_rn(d[e], w[k][e]), rstd2, __ffma2_rn(x[e], slope2, g[e]));
+        for (int e = 0; e < E / 2; ++e) d[e] = __ffma2_rn(__ffma2_rn(x[e], slope2, __fmul2_rn(d[e], w[k][e])), rstd2, g[e]);
         const int first = from - u * E, last = end - u * E;
         if (LINES && (first > 0 || last < E)) store_elements<D>(to + int64_t(u) * 16, D::pack2(d), first, last);
         else st_stream16(to + int64_t(u) * 16, D::pack2(d));
