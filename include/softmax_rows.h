@@ -438,8 +438,9 @@ int cross_entropy_rows_grad(const void* x, int64_t ldx, const int64_t* labels, c
  *   eps         -- finite, >= 0.   offset -- finite (1 where weights are kept as their difference from 1).
  *   y           -- out = RMS_NORM_OUT_SAME: dtype elements.  May be x, or residual, where sum_out is not.
  *                  out = RMS_NORM_OUT_E4M3 (y a matrix of its own): 8-bit floats (e4m3, largest 448), with fp32 scales: the value is
- *                  code * scale, scale = max(max |y| / 448, 2^-126) over a group, code = y * (1 / scale) rounded to
- *                  the nearest (ties to even).
+ *                  code * scale, scale = max(max |y| / 448, 2^-126) over a group, code = y / scale rounded to the nearest
+ *                  (ties to even): of bf16 elements and weights with offset 0, that of the exact quotient, in which rstd
+ *                  cancels out (above the least scale).
  *   scales      -- e4m3 only: [M][groups], groups = 1 for group = 0 (a scale for each row), else ceil(N / group).
  *   group       -- 0 or 128 (the last group of a row may be shorter).
  *   rstd_out    -- fp32 [M] or NULL; the backward pass reads it.

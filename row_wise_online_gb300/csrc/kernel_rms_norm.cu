@@ -48,13 +48,57 @@ struct GradArgs {
   bool w_f32, w_vec, accumulate;
 };
 
-template <class D, class A>
+// What a factor weight + offset is multiplied by on its way into 8 bits (Codes).
+constexpr float kSeven = 3.5f;
+
+// A weight as it lies, to a factor; into 8 bits kSeven times it.
+template <bool E4M3, class A>
+__device__ __forceinline__ float factor(const A& a, float w) {
+  return E4M3 ? __fmaf_rn(w, kSeven, kSeven * a.offset) : w + a.offset;
+}
+template <class D, bool E4M3 = false, class A>
 __device__ __forceinline__ float weight1(const A& a, int64_t i) {
-  if (!a.w) return 1.f;
-  return (a.w_f32 ? __ldg(static_cast<const float*>(a.w) + i) : D::load1(a.w, i)) + a.offset;
+  if (!a.w) return E4M3 ? kSeven : 1.f;
+  return factor<E4M3>(a, a.w_f32 ? __ldg(static_cast<const float*>(a.w) + i) : D::load1(a.w, i));
 }
 
-__device__ __forceinline__ float scale_of(float top) { return fmaxf(top * (1.f / kE4m3Max), kScaleMin); }
+// Codes in 8 bits: the nearest to y / scale, scale = max |y| / 448 over a group.  rstd is in both, so of rstd = two * rest, two a power of
+// 2, the kernels take two alone and work with
+//     v = h two (7/2) (weight + offset) = (7/2) y / rest,    scale = (2/7) rest t,    y / scale = v / t,    t = max |v| / 448.
+// Of bf16 elements and weights v is exact (7 times a product of 16 bits), and so is t.  One value in 2500 lies in the middle between two
+// codes there; roundings of y, scale and 1 / scale put it on either side, by the order in which a row's squares are added up.  So the
+// quotient's remainder against t takes up what v * (1 / t) rounded: the code is that of the exact quotient, ties to even, in every kernel.
+struct Codes {
+  float t, inv;
+};
+struct Parts {
+  float two, back, least;  // back: (2/7) rest; least: the t of the least scale
+};
+__device__ __forceinline__ Parts parts_of(float rstd) {
+  const uint32_t b = __float_as_uint(rstd);
+  const bool number = rstd <= 3.4028234663852886e38f;
+  Parts p;
+  p.two = number ? __uint_as_float(b & 0x7f800000u) : rstd;
+  p.back = (number ? __uint_as_float((b & 0x007fffffu) | 0x3f800000u) : 1.f) * (1.f / kSeven);
+  p.least = __fdividef(kScaleMin, p.back);
+  return p;
+}
+// Of a group whose largest |v| is top; its scale.
+__device__ __forceinline__ Codes codes_of(float top, const Parts& p, float* scale) {
+  float t = top * (1.f / kE4m3Max);
+  if (top <= 3.4028234663852886e38f) t = __fmaf_rn(__fmaf_rn(-t, kE4m3Max, top), 1.f / kE4m3Max, t);
+  *scale = fmaxf(t * p.back, kScaleMin);
+  t = fmaxf(t, p.least);
+  return Codes{t, __fdividef(1.f, t)};
+}
+__device__ __forceinline__ float quotient(float v, const Codes& c) {
+  const float q = v * c.inv;
+  return __fmaf_rn(__fmaf_rn(-q, c.t, v), c.inv, q);
+}
+__device__ __forceinline__ float2 quotient2(const float2& v, const Codes& c) {
+  const float2 inv = make_float2(c.inv, c.inv), q = __fmul2_rn(v, inv);
+  return __ffma2_rn(__ffma2_rn(q, make_float2(-c.t, -c.t), v), inv, q);
+}
 
 // Two values -> two e4m3 codes (lo in the low byte), to the nearest, limited to +-448.
 __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
@@ -125,30 +169,34 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_loop(NormArgs a) {
     if constexpr (!E4M3) {
       for (int64_t i = threadIdx.x; i < a.N; i += kThreads) D::store1(yr, i, load1c<D>(hr, i) * rstd * weight1<D>(a, i));
     } else if (a.groups == 1 && a.N > kGroup) {
+      const Parts p = parts_of(rstd);
       float top = 0.f;
-      for (int64_t i = threadIdx.x; i < a.N; i += kThreads) top = fmaxf(top, fabsf(load1c<D>(hr, i) * rstd * weight1<D>(a, i)));
+      for (int64_t i = threadIdx.x; i < a.N; i += kThreads) top = fmaxf(top, fabsf(load1c<D>(hr, i) * p.two * weight1<D, true>(a, i)));
       top = block_max<kThreads / 32>(top, slots);
-      const float scale = scale_of(top), inv = __fdividef(1.f, scale);
+      float scale;
+      const Codes c = codes_of(top, p, &scale);
       if (threadIdx.x == 0) a.scales[row] = scale;
       for (int64_t i = threadIdx.x; i < a.N; i += kThreads)
-        yr[i] = (unsigned char)(pack_e4m3x2(load1c<D>(hr, i) * rstd * weight1<D>(a, i) * inv, 0.f) & 0xff);
+        yr[i] = (unsigned char)(pack_e4m3x2(quotient(load1c<D>(hr, i) * p.two * weight1<D, true>(a, i), c), 0.f) & 0xff);
     } else {
+      const Parts p = parts_of(rstd);
       for (int64_t g = warp; g < a.groups; g += kThreads / 32) {
         float v[kGroup / 32], top = 0.f;
 #pragma unroll
         for (int k = 0; k < kGroup / 32; ++k) {
           const int64_t i = g * kGroup + k * 32 + lane;
-          v[k] = i < a.N ? load1c<D>(hr, i) * rstd * weight1<D>(a, i) : 0.f;
+          v[k] = i < a.N ? load1c<D>(hr, i) * p.two * weight1<D, true>(a, i) : 0.f;
           top = fmaxf(top, fabsf(v[k]));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        const float scale = scale_of(top), inv = __fdividef(1.f, scale);
+        float scale;
+        const Codes c = codes_of(top, p, &scale);
         if (lane == 0) a.scales[row * a.groups + g] = scale;
 #pragma unroll
         for (int k = 0; k < kGroup / 32; ++k) {
           const int64_t i = g * kGroup + k * 32 + lane;
-          if (i < a.N) yr[i] = (unsigned char)(pack_e4m3x2(v[k] * inv, 0.f) & 0xff);
+          if (i < a.N) yr[i] = (unsigned char)(pack_e4m3x2(quotient(v[k], c), 0.f) & 0xff);
         }
       }
     }
@@ -251,19 +299,19 @@ __device__ __forceinline__ float group_max(float v, float* slots, int group, int
   return v;
 }
 
-// The factors weight + offset of vector u, 0 behind the row's end.
-template <class D, bool SHIFT, class A>
+// The factors weight + offset of vector u (into 8 bits, kSeven times them), 0 behind the row's end.
+template <class D, bool SHIFT, bool E4M3 = false, class A>
 __device__ __forceinline__ void weights(const A& a, int u, float (&w)[D::kVec]) {
   constexpr int E = D::kVec;
   const int left = SHIFT ? int(a.N) - u * E : E;
   if (!a.w) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) w[e] = e < left ? 1.f : 0.f;
+    for (int e = 0; e < E; ++e) w[e] = e < left ? (E4M3 ? kSeven : 1.f) : 0.f;
     return;
   }
   if (SHIFT && (left < E || !a.w_vec)) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) w[e] = e < left ? weight1<D>(a, int64_t(u) * E + e) : 0.f;
+    for (int e = 0; e < E; ++e) w[e] = e < left ? weight1<D, E4M3>(a, int64_t(u) * E + e) : 0.f;
     return;
   }
   if (a.w_f32 && D::kBytes == 2) {
@@ -275,15 +323,18 @@ __device__ __forceinline__ void weights(const A& a, int u, float (&w)[D::kVec]) 
     D::unpack(__ldg(static_cast<const uint4*>(a.w) + u), w);
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) w[e] += a.offset;
+  for (int e = 0; e < E; ++e) w[e] = factor<E4M3>(a, w[e]);
 }
 
 // The codes of vector u, left elements of it.
 template <int E, bool SHIFT>
-__device__ __forceinline__ void store_codes(unsigned char* row, int u, int left, const float (&v)[E], float inv) {
+__device__ __forceinline__ void store_codes(unsigned char* row, int u, int left, const float2 (&v)[E / 2], const Codes& codes) {
   uint16_t c[E / 2];
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) c[e] = pack_e4m3x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+  for (int e = 0; e < E / 2; ++e) {
+    const float2 q = quotient2(v[e], codes);
+    c[e] = pack_e4m3x2(q.x, q.y);
+  }
   unsigned char* p = row + int64_t(u) * E;
   if (SHIFT && (left < E || (reinterpret_cast<uintptr_t>(p) & (E - 1)))) {
 #pragma unroll
@@ -348,65 +399,75 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
     const float rstd = 1.f / sqrtf(sum / float(a.N) + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     unsigned char* yr = a.y + row * a.y_pitch;
-    const auto value = [&](int k, float(&v)[E]) {  // y in 32 bits, 0 behind the row's end
-      const int u = unit_of<K>(t, k);
-      float w[E];
-      D::unpack(h[k], v);
-      if (PACKED && packed) {
-        D::unpack(wq[k], w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) w[e] += a.offset;
-      } else {
-        weights<D, SHIFT>(a, min(u, units - 1), w);  // h is 0 behind the end
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = v[e] * rstd * w[e];
-    };
     if constexpr (!E4M3) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        float v[E];
-        value(k, v);
+        float v[E], w[E];
+        D::unpack(h[k], v);
+        weights<D, SHIFT>(a, min(unit_of<K>(t, k), units - 1), w);  // h is 0 behind the end
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = v[e] * rstd * w[e];
         h[k] = D::pack(v);
       }
       put<D, K, SHIFT>(yr, t, units, n, h);
     } else {
-      const auto top_of = [&](const float(&v)[E]) {
-        float m = fabsf(v[0]);
+      const Parts p = parts_of(rstd);
+      const float2 two = make_float2(p.two, p.two), seven = make_float2(kSeven, kSeven), offset = make_float2(kSeven * a.offset, kSeven * a.offset);
+      const auto value = [&](int k, float2(&v)[E / 2]) {  // v of Codes, 0 behind the row's end
+        float2 w[E / 2];
+        if (PACKED && packed) {
+          D::unpack2(wq[k], w);
 #pragma unroll
-        for (int e = 1; e < E; ++e) m = fmaxf(m, fabsf(v[e]));
+          for (int e = 0; e < E / 2; ++e) w[e] = __ffma2_rn(w[e], seven, offset);
+        } else {
+          float f[E];
+          weights<D, SHIFT, true>(a, min(unit_of<K>(t, k), units - 1), f);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) w[e] = make_float2(f[2 * e], f[2 * e + 1]);
+        }
+        D::unpack2(h[k], v);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) v[e] = __fmul2_rn(__fmul2_rn(v[e], two), w[e]);
+      };
+      const auto top_of = [&](const float2(&v)[E / 2]) {
+        float m = fmaxf(fabsf(v[0].x), fabsf(v[0].y));
+#pragma unroll
+        for (int e = 1; e < E / 2; ++e) m = fmaxf(m, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
         return m;
       };
-      const auto store = [&](int k, const float(&v)[E], float inv) {
+      const auto store = [&](int k, const float2(&v)[E / 2], const Codes& c) {
         const int u = unit_of<K>(t, k);
-        if (u < units) store_codes<E, SHIFT>(yr, u, n - u * E, v, inv);
+        if (u < units) store_codes<E, SHIFT>(yr, u, n - u * E, v, c);
       };
       if (a.groups == 1 && a.N > kGroup) {
-        float y[K][E], top = 0.f;
+        float2 y[K][E / 2];
+        float top = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           value(k, y[k]);
           top = fmaxf(top, top_of(y[k]));
         }
         top = group_max<W>(top, tops[it] + group * W, group, t);
-        const float scale = scale_of(top), inv = __fdividef(1.f, scale);
+        float scale;
+        const Codes c = codes_of(top, p, &scale);
         if (t == 0) a.scales[row] = scale;
 #pragma unroll
-        for (int k = 0; k < K; ++k) store(k, y[k], inv);
+        for (int k = 0; k < K; ++k) store(k, y[k], c);
       } else {
         constexpr int lanes = kGroup / E, per = 32 / lanes;  // of a group; groups of a warp's 32 vectors
         float mine = 0.f;  // lane i: scale i of the warp's
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          float y[E];
+          float2 y[E / 2];
           value(k, y);
           float top = top_of(y);
 #pragma unroll
           for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-          const float scale = scale_of(top), inv = __fdividef(1.f, scale);
+          float scale;
+          const Codes c = codes_of(top, p, &scale);
           const float theirs = __shfl_sync(~0u, scale, (lane & (per - 1)) * lanes);
           if (lane / per == k) mine = theirs;
-          store(k, y, inv);
+          store(k, y, c);
         }
         // one store for the warp's groups, which lie together: by twos, as they came, 16384 x 8192 took 163 us instead of 144
         const int g = unit_of<K>(t - lane, 0) / lanes + lane;
