@@ -545,7 +545,7 @@ typedef struct grad_tensor {
  * values are lost.  +inf or NaN where an element is not finite (or the norm is above fp32's range).
  * clip_grad_norm -- the same, and
  *     out = grad * scale * min(1, max_norm / norm)
- * for each tensor, rounded once.  Where the norm is inf or NaN nothing is limited: out = grad * scale.  A tensor in
+ * for each tensor, the factor in more than fp32's bits and the product rounded once.  Where the norm is inf or NaN nothing is limited: out = grad * scale.  A tensor in
  * place (out == grad) whose factor is 1 is neither read again nor written.
  *   tensors   -- HOST array of count entries (at most 2^20, 2^42 elements in all), read before the call returns; tensors may
  *                not overlap each other.
@@ -555,7 +555,7 @@ typedef struct grad_tensor {
  */
 int grad_norm(const grad_tensor* tensors, int64_t count, float scale, float* norm_out, void* workspace,
               int64_t workspace_bytes, void* stream);
-int clip_grad_norm(const grad_tensor* tensors, int64_t count, float scale, float max_norm, float* norm_out, void* workspace,
+int clip_grad_norm(const grad_tensor* tensors, int64_t count, float scale, double max_norm, float* norm_out, void* workspace,
                    int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace on the current device; -1 for a count that the calls refuse. */

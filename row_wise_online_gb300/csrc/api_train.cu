@@ -250,7 +250,7 @@ int64_t grad_norm_workspace(int64_t count) {
   return int64_t(grad_norm_scratch(count, *dev));
 }
 
-static int run_grad_norm(const grad_tensor* t, int64_t count, float scale, float max_norm, float* norm_out, void* workspace,
+static int run_grad_norm(const grad_tensor* t, int64_t count, float scale, double max_norm, float* norm_out, void* workspace,
                          int64_t workspace_bytes, void* stream) {
   if (count < 0 || (count > 0 && !t) || !finite(scale) || !norm_out) return SOFTMAX_ERR_INVALID_ARG;
   if (count > kMaxTensors) return SOFTMAX_ERR_UNSUPPORTED;
@@ -261,7 +261,7 @@ static int run_grad_norm(const grad_tensor* t, int64_t count, float scale, float
     if (t[i].n > kMaxElements || (total += t[i].n) > kMaxElements) return SOFTMAX_ERR_UNSUPPORTED;
     if (t[i].n > 0 && !t[i].grad) return SOFTMAX_ERR_INVALID_ARG;
     if (!aligned(t[i].grad, uintptr_t(elem_bytes(t[i].dtype)))) return SOFTMAX_ERR_MISALIGNED;
-    if (max_norm == 0.f) continue;
+    if (max_norm == 0.0) continue;
     if (check_dtype(t[i].out_dtype) != SOFTMAX_OK || (t[i].n > 0 && !t[i].out)) return SOFTMAX_ERR_INVALID_ARG;
     if (t[i].out_dtype != t[i].dtype && t[i].out_dtype != SOFTMAX_F32) return SOFTMAX_ERR_UNSUPPORTED;
     if (t[i].out == t[i].grad && t[i].out_dtype != t[i].dtype && t[i].n > 0) return SOFTMAX_ERR_INVALID_ARG;
@@ -285,12 +285,12 @@ static int run_grad_norm(const grad_tensor* t, int64_t count, float scale, float
 
 int grad_norm(const grad_tensor* tensors, int64_t count, float scale, float* norm_out, void* workspace, int64_t workspace_bytes,
               void* stream) {
-  return run_grad_norm(tensors, count, scale, 0.f, norm_out, workspace, workspace_bytes, stream);
+  return run_grad_norm(tensors, count, scale, 0.0, norm_out, workspace, workspace_bytes, stream);
 }
 
-int clip_grad_norm(const grad_tensor* tensors, int64_t count, float scale, float max_norm, float* norm_out, void* workspace,
+int clip_grad_norm(const grad_tensor* tensors, int64_t count, float scale, double max_norm, float* norm_out, void* workspace,
                    int64_t workspace_bytes, void* stream) {
-  if (!finite(max_norm) || !(max_norm > 0.f)) return SOFTMAX_ERR_INVALID_ARG;
+  if (!std::isfinite(max_norm) || !(max_norm > 0.0)) return SOFTMAX_ERR_INVALID_ARG;
   return run_grad_norm(tensors, count, scale, max_norm, norm_out, workspace, workspace_bytes, stream);
 }
 

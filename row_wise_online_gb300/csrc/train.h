@@ -73,7 +73,7 @@ struct GradNorm {
   const grad_tensor* tensors = nullptr;  // host
   int64_t count = 0;
   float scale = 1.f;
-  float max_norm = 0.f;  // 0: the norm alone
+  double max_norm = 0.0;  // 0: the norm alone
   float* norm = nullptr;
   double* parts = nullptr;
   cudaStream_t stream = nullptr;

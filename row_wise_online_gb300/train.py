@@ -20,7 +20,7 @@ import row_wise_online_gb300 as _rwo
 
 from .decode import _raw_stream, _switched
 
-_vp, _i64, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float
+_vp, _i64, _f32, _f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_double
 
 
 class _Norm(ctypes.Structure):
@@ -54,7 +54,7 @@ def _declare(lib) -> None:
     lib.embedding_rows_backward.argtypes = [_vp, _i64, _vp, ci, _vp, _i64, _i64, _i64, _i64, _f32, ci, ci, ci, _vp, _i64, _vp]
     lib.embedding_backward_workspace.argtypes = [_i64] * 3
     lib.grad_norm.argtypes = [_vp, _i64, _f32, _vp, _vp, _i64, _vp]
-    lib.clip_grad_norm.argtypes = [_vp, _i64, _f32, _f32, _vp, _vp, _i64, _vp]
+    lib.clip_grad_norm.argtypes = [_vp, _i64, _f32, _f64, _vp, _vp, _i64, _vp]
     lib.grad_norm_workspace.argtypes = [_i64]
     for name in ("cross_entropy_rows_grad", "rms_norm_rows", "rms_norm_rows_backward", "embedding_rows", "embedding_rows_backward",
                  "grad_norm", "clip_grad_norm"):
