@@ -547,8 +547,9 @@ typedef struct grad_tensor {
  *     out = grad * scale * min(1, max_norm / norm)
  * for each tensor, the factor in more than fp32's bits and the product rounded once.  Where the norm is inf or NaN nothing is limited: out = grad * scale.  A tensor in
  * place (out == grad) whose factor is 1 is neither read again nor written.
- *   tensors   -- HOST array of count entries (at most 2^20, 2^42 elements in all), read before the call returns; tensors may
- *                not overlap each other.
+ *   tensors   -- HOST array of count entries (at most 2^20, 2^42 elements in all), read before the call returns.  What
+ *                clip_grad_norm writes overlaps no other tensor of the list, read or written, nor its own gradient in part (else
+ *                SOFTMAX_ERR_INVALID_ARG).
  *   scale     -- finite: 1 / (loss scale), 1 / (accumulated steps).   max_norm -- finite, > 0.
  *   norm_out  -- fp32 [1], device.
  *   workspace -- at least grad_norm_workspace(count) bytes.

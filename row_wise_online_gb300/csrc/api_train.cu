@@ -1,6 +1,9 @@
 // api_train.cu -- the C ABI of the training-step operators: loss gradient, root-mean-square norm, embedding, gradient
 // norm.  Host side only: argument checks and launches.
+#include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "train.h"
 
@@ -39,6 +42,39 @@ int check_matrix(const void* p, int64_t* ld, int64_t M, int64_t N, int64_t bytes
 bool alike(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M) { return a != b || lda == ldb || M < 2; }
 
 bool finite(float v) { return std::isfinite(v); }
+
+// Whether what a list of checked tensors has written meets what it has read or written elsewhere: a CTA might scale what another has
+// yet to read, or has scaled.  A tensor in place is one range that is written.
+int check_overlaps(const grad_tensor* t, int64_t count) {
+  struct Range {
+    uintptr_t begin, end;
+    bool written;
+  };
+  constexpr int64_t kOnStack = 128;
+  Range few[kOnStack];
+  std::unique_ptr<Range[]> many;
+  Range* r = few;
+  if (2 * count > kOnStack) {
+    many.reset(new (std::nothrow) Range[size_t(2 * count)]);
+    if (!many) return cuda_failure(cudaErrorMemoryAllocation);
+    r = many.get();
+  }
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    const uintptr_t g = reinterpret_cast<uintptr_t>(t[i].grad), out = reinterpret_cast<uintptr_t>(t[i].out);
+    if (out != g) r[n++] = Range{g, g + uintptr_t(t[i].n * elem_bytes(t[i].dtype)), false};
+    r[n++] = Range{out, out + uintptr_t(t[i].n * elem_bytes(t[i].out_dtype)), true};
+  }
+  std::sort(r, r + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t read = 0, written = 0;  // where those before end
+  for (int64_t i = 0; i < n; ++i) {
+    if (r[i].begin < written || (r[i].written && r[i].begin < read)) return SOFTMAX_ERR_INVALID_ARG;
+    uintptr_t& end = r[i].written ? written : read;
+    end = std::max(end, r[i].end);
+  }
+  return SOFTMAX_OK;
+}
 
 int done(cudaError_t err) { return err == cudaSuccess ? SOFTMAX_OK : cuda_failure(err); }
 
@@ -267,9 +303,10 @@ static int run_grad_norm(const grad_tensor* t, int64_t count, float scale, doubl
     if (t[i].out == t[i].grad && t[i].out_dtype != t[i].dtype && t[i].n > 0) return SOFTMAX_ERR_INVALID_ARG;
     if (!aligned(t[i].out, uintptr_t(elem_bytes(t[i].out_dtype)))) return SOFTMAX_ERR_MISALIGNED;
   }
-  const DeviceInfo* dev = nullptr;
-  int st = current_device(&dev);
+  int st = max_norm == 0.0 ? SOFTMAX_OK : check_overlaps(t, count);
   if (st != SOFTMAX_OK) return st;
+  const DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != SOFTMAX_OK) return st;
   if (!workspace || workspace_bytes < int64_t(grad_norm_scratch(count, *dev))) return SOFTMAX_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return SOFTMAX_ERR_MISALIGNED;
   GradNorm p;

@@ -490,7 +490,7 @@ def grad_norm(tensors, scale: float = 1.0, norm_out=None, workspace=None, stream
 def clip_grad_norm(tensors, max_norm: float, out=None, scale: float = 1.0, norm_out=None, workspace=None, stream=None):
     """Scale gradients, each listed once, by ``scale * min(1, max_norm / norm)``, norm = grad_norm(tensors, scale), which is returned.
 
-    In place, or into ``out``: as many tensors, in the gradients' dtypes or float32.  A norm that is inf or NaN limits nothing;
+    In place, or into ``out``: as many tensors, in the gradients' dtypes or float32, that overlap no other tensor of the call.  A norm that is inf or NaN limits nothing;
     in place, gradients whose factor is 1 are not touched.
     """
     return _grad_norm(tensors, out, float(max_norm), scale, norm_out, workspace, stream)
