@@ -301,8 +301,7 @@ cudaError_t launch_causal_warp(const RowProblem& p, const DeviceInfo& dev, int64
   const CausalPlan plan = plan_causal(p, dev);
   if (!plan.cfg || q_period < 1) return cudaErrorInvalidValue;
   CausalKernel fn = plan.cfg->fn[p.dtype];
-  cudaError_t err = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(plan.smem));
+  cudaError_t err = allow_shared((const void*)fn, dev);
   if (err != cudaSuccess) return err;
   const int threads = plan.warps * 32;
   int occ = 0;

@@ -26,6 +26,7 @@ int chunk_of(int64_t T, int64_t D) {
   return c;
 }
 
+constexpr int kStaticShared = 1024;  // more than the sort has
 constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCtas = 16;
 constexpr int kDigitBits = 10;
 
@@ -685,7 +686,7 @@ cudaError_t launch_grad(const EmbeddingGrad& p, const DeviceInfo& dev) {
     k_rank_tokens<<<unsigned(dev.sm_count), kSortThreads, 0, p.stream>>>(a);
   } else {
     const size_t shared = (size_t(1) << a.digit_bits) * 35 * 4;
-    if ((e = cudaFuncSetAttribute(k_sort_tokens, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared))) != cudaSuccess) return e;
+    if ((e = allow_shared((const void*)k_sort_tokens, dev, kStaticShared)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(k_sort_tokens, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kSortCtas);

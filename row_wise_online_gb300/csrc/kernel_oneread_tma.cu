@@ -526,8 +526,7 @@ cudaError_t launch_oneread_tma(const RowProblem& p, const DeviceInfo& dev) {
   if (p.loss && out != kTmaState) return cudaErrorInvalidValue;
   TmaKernel fn = plan.cfg->fn[out][p.dtype];
   if (!fn) return cudaErrorInvalidValue;
-  cudaError_t err = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(plan.smem));
+  cudaError_t err = allow_shared((const void*)fn, dev);
   if (err != cudaSuccess) return err;
   const int threads = (plan.cfg->ncw + 1) * 32;
   int occ = 0;

@@ -213,8 +213,7 @@ cudaError_t launch_oneread_warp(const RowProblem& p, const DeviceInfo& dev) {
   const WarpPlan plan = plan_warp(p, dev);
   if (!plan.cfg) return cudaErrorInvalidValue;
   WarpKernel fn = plan.cfg->fn[p.dtype];
-  cudaError_t err = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(plan.smem));
+  cudaError_t err = allow_shared((const void*)fn, dev);
   if (err != cudaSuccess) return err;
   const int threads = plan.warps * 32;
   int occ = 0;

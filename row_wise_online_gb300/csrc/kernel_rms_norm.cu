@@ -663,6 +663,7 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
 // worked on where they are, with the weights and the sums of dw moved instead (16384 x 5003 bf16 153 us; vectors shifted out of the
 // slots' lines 237, out of lines in registers 387).
 constexpr int kMostSlots = 4;
+constexpr int kStaticShared = 1024;  // more than these kernels have
 
 struct RingArgs {
   GradArgs g;
@@ -961,7 +962,7 @@ cudaError_t launch_norm_type(const RmsNorm& p, const NormArgs& a, const DeviceIn
   if (const LinesConfig* l = lines ? pick(lined, (p.N + 2 * D::kVec - 2) / D::kVec) : nullptr) {
     const int threads = reg_threads(l->warps), groups = threads / 32 / l->warps;
     const int64_t ctas = (p.M + groups - 1) / groups, most = int64_t(dev.sm_count) * l->ctas / D::kVec * D::kVec;
-    const cudaError_t e = cudaFuncSetAttribute((const void*)l->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, l->shared);
+    const cudaError_t e = allow_shared((const void*)l->fn, dev, kStaticShared);
     if (e != cudaSuccess) return e;
     l->fn<<<unsigned(ctas < most ? ctas : most), threads, size_t(l->shared), p.stream>>>(a);
   } else if (c) {
@@ -1003,7 +1004,7 @@ cudaError_t launch_grad_type(const RmsNormGrad& p, GradArgs a, const DeviceInfo&
     r.row_bytes = uint32_t(p.N * D::kBytes);
     r.slot_row = vec ? r.row_bytes : (r.row_bytes + 15) / 16 * 16 + 16;  // lines that a row has parts in
     r.slot_bytes = r.slot_row * uint32_t(groups * arrays);
-    const auto slots = [&](int ctas) { return (dev.max_smem_per_sm / ctas - 2048) / int(r.slot_bytes); };
+    const auto slots = [&](int ctas) { return (dev.max_smem_per_sm / ctas - 1024 - kStaticShared) / int(r.slot_bytes); };
     for (ring_ctas = 512 / threads; ring_ctas > 1 && slots(ring_ctas) < 2;) --ring_ctas;
     r.slots = slots(ring_ctas) < kMostSlots ? slots(ring_ctas) : kMostSlots;
     shared = r.slots * int(r.slot_bytes);
@@ -1020,7 +1021,7 @@ cudaError_t launch_grad_type(const RmsNormGrad& p, GradArgs a, const DeviceInfo&
     r.g = a;
     r.status = dev.status;
     r.wait_ns = local_wait_limit_ns();
-    cudaError_t e = cudaFuncSetAttribute((const void*)ring->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+    cudaError_t e = allow_shared((const void*)ring->fn, dev, kStaticShared);
     if (e != cudaSuccess) return e;
     ring->fn<<<unsigned(a.parts_n), threads, size_t(shared), p.stream>>>(r);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -817,7 +817,7 @@ OnchipShape onchip_local_shape(const RowProblem& p, const DeviceInfo& dev) {
 
 cudaError_t launch_onchip(const RowProblem& p, const DeviceInfo& dev, const OnchipShape& s, unsigned long long* pub) {
   OnchipKernel fn = onchip_kernel(p.dtype, s.hold, p.log_out);
-  cudaError_t err = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(s.smem));
+  cudaError_t err = allow_shared((const void*)fn, dev);
   if (err != cudaSuccess) return err;
   if (s.cluster > 8 &&
       (err = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)

@@ -17,6 +17,12 @@ struct DeviceInfo {
   unsigned* status = nullptr;  // device address of this device's status word
 };
 
+// Sets a kernel's limit of dynamic shared memory: the most that its static_bytes leave, whatever a launch needs.  The limit is the kernel's,
+// not the launch's, so threads that each set it to their own launch's size would lower it under one another's.
+inline cudaError_t allow_shared(const void* kernel, const DeviceInfo& dev, int static_bytes = 0) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.max_smem_per_block_optin - static_bytes);
+}
+
 // One softmax problem.  Pointers are device pointers; y may be null for state-only work.
 struct RowProblem {
   const void* x = nullptr;
