@@ -138,31 +138,59 @@ __device__ __forceinline__ float block_max(float v, float* slots) {
 // ---- rows of any length and alignment: a CTA a row, read anew for each pass -----------------------------------------
 
 constexpr int kThreads = 256;
+// A thread's elements are loaded kBatch at a time, and kPlain of them added up before they go to its long sum (all of them plainly, 2^22
+// equal squares are off by 2e-4).
+// Eight CTAs an SM, as many as row_grid() counts on (at 40 registers a thread some of them make a second round: 4096 x 40960 fp32 forward
+// 961 us instead of 738).
+constexpr int kBatch = 4, kPlain = 64;
+
+// Elements i, i + kThreads, ... of a row of n, 0 behind its end.
+template <class D>
+__device__ __forceinline__ void load_batch(const unsigned char* row, int64_t i, int64_t n, float (&v)[kBatch]) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) v[k] = i + k * kThreads < n ? load1c<D>(row, i + k * kThreads) : 0.f;
+}
 
 template <class D, bool E4M3>
-__global__ void __launch_bounds__(kThreads) k_rms_norm_loop(NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) k_rms_norm_loop(NormArgs a) {
   __shared__ float slots[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
     const unsigned char* xr = a.x + row * a.x_pitch;
     const unsigned char* hr = xr;
-    float sum = 0.f;
+    LongSum squares;
     if (a.r) {
       const unsigned char* rr = a.r + row * a.r_pitch;
       unsigned char* to = a.h + row * a.h_pitch;
       hr = to;
-      for (int64_t i = threadIdx.x; i < a.N; i += kThreads) {
-        const float h = rounded<D>(load1c<D>(xr, i) + load1c<D>(rr, i));
-        D::store1(to, i, h);
-        sum = __fmaf_rn(h, h, sum);
+      for (int64_t i = threadIdx.x; i < a.N;) {
+        float part = 0.f;
+        for (int j = 0; j < kPlain / kBatch && i < a.N; ++j, i += kBatch * kThreads) {
+          float h[kBatch], r[kBatch];
+          load_batch<D>(xr, i, a.N, h);
+          load_batch<D>(rr, i, a.N, r);
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            h[k] = rounded<D>(h[k] + r[k]);
+            if (i + k * kThreads < a.N) D::store1(to, i + k * kThreads, h[k]);
+            part = __fmaf_rn(h[k], h[k], part);
+          }
+        }
+        squares.add(part);
       }
     } else {
-      for (int64_t i = threadIdx.x; i < a.N; i += kThreads) {
-        const float h = load1c<D>(xr, i);
-        sum = __fmaf_rn(h, h, sum);
+      for (int64_t i = threadIdx.x; i < a.N;) {
+        float part = 0.f;
+        for (int j = 0; j < kPlain / kBatch && i < a.N; ++j, i += kBatch * kThreads) {
+          float h[kBatch];
+          load_batch<D>(xr, i, a.N, h);
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) part = __fmaf_rn(h[k], h[k], part);
+        }
+        squares.add(part);
       }
     }
-    sum = block_sum<kThreads / 32>(sum, slots);  // its barriers also order h's stores before the loads below
+    const float sum = block_sum<kThreads / 32>(squares.s, slots);  // its barriers also order h's stores before the loads below
     const float rstd = 1.f / sqrtf(sum / float(a.N) + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     unsigned char* yr = a.y + row * a.y_pitch;
@@ -205,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_loop(NormArgs a) {
 
 // dx alone, two reads of the row.
 template <class D>
-__global__ void __launch_bounds__(kThreads) k_rms_grad_loop(GradArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) k_rms_grad_loop(GradArgs a) {
   __shared__ float slots[32];
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
     const unsigned char* dr = a.dy + row * a.dy_pitch;
@@ -213,9 +241,20 @@ __global__ void __launch_bounds__(kThreads) k_rms_grad_loop(GradArgs a) {
     const unsigned char* sr = a.sg + row * a.sg_pitch;
     unsigned char* to = a.dx + row * a.dx_pitch;
     const float rstd = a.rstd[row];
-    float sum = 0.f;
-    for (int64_t i = threadIdx.x; i < a.N; i += kThreads) sum = __fmaf_rn(load1c<D>(dr, i) * weight1<D>(a, i), load1c<D>(hr, i) * rstd, sum);
-    const float mean = block_sum<kThreads / 32>(sum, slots) / float(a.N);
+    LongSum sum;
+    for (int64_t i = threadIdx.x; i < a.N;) {
+      float part = 0.f;
+      for (int j = 0; j < kPlain / kBatch && i < a.N; ++j, i += kBatch * kThreads) {
+        float d[kBatch], h[kBatch];
+        load_batch<D>(dr, i, a.N, d);
+        load_batch<D>(hr, i, a.N, h);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i + k * kThreads < a.N) part = __fmaf_rn(d[k] * weight1<D>(a, i + k * kThreads), h[k] * rstd, part);
+      }
+      sum.add(part);
+    }
+    const float mean = block_sum<kThreads / 32>(sum.s, slots) / float(a.N);
     for (int64_t i = threadIdx.x; i < a.N; i += kThreads) {
       float v = rstd * __fmaf_rn(-(load1c<D>(hr, i) * rstd), mean, load1c<D>(dr, i) * weight1<D>(a, i));
       if (a.sg) v += load1c<D>(sr, i);

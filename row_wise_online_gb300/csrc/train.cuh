@@ -17,6 +17,16 @@ __device__ __forceinline__ float load1c(const void* p, int64_t i) {
   }
 }
 
+// A long sum of a thread: lost is what the additions to s rounded away, which the next one takes up.  An infinite sum stays one.
+struct LongSum {
+  float s = 0.f, lost = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    const float want = __fsub_rn(v, lost), t = __fadd_rn(s, want);
+    lost = fabsf(t) < INFINITY ? __fsub_rn(__fsub_rn(t, s), want) : 0.f;
+    s = t;
+  }
+};
+
 // A value as the element type holds it.
 template <class D>
 __device__ __forceinline__ float rounded(float v) {
