@@ -87,9 +87,14 @@ __global__ void __launch_bounds__(reg_threads(W), 1024 / reg_threads(W)) k_loss_
 
 constexpr int kThreads = 512;
 
+// A thread's sums are relative to a reference that rises to the maximum only when that is kRise above it, not to the maximum itself: each time
+// they are rescaled they take on the exponential's error, and entries that rise along a row of millions did so 8192 times (1.5e-5 of
+// the sum).  e^kRise times 2^31 terms is far from fp32's range.
+constexpr float kRise = 8.f;
+
 // A CTA a row: the fold, then the gradient from a second read.  VEC: 16-byte units, else single elements.
 template <class D, bool VEC, bool SMOOTH>
-__global__ void __launch_bounds__(kThreads) k_loss_grad_twopass(LossArgs a) {
+__global__ void __launch_bounds__(kThreads, VEC ? 3 : 4) k_loss_grad_twopass(LossArgs a) {
   constexpr int E = VEC ? D::kVec : 1;
   __shared__ Fold parts[2][kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -101,7 +106,8 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad_twopass(LossArgs a) {
     const int64_t label = a.labels[row];
     // read before any element is overwritten: the gradient may go where the logits are
     const float x_label = label >= 0 && label < a.N ? load1c<D>(xr, label) : 0.f;
-    Fold f = empty_fold();
+    Fold f = empty_fold();  // f.m: the reference
+    float top = -INFINITY;
     float lost = 0.f;  // what the additions to f.d rounded away (long runs of a thread)
     for (int64_t u = threadIdx.x; u < units; u += kThreads) {
       float v[E];
@@ -110,7 +116,8 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad_twopass(LossArgs a) {
       float mx = v[0];
 #pragma unroll
       for (int e = 1; e < E; ++e) mx = fmaxf(mx, v[e]);
-      if (mx > f.m) {
+      top = fmaxf(top, mx);
+      if (mx > f.m + kRise) {
         const float k = exp_diff(f.m, mx);
         f.d *= k;
         lost *= k;
@@ -132,6 +139,9 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad_twopass(LossArgs a) {
         f.n += float(E);
       }
     }
+    f.d *= exp_diff(f.m, safe_max(top));
+    if constexpr (SMOOTH) f.s = moved(f, top);
+    f.m = top;
     f = fold_lanes<SMOOTH>(f, 32);
     if (lane == 0) parts[it][warp] = f;
     __syncthreads();
