@@ -2,6 +2,8 @@
 
 Tolerances as for shorter rows: 1e-5 of the softmax and of the loss.
 """
+import math
+
 import pytest
 import torch
 
@@ -34,3 +36,30 @@ def test_rising_entries(N, dt, eps):
         x[1, 5:] = -torch.inf
         x[2] = x[2].flip(0)
         check(x.to(dt).cuda(), labels)
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("N", LENGTHS)
+def test_smoothed_loss(N, dt):
+    """Entries at one distance from the maximum, which every thread meets at the start, at the end, or is the only one not to."""
+    x = torch.full((4, N), -11.7)
+    x[0, :8192] = 0.0
+    x[1, -8192:] = 0.0
+    x[2] = -5.3
+    x[2, N // 2] = 9.0
+    x[3, :8192] = 1.4
+    labels = torch.tensor([0, 5, N // 2, N - 1], device="cuda")
+    check(x.to(dt).cuda(), labels, eps=0.9)
+    check(x.to(dt).cuda(), labels, eps=0.1, z=1e-3)
+
+
+def test_masked_entries():
+    """A masked entry gives an infinite smoothed loss, in the first and in a later part of a thread's run; gradients stay finite."""
+    N = 1 << 20
+    x = torch.randn(3, N, generator=torch.Generator().manual_seed(2))
+    x[0, 0] = x[1, N - 9] = -math.inf
+    x[2, : N // 2] = -math.inf
+    labels = torch.tensor([5, 5, N - 5], device="cuda")
+    loss, g = rwo.cross_entropy_rows_grad(x.cuda(), labels, label_smoothing=0.1)
+    assert (loss == math.inf).all() and torch.isfinite(g).all()
+    check(x.cuda(), labels)
