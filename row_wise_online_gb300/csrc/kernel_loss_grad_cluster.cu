@@ -12,7 +12,6 @@
 // whole 16-byte lines of x, the few elements around them are copied one by one, and where x lies otherwise than the gradient
 // (SHIFT) a vector is put together from two of shared memory.
 #include <mutex>
-#include <vector>
 
 #include "loss_grad.cuh"
 
@@ -270,14 +269,18 @@ cudaError_t resident_clusters(Kernel fn, const cudaLaunchConfig_t& cfg, int clus
     size_t shared;
     int clusters;
   };
+  constexpr int kMost = 256;
   static std::mutex mutex;
-  static std::vector<Known> known;
+  static Known known[kMost];  // nothing is allocated, and so nothing thrown, behind the C calls
+  static int held = 0;
   std::lock_guard<std::mutex> lock(mutex);
-  for (const Known& k : known)
+  for (int i = 0; i < held; ++i) {
+    const Known& k = known[i];
     if (k.device == dev.device && k.fn == fn && k.cluster == cluster && k.shared == cfg.dynamicSmemBytes) {
       *out = k.clusters;
       return cudaSuccess;
     }
+  }
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, (const void*)fn);
   if (e == cudaSuccess)
@@ -285,8 +288,8 @@ cudaError_t resident_clusters(Kernel fn, const cudaLaunchConfig_t& cfg, int clus
   if (e == cudaSuccess) e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(out, (const void*)fn, &cfg);
   if (e == cudaSuccess) {
-    if (known.size() >= 256) known.clear();
-    known.push_back(Known{dev.device, fn, cluster, cfg.dynamicSmemBytes, *out});
+    if (held == kMost) held = 0;
+    known[held++] = Known{dev.device, fn, cluster, cfg.dynamicSmemBytes, *out};
   }
   return e;
 }
