@@ -91,11 +91,14 @@ constexpr int kThreads = 512;
 // they are rescaled they take on the exponential's error, and entries that rise along a row of millions did so 8192 times (1.5e-5 of
 // the sum).  e^kRise times 2^31 terms is far from fp32's range.
 constexpr float kRise = 8.f;
+constexpr int kBatch = 4;
 
-// A CTA a row: the fold, then the gradient from a second read.  VEC: 16-byte units, else single elements.
+// A CTA a row: the fold, then the gradient from a second read.  VEC: 16-byte units, else single elements, kBatch of them under way.
+// Four CTAs an SM, as many as the grid counts on (2000 rows of 600001 bf16 1839 us; single elements one by one, 2972), but for vectors without
+// smoothing, which gain nothing by it (8 x 4194304 bf16 854 us, held to 32 registers 999).
 template <class D, bool VEC, bool SMOOTH>
-__global__ void __launch_bounds__(kThreads, VEC ? 3 : 4) k_loss_grad_twopass(LossArgs a) {
-  constexpr int E = VEC ? D::kVec : 1;
+__global__ void __launch_bounds__(kThreads, VEC && !SMOOTH ? 0 : 4) k_loss_grad_twopass(LossArgs a) {
+  constexpr int E = VEC ? D::kVec : 1, B = VEC ? E : kBatch;
   __shared__ Fold parts[2][kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t units = a.N / E;
@@ -110,22 +113,21 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 4) k_loss_grad_twopass(Los
     float top = -INFINITY;
     float lost = 0.f;  // what the additions to f.d rounded away (long runs of a thread)
     LongSum far;       // f.s, alike (added up plainly, 2^22 equal distances are off by 8e-5)
-    const auto load = [&](int64_t u) {
-      if constexpr (VEC) return ld16(xr + u * 16);
-      else return D::load1(xr, u);
-    };
-    decltype(load(0)) unit;
-    if (SMOOTH) unit = load(threadIdx.x < units ? threadIdx.x : 0);
-    for (int64_t u = threadIdx.x; u < units; u += kThreads) {
-      float v[E];
-      if (!SMOOTH) unit = load(u);
-      if constexpr (VEC) D::unpack(unit, v);
-      else v[0] = unit;
-      // with smoothing the next is under way meanwhile (8 x 4194304 bf16 940 us, loaded where it is used 1027; without, 945 and 861)
-      if (SMOOTH && u + kThreads < units) unit = load(u + kThreads);
+    uint4 q;  // VEC: with smoothing the next vector is under way meanwhile
+    if (VEC && SMOOTH) q = ld16(xr + (threadIdx.x < units ? threadIdx.x : 0) * 16);
+    for (int64_t u = threadIdx.x; u < units; u += kThreads * (VEC ? 1 : B)) {
+      float v[B];
+      if constexpr (VEC) {
+        if (!SMOOTH) q = ld16(xr + u * 16);
+        D::unpack(q, v);
+        if (SMOOTH && u + kThreads < units) q = ld16(xr + (u + kThreads) * 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < B; ++e) v[e] = u + e * kThreads < units ? D::load1(xr, u + e * kThreads) : -INFINITY;
+      }
       float mx = v[0];
 #pragma unroll
-      for (int e = 1; e < E; ++e) mx = fmaxf(mx, v[e]);
+      for (int e = 1; e < B; ++e) mx = fmaxf(mx, v[e]);
       top = fmaxf(top, mx);
       if (mx > f.m + kRise) {
         const float k = exp_diff(f.m, mx);
@@ -143,17 +145,19 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 4) k_loss_grad_twopass(Los
       const float ms = safe_max(f.m);
       float t = 0.f, r = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
+      for (int e = 0; e < B; ++e) {
         t += exp_diff(v[e], ms);
-        if constexpr (SMOOTH) r += ms - v[e];
+        if constexpr (SMOOTH) {
+          if (VEC || u + e * kThreads < units) {
+            r += ms - v[e];
+            f.n += 1.f;
+          }
+        }
       }
       const float want = t - lost, sum = __fadd_rn(f.d, want);
       lost = __fsub_rn(__fsub_rn(sum, f.d), want);
       f.d = sum;
-      if constexpr (SMOOTH) {
-        far.add(r);
-        f.n += float(E);
-      }
+      if constexpr (SMOOTH) far.add(r);
     }
     f.s = far.s;
     f.d *= exp_diff(f.m, safe_max(top));
