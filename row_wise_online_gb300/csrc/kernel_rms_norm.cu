@@ -388,8 +388,8 @@ __device__ __forceinline__ void store_codes(unsigned char* row, int u, int left,
 
 __host__ __device__ constexpr int reg_threads(int warps) { return warps * 32 > 256 ? warps * 32 : 256; }
 
-// CTAs of 256 threads an SM: in 8 bits three for 16-bit rows (16384 x 4096 bf16 with a residual 74 us; two 101, four 97), else
-// four (16384 x 8192 bf16 84 us, three 93, six 91).
+// CTAs of 256 threads an SM: in 8 bits three for 16-bit rows (16384 x 4096 bf16 with a residual 75 us; when it took 74, two 101, four 97), else
+// four (16384 x 8192 bf16 86 us; when it took 84, three 93, six 91).
 template <class D, int K, int W, bool SHIFT, bool E4M3>
 __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes == 2 ? 3 : 4) * 256 / reg_threads(W)) k_rms_norm(NormArgs a) {
   constexpr int E = D::kVec, GT = W * 32, G = reg_threads(W) / GT;
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(reg_threads(W), (K > 4 ? 2 : E4M3 && D::kBytes
 // Forward into the element type for rows of x on no boundary (and a residual that starts at the same place of its 16-byte lines).  As
 // that place comes again after 16 bytes' worth of rows, and a CTA's turns are a multiple of those apart, it is one for all rows of a group: lines
 // are worked on where they are, and the weights lie moved in shared memory, each thread's for itself.  Taken by what is read alone:
-// a call in place gives the bits of one that is not.  16384 x 5003 bf16 with a residual 132 us (lines shifted in registers, for single rows, 243), 65536 x 333 fp32 71.
+// a call in place gives the bits of one that is not.  16384 x 5003 bf16 with a residual 130 us (lines shifted in registers, for single rows, 243), 65536 x 333 fp32 71.
 template <class D, int K>
 constexpr int lines_shared(int threads) { return threads * K * D::kVec * 4; }
 constexpr int lines_ctas(int K, int threads) { return (K > 4 ? 2 : 4) * 256 / threads; }
@@ -695,12 +695,12 @@ __global__ void __launch_bounds__(reg_threads(W)) k_rms_grad(GradArgs a) {
 
 // The same with the rows on their way in shared memory: a slot has the G rows of dy, h and sum_grad that the CTA's groups take
 // next, copied by cp.async.bulk, and is read twice.  The copies of up to kMostSlots turns are under way while one is worked on,
-// whatever the registers leave of the SM's warps: 16384 x 4096 bf16 takes 88 us, with the rows in registers 103 (at the best
+// whatever the registers leave of the SM's warps: 16384 x 4096 bf16 takes 85 us; when it took 88, with the rows in registers 103 (at the best
 // number of CTAs an SM).  Arithmetic in pairs of fp32: with single operations, 104 us.
 // LINES: rows on no boundary, which start at the same place of their 16-byte lines in all matrices.  That place comes again
 // after 16 bytes' worth of rows, and a CTA's turns are a multiple of those apart: it is one for all rows of a group, so lines are
-// worked on where they are, with the weights and the sums of dw moved instead (16384 x 5003 bf16 153 us; vectors shifted out of the
-// slots' lines 237, out of lines in registers 387).
+// worked on where they are, with the weights and the sums of dw moved instead (16384 x 5003 bf16 151 us; vectors shifted out of the
+// slots' lines 237, out of lines in registers 384).
 constexpr int kMostSlots = 4;
 constexpr int kStaticShared = 1024;  // more than these kernels have
 
