@@ -444,6 +444,8 @@ int cross_entropy_rows_grad(const void* x, int64_t ldx, const int64_t* labels, c
  *   scales      -- e4m3 only: [M][groups], groups = 1 for group = 0 (a scale for each row), else ceil(N / group).
  *   group       -- 0 or 128 (the last group of a row may be shorter).
  *   rstd_out    -- fp32 [M] or NULL; the backward pass reads it.
+ * Squares are added up in fp32: rows of magnitudes up to 1e17, and with eps = 0 down to 1e-18, here and in the backward
+ * pass; beyond them rstd is 0 or inf.
  */
 typedef struct rms_norm_args {
   const void* x;

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, VEC && !SMOOTH ? 0 : 4) k_loss_grad_
     }
     f.s = far.s;
     f.d *= exp_diff(f.m, safe_max(top));
-    if constexpr (SMOOTH) f.s = moved(f, top);
+    if constexpr (SMOOTH) f.s = moved(f, safe_max(top));
     f.m = top;
     f = fold_lanes<SMOOTH>(f, 32);
     if (lane == 0) parts[it][warp] = f;

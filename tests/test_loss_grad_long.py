@@ -63,3 +63,21 @@ def test_masked_entries():
     loss, g = rwo.cross_entropy_rows_grad(x.cuda(), labels, label_smoothing=0.1)
     assert (loss == math.inf).all() and torch.isfinite(g).all()
     check(x.cuda(), labels)
+
+
+@pytest.mark.parametrize("dt", [F32, BF, FP])
+@pytest.mark.parametrize("N", [(1 << 20) + 8, 1_100_001])
+@pytest.mark.parametrize("eps", [0.0, 0.1])
+def test_rows_with_little_left(N, dt, eps):
+    """All but one, all but a few, and all entries masked: most threads meet nothing else."""
+    x = torch.full((5, N), -math.inf)
+    x[0, 77] = 2.5
+    x[1, 1000:1100] = torch.randn(100, generator=torch.Generator().manual_seed(3))
+    x[2, -1] = -4.0
+    x[3] = 1.0
+    x[3, : N - 5] = -math.inf
+    labels = torch.tensor([77, 1050, 3, N - 1, 9], device="cuda")
+    if eps:
+        loss, g = rwo.cross_entropy_rows_grad(x.to(dt).cuda(), labels, label_smoothing=eps)
+        assert (loss[:4] == math.inf).all() and torch.isnan(loss[4]) and torch.isfinite(g[:4]).all()
+    check(x.to(dt).cuda(), labels, eps=eps)
